@@ -26,12 +26,14 @@ __all__ = [
     "attn_device_status", "attn_last_error", "attention", "attn_bwd_noalloc",
     "attn_selftest_wait_timeout", "attn_fwd_split", "attn_fwd_split_count",
     "attn_fwd_split_workspace_bytes", "attn_merge", "attn_selftest_exp2",
-    "attn_debug_set_ring_stages",
+    "attn_debug_set_ring_stages", "ATTN_WARN_CLAMPED", "attn_kv8_append", "attn_fwd_kv8",
+    "attn_fwd_kv8_workspace_bytes", "attn_kv8_weights", "attn_kv8_evict",
 ]
 
 
 ATTN_OK = 0
 ATTN_WARN_EMPTY_ROW = 1
+ATTN_WARN_CLAMPED = 2
 ATTN_ERR_INVALID_ARG = -1
 ATTN_ERR_UNSUPPORTED = -2
 ATTN_ERR_ALIGNMENT = -3
@@ -117,6 +119,16 @@ def load():
     lib.attn_debug_set_ring_stages.argtypes = [i32]
     lib.attn_debug_set_ring_stages.restype = i32
     lib.attn_selftest_exp2.restype = i32
+    lib.attn_kv8_append.argtypes = [i32] * 7 + [vp] * 10
+    lib.attn_kv8_append.restype = i32
+    lib.attn_fwd_kv8_workspace_bytes.argtypes = [i32] * 7
+    lib.attn_fwd_kv8_workspace_bytes.restype = sz
+    lib.attn_fwd_kv8.argtypes = [i32] * 8 + [f32] + [vp] * 7 + [i32, vp, vp, vp, sz, vp]
+    lib.attn_fwd_kv8.restype = i32
+    lib.attn_kv8_weights.argtypes = [i32] * 8 + [f32] + [vp] * 5 + [i32] + [vp] * 4
+    lib.attn_kv8_weights.restype = i32
+    lib.attn_kv8_evict.argtypes = [i32] * 5 + [vp] * 6 + [i32] * 4 + [vp] * 8
+    lib.attn_kv8_evict.restype = i32
     _lib = lib
     return lib
 
@@ -362,6 +374,184 @@ def attn_fwd_fp8_blocks(q8, k8, vt8, q_scales, k_scales, v_scales, c, mask="none
                                       _ptr(bits), row_words, hs, _ptr(o), _ptr(lse),
                                       _stream_ptr(stream)))
     return o, lse
+
+
+def _kv8_cache(codes, scales, lengths, device=None):
+    """(B, H_kv, cap, d, block) of an 8-bit cache: code tensors [B,H_kv,cap,d], scale tensors
+    [B,H_kv,cap/block] and lengths [B], all contiguous on one CUDA device."""
+    first = codes[0]
+    if first.dim() != 4:
+        raise ValueError("codes must be [B,H_kv,cap,d]")
+    B, Hk, cap, d = first.shape
+    device = first.device if device is None else device
+    for t in codes:
+        _fp8_bytes(t, "codes")
+        if t.shape != first.shape:
+            raise ValueError("k8 and v8 must have the same shape")
+    nblk = scales[0].shape[-1] if scales[0].dim() == 3 else 0
+    if nblk < 1 or cap % nblk:
+        raise ValueError("scales must be [B,H_kv,cap/block]")
+    for t in scales:
+        _kv8_array(t, torch.float32, (B, Hk, nblk), "scales")
+    _kv8_array(lengths, torch.int32, (B,), "lengths")
+    for t in (*codes, *scales, lengths):
+        if t.device != device:
+            raise ValueError("the call's tensors must lie on one device")
+    return B, Hk, cap, d, cap // nblk
+
+
+def _kv8_array(t, dtype, shape, name, device=None):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError("the call's tensors must lie on one device")
+    return t
+
+
+def _kv8_input(t, shape, name, device):
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be float16 or bfloat16")
+    return _kv8_array(t, t.dtype, shape, name, device)
+
+
+class _On:
+    """The device of the call's tensors made current, and the stream it is to run on; what is
+    allocated inside belongs to that stream."""
+
+    def __init__(self, device, stream):
+        self._device = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self._stream = stream
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._stream = torch.cuda.stream(self._stream)
+            self._stream.__enter__()
+        return _stream_ptr(None)
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+
+
+def attn_kv8_append(k_new, v_new, k8, v8, k_scales, v_scales, lengths, counts=None, weights=None,
+                    stream=None):
+    """Writes k_new, v_new [B,H_kv,n,d] (float16 or bfloat16) into the 8-bit cache k8, v8 (E4M3
+    [B,H_kv,cap,d]) with k_scales, v_scales (float32 [B,H_kv,cap/block]), in place, at the last
+    counts[b] (None: n) of the lengths[b] positions of each sequence; ``lengths`` and ``counts``
+    are int32 CUDA tensors [B], the lengths already counting the new tokens.  ``weights`` (float32
+    [B,H_kv,cap], optional) is set to 0 there."""
+    B, Hk, cap, d, block = _kv8_cache((k8, v8), (k_scales, v_scales), lengths)
+    dev = k8.device
+    if k_new.dim() != 4:
+        raise ValueError("k_new and v_new must be [B,H_kv,n,d]")
+    n = k_new.shape[2]
+    for t, nm in ((k_new, "k_new"), (v_new, "v_new")):
+        _kv8_input(t, (B, Hk, n, d), nm, dev)
+    if v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must share one dtype")
+    if counts is not None:
+        _kv8_array(counts, torch.int32, (B,), "counts", dev)
+    if weights is not None:
+        _kv8_array(weights, torch.float32, (B, Hk, cap), "weights", dev)
+    with _On(dev, stream) as s:
+        _check(load().attn_kv8_append(DTYPE_CODE[k_new.dtype], B, Hk, n, d, cap, block, _ptr(k_new),
+                                      _ptr(v_new), _ptr(lengths), _ptr(counts), _ptr(k8), _ptr(v8),
+                                      _ptr(k_scales), _ptr(v_scales), _ptr(weights), s))
+
+
+def attn_fwd_kv8_workspace_bytes(dtype, B, H, H_kv, n_q, d, cap) -> int:
+    """Bytes of workspace attn_fwd_kv8 needs on the current device."""
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load().attn_fwd_kv8_workspace_bytes(code, B, H, H_kv, n_q, d, cap))
+
+
+def _kv8_query(q, B, Hk, d, counts, mask, device):
+    if q.dim() != 4 or q.shape[1] < 1 or q.shape[1] % Hk:
+        raise ValueError("q must be [B,H,n_q,d] with H a multiple of H_kv")
+    H, n = q.shape[1], q.shape[2]
+    _kv8_input(q, (B, H, n, d), "q", device)
+    if counts is not None:
+        _kv8_array(counts, torch.int32, (B,), "counts", device)
+    return H, n, MASK_CODE[mask]
+
+
+def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="none", o=None,
+                 lse=None, workspace=None, stream=None):
+    """Attention of q [B,H,n_q,d] (float16 or bfloat16) over the 8-bit cache of
+    ``attn_kv8_append``, H a multiple of H_kv; the queries are each sequence's last counts[b]
+    (None: n_q) positions, rows past that are padding.  mask "none" or "causal".  Returns
+    (o [B,H,n_q,d], lse [B,H,n_q] float32)."""
+    B, Hk, cap, d, block = _kv8_cache((k8, v8), (k_scales, v_scales), lengths)
+    H, n, kind = _kv8_query(q, B, Hk, d, counts, mask, k8.device)
+    with _On(q.device, stream) as s:
+        o = torch.empty_like(q) if o is None else _kv8_array(o, q.dtype, q.shape, "o", q.device)
+        if lse is None:
+            lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
+        else:
+            _kv8_array(lse, torch.float32, (B, H, n), "lse", q.device)
+        lib = load()
+        code = DTYPE_CODE[q.dtype]
+        if workspace is None:
+            need = lib.attn_fwd_kv8_workspace_bytes(code, B, H, Hk, n, d, cap)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the call's device")
+        _check(lib.attn_fwd_kv8(code, B, H, Hk, n, d, cap, block, float(c), _ptr(q), _ptr(k8),
+                                _ptr(v8), _ptr(k_scales), _ptr(v_scales), _ptr(lengths),
+                                _ptr(counts), kind, _ptr(o), _ptr(lse), _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), s))
+    return o, lse
+
+
+def attn_kv8_weights(q, k8, k_scales, lengths, lse, weights, c, counts=None, mask="none", out=None,
+                     stream=None):
+    """Adds to the running attention weight of each cached key (``weights`` float32
+    [B,H_kv,cap]; None: zeros) what the queries give it, from the lse of ``attn_fwd_kv8`` on the
+    same arguments.  Writes ``out`` (None: ``weights`` in place) and returns it."""
+    B, Hk, cap, d, block = _kv8_cache((k8,), (k_scales,), lengths)
+    H, n, kind = _kv8_query(q, B, Hk, d, counts, mask, k8.device)
+    _kv8_array(lse, torch.float32, (B, H, n), "lse", q.device)
+    for t in (weights, out):
+        if t is not None:
+            _kv8_array(t, torch.float32, (B, Hk, cap), "weights", q.device)
+    with _On(q.device, stream) as s:
+        if out is None:
+            out = torch.zeros((B, Hk, cap), device=q.device) if weights is None else weights
+        _check(load().attn_kv8_weights(DTYPE_CODE[q.dtype], B, H, Hk, n, d, cap, block, float(c),
+                                       _ptr(q), _ptr(k8), _ptr(k_scales), _ptr(lengths),
+                                       _ptr(counts), kind, _ptr(lse), _ptr(weights), _ptr(out), s))
+    return out
+
+
+def attn_kv8_evict(k8, v8, k_scales, v_scales, weights, lengths, keep, k8_out, v8_out, k_scales_out,
+                   v_scales_out, weights_out, lengths_out, sink=0, recent=0, kept=None, stream=None):
+    """Writes into another 8-bit cache (the ``*_out`` tensors, capacity at least ``keep``) the
+    tokens of each sequence and head worth keeping: the first ``sink``, the last ``recent`` and
+    the heaviest of the rest by ``weights``, in order, ``keep`` at most.  Returns the kept
+    positions, int32 [B,H_kv,keep], -1 past the new length."""
+    B, Hk, cap, d, block = _kv8_cache((k8, v8), (k_scales, v_scales), lengths)
+    dev, keep = k8.device, int(keep)
+    B2, Hk2, cap_out, d2, block2 = _kv8_cache((k8_out, v8_out), (k_scales_out, v_scales_out),
+                                              lengths_out, dev)
+    if (B2, Hk2, d2, block2) != (B, Hk, d, block):
+        raise ValueError("the two caches must agree on B, H_kv, d and block")
+    _kv8_array(weights, torch.float32, (B, Hk, cap), "weights", dev)
+    _kv8_array(weights_out, torch.float32, (B, Hk, cap_out), "weights_out", dev)
+    with _On(dev, stream) as s:
+        if kept is None:
+            kept = torch.empty((B, Hk, max(keep, 0)), dtype=torch.int32, device=dev)
+        else:
+            _kv8_array(kept, torch.int32, (B, Hk, keep), "kept", dev)
+        _check(load().attn_kv8_evict(B, Hk, d, cap, block, _ptr(k8), _ptr(v8), _ptr(k_scales),
+                                     _ptr(v_scales), _ptr(weights), _ptr(lengths), keep, int(sink),
+                                     int(recent), cap_out, _ptr(k8_out), _ptr(v8_out),
+                                     _ptr(k_scales_out), _ptr(v_scales_out), _ptr(weights_out),
+                                     _ptr(lengths_out), _ptr(kept), s))
+    return kept
 
 
 def attn_merge(o_parts, lse_parts, dtype=torch.float32, o=None, lse=None, stream=None):

@@ -216,6 +216,8 @@ __global__ void selftest_exp2_kernel(const float* x, float* y_fma, float* y_mufu
 }  // namespace
 
 void ea::set_last_error(const std::string& msg) { g_last_error = msg; }
+int ea::device_status_word(uint32_t** out) { return status_ptr(out); }
+int ea::device_sm_count() { return sm_count(); }
 
 extern "C" {
 
@@ -593,6 +595,7 @@ int attn_device_status(void* stream) {
     snprintf(buf, sizeof(buf), "an in-kernel wait gave up (sites 0x%02x)", (word >> 8) & 0xFFu);
     return fail(ATTN_ERR_DEVICE_TIMEOUT, buf);
   }
+  if (word & 4u) return ATTN_WARN_CLAMPED;
   if (word & 2u) return ATTN_WARN_EMPTY_ROW;
   return ATTN_OK;
 }

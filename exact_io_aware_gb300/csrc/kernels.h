@@ -174,6 +174,12 @@ constexpr int bwd_pad_rows(int n) { return (n + 127) / 128 * 128; }
 size_t bwd_tc_workspace_bytes(int B, int H, int n, int d);
 size_t bwd_f32_workspace_bytes(int B, int H, int n, int d);
 
+// The current device's status word (device pointer), with the context bound to the calling
+// thread; 0 or a negative ATTN_ERR_* code with the message set.
+int device_status_word(uint32_t** out);
+// Streaming multiprocessors of the current device (0 if it cannot be told).
+int device_sm_count();
+
 // Sets the message attn_last_error() returns on the calling thread.
 void set_last_error(const std::string& msg);
 

@@ -68,6 +68,7 @@ typedef enum { ATTN_MASK_NONE = 0, ATTN_MASK_CAUSAL = 1, ATTN_MASK_BITMAP = 2 } 
 enum {
   ATTN_OK = 0,
   ATTN_WARN_EMPTY_ROW = 1,       /* status only: some row had an empty allowed set */
+  ATTN_WARN_CLAMPED = 2,         /* status only: a cache length or token count was out of range */
   ATTN_ERR_INVALID_ARG = -1,     /* null pointer, non-positive size, bad enum */
   ATTN_ERR_UNSUPPORTED = -2,     /* head dim / key block / dtype combination not built */
   ATTN_ERR_ALIGNMENT = -3,       /* a device pointer is not 16-byte aligned */
@@ -231,6 +232,100 @@ int attn_fwd_fp8_blocks(int B, int H, int n, int d, float c,
                         int mask_kind, const uint32_t* mask_bits, int64_t mask_row_words,
                         int64_t mask_head_stride_words, void* o, float* lse, void* stream);
 
+/*
+ * Key/value cache in 8 bits (no counterpart on the pages, whose key/value cache is of the
+ * input type).  Of each sequence and key/value head it holds up to `cap` tokens:
+ *   k8, v8               E4M3 [B][H_kv][cap][d]
+ *   k_scales, v_scales   float32 [B][H_kv][cap / block]: token j of K is
+ *                        k_scales[j / block] k8_j, of V v_scales[j / block] v8_j
+ *   lengths              int32 [B] (device): tokens each sequence holds, the tokens of the call
+ *                        at hand among them
+ *   counts               int32 [B] (device) or NULL: how many of a call's n tokens (or query
+ *                        rows) sequence b has; NULL is n for all.  Token i < counts[b] has the
+ *                        position lengths[b] - counts[b] + i; rows i >= counts[b] are padding.
+ *   weights              float32 [B][H_kv][cap]: accumulated attention weight of each token
+ * d: 64 or 128; block: 16, 32, 64 or 128; cap: a multiple of block; B * H_kv at most 65535.
+ * Scales must be positive and finite (those of blocks with no held token are not read); the
+ * entry points below write powers of two, which E4M3, a floating-point format, loses no
+ * precision to, so codes move between blocks exactly down to E4M3's subnormals.  What lies past
+ * a sequence's length is neither used nor changed.  A length outside [0, cap] or a count
+ * outside [0, n] is clamped and raises ATTN_WARN_CLAMPED.  Code arrays and 16-bit arrays are
+ * 16-byte aligned, the others 4-byte.  All calls are asynchronous on `stream`, can be
+ * captured, and allocate nothing.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
+ * ATTN_ERR_ALIGNMENT, ATTN_ERR_WORKSPACE, ATTN_ERR_CUDA, as for attn_fwd_kv.
+ */
+
+/*
+ * Writes new tokens k_new, v_new ([B][H_kv][n_new][d], ATTN_F16 or ATTN_BF16) into the cache at
+ * positions lengths[b] - counts[b] .. lengths[b] - 1 (lengths already count them; a token whose
+ * position would be negative is dropped, with ATTN_WARN_CLAMPED).  A block's scale is the least
+ * power of two s in [2^-100, 2^120] with |x| <= 448 s for each finite value x it holds, and a
+ * code E4M3(x / s), rounded to nearest even; a value that is not finite is stored as NaN (E4M3
+ * has no infinity) and leaves the scale alone.  A block that already holds tokens (positions
+ * below the new ones) keeps the larger of its scale and the one the new tokens need; if it
+ * grows, the held codes become E4M3(code * old / new).  With weights != NULL the new positions'
+ * weights are set to 0.
+ */
+int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int block,
+                    const void* k_new, const void* v_new, const int32_t* lengths,
+                    const int32_t* counts, void* k8, void* v8, float* k_scales, float* v_scales,
+                    float* weights, void* stream);
+
+/*
+ * Attention of n_q query rows of each of H = G H_kv heads over the cache (query head h reads
+ * key/value head h / G).  q and o are [B][H][n_q][d] of dtype (ATTN_F16 or ATTN_BF16), lse
+ * [B][H][n_q] float32.  The queries are the sequence's last counts[b] positions: under
+ * ATTN_MASK_CAUSAL row i sees keys j <= lengths[b] - counts[b] + i, under ATTN_MASK_NONE every
+ * key below lengths[b] (ATTN_MASK_BITMAP is refused).  A padding row (i >= counts[b]) gets
+ * O = 0, LSE = -inf; so does a row that sees no key, which also raises ATTN_WARN_EMPTY_ROW.
+ * The codes are read exactly and the queries keep their bits; probabilities are rounded to 11
+ * bits (half a step 2^-12) before the product with V, sums are float32.
+ *   workspace  device buffer of at least attn_fwd_kv8_workspace_bytes(...) bytes, 16-byte
+ *              aligned; its contents on entry do not matter.  Calls that may overlap on the GPU
+ *              need workspaces of their own.
+ * The result does not depend on how the device's lengths divide the work, up to rounding, and
+ * repeats bit for bit on the same arguments.  Forward only.
+ */
+int attn_fwd_kv8(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int block, float c,
+                 const void* q, const void* k8, const void* v8, const float* k_scales,
+                 const float* v_scales, const int32_t* lengths, const int32_t* counts,
+                 int mask_kind, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/* Bytes of workspace attn_fwd_kv8 needs on the current device (0 for sizes it refuses). */
+size_t attn_fwd_kv8_workspace_bytes(int dtype, int B, int H, int H_kv, int n_q, int d, int cap);
+
+/*
+ * Adds to each held key's weight what the queries give it:
+ *     weights_out[b][hk][j] = weights[b][hk][j] + sum_{h of hk, i < counts[b]} e^{s_hij - LSE_hi}
+ * for j < lengths[b], over the rows that see key j, with the scores and masks of attn_fwd_kv8
+ * and the lse it returned for the same arguments.  weights_out may be weights itself;
+ * weights = NULL starts from zero.
+ */
+int attn_kv8_weights(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int block, float c,
+                     const void* q, const void* k8, const float* k_scales, const int32_t* lengths,
+                     const int32_t* counts, int mask_kind, const float* lse, const float* weights,
+                     float* weights_out, void* stream);
+
+/*
+ * Eviction: writes into another cache (of capacity cap_out, same d and block) the tokens worth
+ * keeping.  Of a sequence of length L > keep each head keeps its first `sink` and last `recent`
+ * tokens and, of those between, the keep - sink - recent of the largest weight (equal weights:
+ * the lower position first; a NaN weight counts as -inf); of a shorter one it keeps all.  The
+ * tokens keep their order, so attention and later appends go on as before.
+ *   kept         int32 [B][H_kv][keep]: the kept positions, ascending, then -1
+ *   lengths_out  min(L, keep); k8_out, v8_out, k_scales_out, v_scales_out, weights_out: the
+ *                tokens' values quantized again in their new blocks by attn_kv8_append's rule,
+ *                and their weights.  Positions past lengths_out[b] are left as they were.
+ * keep: 1 .. cap_out; sink, recent >= 0 with sink + recent <= keep.  No output may overlap an
+ * input.
+ */
+int attn_kv8_evict(int B, int H_kv, int d, int cap, int block, const void* k8, const void* v8,
+                   const float* k_scales, const float* v_scales, const float* weights,
+                   const int32_t* lengths, int keep, int sink, int recent, int cap_out,
+                   void* k8_out, void* v8_out, float* k_scales_out, float* v_scales_out,
+                   float* weights_out, int32_t* lengths_out, int32_t* kept, void* stream);
+
 /* The number of key shares attn_fwd_kv uses when num_splits = 0 on the current device. */
 int attn_fwd_kv_split_count(int dtype, int B, int H, int n_q, int n_kv, int d, int kv_block);
 
@@ -355,7 +450,8 @@ int attn_bwd_noalloc(int dtype, int B, int H, int n, int d, float c,
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of the current device.
- * Returns ATTN_OK, ATTN_WARN_EMPTY_ROW, ATTN_ERR_DEVICE_TIMEOUT (a bounded wait inside a kernel
+ * Returns ATTN_OK, ATTN_WARN_EMPTY_ROW, ATTN_WARN_CLAMPED (which hides an empty row's warning:
+ * the lengths are to be mended first), ATTN_ERR_DEVICE_TIMEOUT (a bounded wait inside a kernel
  * gave up; the kernel freed its resources and returned without finishing) or ATTN_ERR_CUDA.
  */
 int attn_device_status(void* stream);
