@@ -376,65 +376,78 @@ def attn_fwd_fp8_blocks(q8, k8, vt8, q_scales, k_scales, v_scales, c, mask="none
     return o, lse
 
 
-def _kv8_cache(codes, scales, lengths, device=None):
-    """(B, H_kv, cap, d, block) of an 8-bit cache: code tensors [B,H_kv,cap,d], scale tensors
-    [B,H_kv,cap/block] and lengths [B], all contiguous on one CUDA device."""
-    first = codes[0]
-    if first.dim() != 4:
-        raise ValueError("codes must be [B,H_kv,cap,d]")
-    B, Hk, cap, d = first.shape
-    device = first.device if device is None else device
-    for t in codes:
-        _fp8_bytes(t, "codes")
-        if t.shape != first.shape:
-            raise ValueError("k8 and v8 must have the same shape")
-    nblk = scales[0].shape[-1] if scales[0].dim() == 3 else 0
-    if nblk < 1 or cap % nblk:
-        raise ValueError("scales must be [B,H_kv,cap/block]")
-    for t in scales:
-        _kv8_array(t, torch.float32, (B, Hk, nblk), "scales")
-    _kv8_array(lengths, torch.int32, (B,), "lengths")
-    for t in (*codes, *scales, lengths):
-        if t.device != device:
-            raise ValueError("the call's tensors must lie on one device")
-    return B, Hk, cap, d, cap // nblk
+_KV8_CODES = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+_KV8_INPUTS = (torch.float16, torch.bfloat16)
 
 
-def _kv8_array(t, dtype, shape, name, device=None):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+def _kv8_array(t, dtype, shape, name, device):
+    """The address of t, a contiguous tensor of the given type and shape on the call's device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError("the call's tensors must lie on one device")
-    return t
+    if t.device != device:
+        raise ValueError(f"{name} must lie on the call's device, {device}")
+    return t.data_ptr()
+
+
+def _kv8_codes(t, shape, name, device):
+    if t.dtype not in _KV8_CODES:
+        raise ValueError(f"{name} must hold E4M3 values (torch.float8_e4m3fn or uint8)")
+    return _kv8_array(t, t.dtype, shape, name, device)
 
 
 def _kv8_input(t, shape, name, device):
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    if t.dtype not in _KV8_INPUTS:
         raise ValueError(f"{name} must be float16 or bfloat16")
     return _kv8_array(t, t.dtype, shape, name, device)
 
 
+def _kv8_optional(t, dtype, shape, name, device):
+    return None if t is None else _kv8_array(t, dtype, shape, name, device)
+
+
+def _kv8_shape(k8, k_scales):
+    """(B, H_kv, cap, d, block, device) from the codes [B,H_kv,cap,d] and scales [B,H_kv,cap/block]."""
+    if not k8.is_cuda:
+        raise ValueError("the 8-bit cache must be CUDA tensors")
+    if k8.dim() != 4 or k_scales.dim() != 3:
+        raise ValueError("codes must be [B,H_kv,cap,d] and scales [B,H_kv,cap/block]")
+    B, Hk, cap, d = k8.shape
+    nblk = k_scales.shape[2]
+    if nblk < 1 or cap % nblk:
+        raise ValueError("scales must be [B,H_kv,cap/block]")
+    return B, Hk, cap, d, cap // nblk, k8.device
+
+
+def _kv8_heads(q, B, Hk, mask):
+    if q.dim() != 4 or q.shape[0] != B or q.shape[1] < 1 or q.shape[1] % Hk:
+        raise ValueError("q must be [B,H,n_q,d] with H a multiple of H_kv")
+    return q.shape[1], q.shape[2], MASK_CODE[mask]
+
+
 class _On:
-    """The device of the call's tensors made current, and the stream it is to run on; what is
-    allocated inside belongs to that stream."""
+    """The call's device made current for a call, and its stream: what is allocated inside belongs
+    to the stream the kernels run on.  Yields the stream's handle."""
+
+    __slots__ = ("index", "stream", "was")
 
     def __init__(self, device, stream):
-        self._device = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self._stream = stream
+        self.index, self.stream, self.was = device.index, stream, None
 
     def __enter__(self):
-        if self._device is not None:
-            self._device.__enter__()
-        if self._stream is not None:
-            self._stream = torch.cuda.stream(self._stream)
-            self._stream.__enter__()
-        return _stream_ptr(None)
+        was = torch.cuda.current_device()
+        if was != self.index:
+            torch.cuda.set_device(self.index)
+            self.was = was
+        if self.stream is not None:
+            self.stream = torch.cuda.stream(self.stream)
+            self.stream.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.was is not None:
+            torch.cuda.set_device(self.was)
 
 
 def attn_kv8_append(k_new, v_new, k8, v8, k_scales, v_scales, lengths, counts=None, weights=None,
@@ -444,23 +457,22 @@ def attn_kv8_append(k_new, v_new, k8, v8, k_scales, v_scales, lengths, counts=No
     counts[b] (None: n) of the lengths[b] positions of each sequence; ``lengths`` and ``counts``
     are int32 CUDA tensors [B], the lengths already counting the new tokens.  ``weights`` (float32
     [B,H_kv,cap], optional) is set to 0 there."""
-    B, Hk, cap, d, block = _kv8_cache((k8, v8), (k_scales, v_scales), lengths)
-    dev = k8.device
+    B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
     if k_new.dim() != 4:
         raise ValueError("k_new and v_new must be [B,H_kv,n,d]")
-    n = k_new.shape[2]
-    for t, nm in ((k_new, "k_new"), (v_new, "v_new")):
-        _kv8_input(t, (B, Hk, n, d), nm, dev)
-    if v_new.dtype != k_new.dtype:
+    if v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new must share one dtype")
-    if counts is not None:
-        _kv8_array(counts, torch.int32, (B,), "counts", dev)
-    if weights is not None:
-        _kv8_array(weights, torch.float32, (B, Hk, cap), "weights", dev)
+    n, f32, i32 = k_new.shape[2], torch.float32, torch.int32
+    new, codes, scales = (B, Hk, n, d), (B, Hk, cap, d), (B, Hk, cap // block)
+    ptrs = (_kv8_input(k_new, new, "k_new", dev), _kv8_input(v_new, new, "v_new", dev),
+            _kv8_array(lengths, i32, (B,), "lengths", dev),
+            _kv8_optional(counts, i32, (B,), "counts", dev),
+            _kv8_codes(k8, codes, "k8", dev), _kv8_codes(v8, codes, "v8", dev),
+            _kv8_array(k_scales, f32, scales, "k_scales", dev),
+            _kv8_array(v_scales, f32, scales, "v_scales", dev),
+            _kv8_optional(weights, f32, (B, Hk, cap), "weights", dev))
     with _On(dev, stream) as s:
-        _check(load().attn_kv8_append(DTYPE_CODE[k_new.dtype], B, Hk, n, d, cap, block, _ptr(k_new),
-                                      _ptr(v_new), _ptr(lengths), _ptr(counts), _ptr(k8), _ptr(v8),
-                                      _ptr(k_scales), _ptr(v_scales), _ptr(weights), s))
+        _check(load().attn_kv8_append(DTYPE_CODE[k_new.dtype], B, Hk, n, d, cap, block, *ptrs, s))
 
 
 def attn_fwd_kv8_workspace_bytes(dtype, B, H, H_kv, n_q, d, cap) -> int:
@@ -469,41 +481,40 @@ def attn_fwd_kv8_workspace_bytes(dtype, B, H, H_kv, n_q, d, cap) -> int:
     return int(load().attn_fwd_kv8_workspace_bytes(code, B, H, H_kv, n_q, d, cap))
 
 
-def _kv8_query(q, B, Hk, d, counts, mask, device):
-    if q.dim() != 4 or q.shape[1] < 1 or q.shape[1] % Hk:
-        raise ValueError("q must be [B,H,n_q,d] with H a multiple of H_kv")
-    H, n = q.shape[1], q.shape[2]
-    _kv8_input(q, (B, H, n, d), "q", device)
-    if counts is not None:
-        _kv8_array(counts, torch.int32, (B,), "counts", device)
-    return H, n, MASK_CODE[mask]
-
-
 def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="none", o=None,
                  lse=None, workspace=None, stream=None):
     """Attention of q [B,H,n_q,d] (float16 or bfloat16) over the 8-bit cache of
     ``attn_kv8_append``, H a multiple of H_kv; the queries are each sequence's last counts[b]
     (None: n_q) positions, rows past that are padding.  mask "none" or "causal".  Returns
     (o [B,H,n_q,d], lse [B,H,n_q] float32)."""
-    B, Hk, cap, d, block = _kv8_cache((k8, v8), (k_scales, v_scales), lengths)
-    H, n, kind = _kv8_query(q, B, Hk, d, counts, mask, k8.device)
-    with _On(q.device, stream) as s:
-        o = torch.empty_like(q) if o is None else _kv8_array(o, q.dtype, q.shape, "o", q.device)
-        if lse is None:
-            lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
+    B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
+    H, n, kind = _kv8_heads(q, B, Hk, mask)
+    f32, i32 = torch.float32, torch.int32
+    codes, scales = (B, Hk, cap, d), (B, Hk, cap // block)
+    ptrs = (_kv8_input(q, (B, H, n, d), "q", dev), _kv8_codes(k8, codes, "k8", dev),
+            _kv8_codes(v8, codes, "v8", dev), _kv8_array(k_scales, f32, scales, "k_scales", dev),
+            _kv8_array(v_scales, f32, scales, "v_scales", dev),
+            _kv8_array(lengths, i32, (B,), "lengths", dev),
+            _kv8_optional(counts, i32, (B,), "counts", dev))
+    lib, code = load(), DTYPE_CODE[q.dtype]
+    with _On(dev, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
         else:
-            _kv8_array(lse, torch.float32, (B, H, n), "lse", q.device)
-        lib = load()
-        code = DTYPE_CODE[q.dtype]
+            _kv8_array(o, q.dtype, q.shape, "o", dev)
+        if lse is None:
+            lse = torch.empty((B, H, n), dtype=f32, device=dev)
+        else:
+            _kv8_array(lse, f32, (B, H, n), "lse", dev)
         if workspace is None:
-            need = lib.attn_fwd_kv8_workspace_bytes(code, B, H, Hk, n, d, cap)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        elif workspace.device != q.device or not workspace.is_contiguous():
+            size = lib.attn_fwd_kv8_workspace_bytes(code, B, H, Hk, n, d, cap)
+            workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the call's device")
-        _check(lib.attn_fwd_kv8(code, B, H, Hk, n, d, cap, block, float(c), _ptr(q), _ptr(k8),
-                                _ptr(v8), _ptr(k_scales), _ptr(v_scales), _ptr(lengths),
-                                _ptr(counts), kind, _ptr(o), _ptr(lse), _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), s))
+        else:
+            size = workspace.numel() * workspace.element_size()
+        _check(lib.attn_fwd_kv8(code, B, H, Hk, n, d, cap, block, c, *ptrs, kind, o.data_ptr(),
+                                lse.data_ptr(), workspace.data_ptr(), size, s))
     return o, lse
 
 
@@ -512,18 +523,21 @@ def attn_kv8_weights(q, k8, k_scales, lengths, lse, weights, c, counts=None, mas
     """Adds to the running attention weight of each cached key (``weights`` float32
     [B,H_kv,cap]; None: zeros) what the queries give it, from the lse of ``attn_fwd_kv8`` on the
     same arguments.  Writes ``out`` (None: ``weights`` in place) and returns it."""
-    B, Hk, cap, d, block = _kv8_cache((k8,), (k_scales,), lengths)
-    H, n, kind = _kv8_query(q, B, Hk, d, counts, mask, k8.device)
-    _kv8_array(lse, torch.float32, (B, H, n), "lse", q.device)
-    for t in (weights, out):
-        if t is not None:
-            _kv8_array(t, torch.float32, (B, Hk, cap), "weights", q.device)
-    with _On(q.device, stream) as s:
+    B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
+    H, n, kind = _kv8_heads(q, B, Hk, mask)
+    f32, i32 = torch.float32, torch.int32
+    ptrs = (_kv8_input(q, (B, H, n, d), "q", dev), _kv8_codes(k8, (B, Hk, cap, d), "k8", dev),
+            _kv8_array(k_scales, f32, (B, Hk, cap // block), "k_scales", dev),
+            _kv8_array(lengths, i32, (B,), "lengths", dev),
+            _kv8_optional(counts, i32, (B,), "counts", dev))
+    p_lse = _kv8_array(lse, f32, (B, H, n), "lse", dev)
+    p_w = _kv8_optional(weights, f32, (B, Hk, cap), "weights", dev)
+    _kv8_optional(out, f32, (B, Hk, cap), "out", dev)
+    with _On(dev, stream) as s:
         if out is None:
-            out = torch.zeros((B, Hk, cap), device=q.device) if weights is None else weights
-        _check(load().attn_kv8_weights(DTYPE_CODE[q.dtype], B, H, Hk, n, d, cap, block, float(c),
-                                       _ptr(q), _ptr(k8), _ptr(k_scales), _ptr(lengths),
-                                       _ptr(counts), kind, _ptr(lse), _ptr(weights), _ptr(out), s))
+            out = torch.zeros((B, Hk, cap), dtype=f32, device=dev) if weights is None else weights
+        _check(load().attn_kv8_weights(DTYPE_CODE[q.dtype], B, H, Hk, n, d, cap, block, c, *ptrs,
+                                       kind, p_lse, p_w, out.data_ptr(), s))
     return out
 
 
@@ -533,24 +547,27 @@ def attn_kv8_evict(k8, v8, k_scales, v_scales, weights, lengths, keep, k8_out, v
     tokens of each sequence and head worth keeping: the first ``sink``, the last ``recent`` and
     the heaviest of the rest by ``weights``, in order, ``keep`` at most.  Returns the kept
     positions, int32 [B,H_kv,keep], -1 past the new length."""
-    B, Hk, cap, d, block = _kv8_cache((k8, v8), (k_scales, v_scales), lengths)
-    dev, keep = k8.device, int(keep)
-    B2, Hk2, cap_out, d2, block2 = _kv8_cache((k8_out, v8_out), (k_scales_out, v_scales_out),
-                                              lengths_out, dev)
-    if (B2, Hk2, d2, block2) != (B, Hk, d, block):
-        raise ValueError("the two caches must agree on B, H_kv, d and block")
-    _kv8_array(weights, torch.float32, (B, Hk, cap), "weights", dev)
-    _kv8_array(weights_out, torch.float32, (B, Hk, cap_out), "weights_out", dev)
+    B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
+    cap_out, keep, f32, i32 = k8_out.shape[2], int(keep), torch.float32, torch.int32
+    if cap_out % block:
+        raise ValueError("the output cache's capacity must be a multiple of the block")
+
+    def cache(k, v, ks, vs, w, lens, m):
+        return ((_kv8_codes(k, (B, Hk, m, d), "k8", dev), _kv8_codes(v, (B, Hk, m, d), "v8", dev),
+                 _kv8_array(ks, f32, (B, Hk, m // block), "k_scales", dev),
+                 _kv8_array(vs, f32, (B, Hk, m // block), "v_scales", dev),
+                 _kv8_array(w, f32, (B, Hk, m), "weights", dev),
+                 _kv8_array(lens, i32, (B,), "lengths", dev)))
+
+    src = cache(k8, v8, k_scales, v_scales, weights, lengths, cap)
+    dst = cache(k8_out, v8_out, k_scales_out, v_scales_out, weights_out, lengths_out, cap_out)
     with _On(dev, stream) as s:
         if kept is None:
-            kept = torch.empty((B, Hk, max(keep, 0)), dtype=torch.int32, device=dev)
+            kept = torch.empty((B, Hk, max(keep, 0)), dtype=i32, device=dev)
         else:
-            _kv8_array(kept, torch.int32, (B, Hk, keep), "kept", dev)
-        _check(load().attn_kv8_evict(B, Hk, d, cap, block, _ptr(k8), _ptr(v8), _ptr(k_scales),
-                                     _ptr(v_scales), _ptr(weights), _ptr(lengths), keep, int(sink),
-                                     int(recent), cap_out, _ptr(k8_out), _ptr(v8_out),
-                                     _ptr(k_scales_out), _ptr(v_scales_out), _ptr(weights_out),
-                                     _ptr(lengths_out), _ptr(kept), s))
+            _kv8_array(kept, i32, (B, Hk, keep), "kept", dev)
+        _check(load().attn_kv8_evict(B, Hk, d, cap, block, *src, keep, int(sink), int(recent), cap_out,
+                                     *dst, kept.data_ptr(), s))
     return kept
 
 

@@ -51,6 +51,7 @@ struct Kv8EvictArgs {
   int32_t* lengths_out;
   int32_t* kept;
   uint32_t* status;
+  int sms;
 };
 
 // Each launcher returns 0 or a negative ATTN_ERR_* code and fills `err` on failure.

@@ -247,7 +247,7 @@ int attn_kv8_evict(int B, int H_kv, int d, int cap, int block, const void* k8, c
                        static_cast<const uint8_t*>(k8), static_cast<const uint8_t*>(v8), k_scales,
                        v_scales, weights, lengths, static_cast<uint8_t*>(k8_out),
                        static_cast<uint8_t*>(v8_out), k_scales_out, v_scales_out, weights_out,
-                       lengths_out, kept, nullptr};
+                       lengths_out, kept, nullptr, ea::device_sm_count()};
     if (int rc = ea::device_status_word(&a.status)) return rc;
     std::string err;
     const int rc = ea::launch_kv8_evict(a, static_cast<cudaStream_t>(stream), err);

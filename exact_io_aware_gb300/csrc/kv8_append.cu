@@ -53,9 +53,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
   const bool takes = start < len && start + p.block > from;
   const bool holds = takes && from > start;
 
-  const uint16_t* src = static_cast<const uint16_t*>(p.x[side]) + static_cast<int64_t>(bh) * p.n * D;
-  uint8_t* dst = p.codes[side] + static_cast<int64_t>(bh) * p.cap * D;
-  float* scale = p.scales[side] + static_cast<int64_t>(bh) * (p.cap / p.block) + start / p.block;
+  const uint16_t* src = static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) + static_cast<int64_t>(bh) * p.n * D;
+  uint8_t* dst = (side ? p.codes[1] : p.codes[0]) + static_cast<int64_t>(bh) * p.cap * D;
+  float* scale = (side ? p.scales[1] : p.scales[0]) + static_cast<int64_t>(bh) * (p.cap / p.block) + start / p.block;
   const int sub = lane / kLanes, col = lane % kLanes * 8;
 
   const float old = holds ? *scale : 0.0f;

@@ -22,11 +22,15 @@
 namespace ea {
 namespace kv8 {
 
-constexpr int kAttendWarps = 8;
+constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = kAttendWarps * 32;
 constexpr float kTop = 6.0f;     // log2 of the largest P when m is set
 constexpr float kRaise = 14.0f;  // a larger log2 P raises m
 constexpr float kNoMax = -3.0e38f;
+// A cache of at most this many tokens a sequence is not cut: each tile is one CTA's, and there is
+// nothing to join.
+constexpr int kAlignedCap = 512;
+constexpr int kMostCtas = 3;  // of any variant, on a multiprocessor
 
 struct AttendParams {
   Geometry geo;
@@ -39,42 +43,53 @@ struct AttendParams {
   const float* v_scales;
   uint16_t* o;
   float* lse;
-  float* part;     // [2 gridDim.x][tile][D + 2]: z, l, m
-  int min_chunks;  // a CTA's run has at least this many
+  float* part_z;   // [2 ctas][tile][D]: parts of shared tiles, two places a CTA
+  float* part_lm;  // [2 ctas][tile][2]: their l and m
+  int ctas;        // runs the work is cut into; 0: one CTA a tile, and no parts
+  int min_chunks;  // a run has at least this many
   uint32_t* status;
 };
 
-template <int D>
-constexpr int attend_stages() { return D == 128 ? 3 : 6; }
+// CTAs resident on a multiprocessor (registers and shared memory are sized for them): while one
+// starts on a tile or merges its warps, the others stream.
+template <int NT>
+constexpr int attend_ctas_per_sm() { return NT == 1 ? 3 : 2; }
 template <int D>
 constexpr int stage_bytes() { return 2 * Chunk<D>::kBytes + 32; }  // K, V, four scales
-template <int D>
-constexpr size_t ring_bytes() { return static_cast<size_t>(kAttendWarps) * attend_stages<D>() * stage_bytes<D>(); }
-// The warps' states at a tile's end, over the drained ring: z, then l and m of each row.
 template <int D, int NT>
-constexpr size_t merge_bytes() { return static_cast<size_t>(kAttendWarps) * NT * 8 * (D + 2) * sizeof(float); }
-
-__device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int min_chunks) {
-  const int64_t per = (total + ctas - 1) / ctas;
-  return per < min_chunks ? min_chunks : per;
+constexpr int attend_stages() {
+  const int fit = (225 * 1024 / attend_ctas_per_sm<NT>() - 1024) / (kAttendWarps * stage_bytes<D>());
+  return fit < 5 ? fit : 5;
+}
+template <int D, int NT>
+constexpr size_t ring_bytes() { return static_cast<size_t>(kAttendWarps) * attend_stages<D, NT>() * stage_bytes<D>(); }
+// The warps' states at a tile's end, over the drained ring: z (rows padded apart), then l and m.
+template <int D>
+constexpr int merge_stride() { return D + 4; }
+template <int D, int NT>
+constexpr size_t merge_bytes() {
+  return static_cast<size_t>(kAttendWarps) * NT * 8 * (merge_stride<D>() + 2) * sizeof(float);
 }
 
-template <bool kBf16>
-__device__ __forceinline__ uint16_t to16(float x) {
-  if constexpr (kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  return __half_as_ushort(__float2half_rn(x));
-}
-
-// Writes one element of a finished row and, for column 0, its LSE.  z / l with l = 0 is a row
+// Writes four columns of a finished row and, with the first of them, its LSE.  l = 0 is a row
 // that sees no key: O = 0, LSE = -inf.
-template <bool kBf16>
-__device__ __forceinline__ void write_out(const AttendParams& p, int D, int64_t row, int col,
-                                          float z, float l, float m, bool real) {
-  const bool empty = l == 0.0f;
-  p.o[row * D + col] = to16<kBf16>(empty || !real ? 0.0f : z / l);
+template <bool kBf16, int D>
+__device__ __forceinline__ void write_out(const AttendParams& p, int64_t row, int col, float4 z,
+                                          float l, float m, bool real) {
+  const bool none = l == 0.0f || !real;
+  const float inv = none ? 0.0f : 1.0f / l;
+  uint2 w;
+  if constexpr (kBf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(z.x * inv, z.y * inv), b = __floats2bfloat162_rn(z.z * inv, z.w * inv);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    w = make_uint2(pack_f16(z.x * inv, z.y * inv), pack_f16(z.z * inv, z.w * inv));
+  }
+  if (none) w = make_uint2(0u, 0u);
+  *reinterpret_cast<uint2*>(p.o + row * D + col) = w;
   if (col == 0) {
-    p.lse[row] = empty || !real ? -INFINITY : kLn2 * (m + log2f(l));
-    if (empty && real) raise_empty_row(p.status);
+    p.lse[row] = none ? -INFINITY : kLn2 * (m + log2f(l));
+    if (none && real) raise_empty_row(p.status);
   }
 }
 
@@ -213,20 +228,34 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
 }
 
 template <bool kBf16, int D, int NT>
-__global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
+    attend_kernel(const AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kStages = attend_stages<D>();
+  constexpr int kStages = attend_stages<D, NT>();
   constexpr int kTile = NT * 8;
   const int lane = lane_id(), warp = warp_id(), g = lane >> 2, t = lane & 3;
   const Geometry& geo = p.geo;
-  const int64_t total = total_chunks(geo);
-  const int64_t per = run_length(total, gridDim.x, p.min_chunks);
-  const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, total);
-  if (u0 >= u1) return;
+  grid_launch_dependents();
   uint8_t* ring = smem + warp * (kStages * stage_bytes<D>());
   const int nblk = geo.cap / p.block;
 
-  Place pl = place_of(geo, u0);
+  int64_t u0, u1;
+  Place pl;
+  if (p.ctas > 0) {
+    pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    if (u0 >= u1) return;
+  } else {
+    const int tile = blockIdx.x;
+    pl.rt = tile % geo.tiles;
+    pl.hk = tile / geo.tiles % geo.Hk;
+    pl.b = tile / geo.tiles / geo.Hk;
+    pl.start = u0 = 0;
+    const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
+    pl.keys = tile_keys(geo, len, cnt, pl.rt);
+    u1 = chunks_of(pl.keys);
+    if (pl.rt == 0 && pl.hk == 0 && threadIdx.x == 0)
+      check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
+  }
   for (;;) {
     const int tile_chunks = chunks_of(pl.keys);
     const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
@@ -317,7 +346,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendP
     }
     cp_async_wait<0>();
 
-    // Merge the warps' states: each warp puts its z, l, m into shared memory.
+    // Merge the warps' states: each warp puts its z, l, m into shared memory.  Rows 2t and 2t + 1
+    // of a block of eight lie at t and 4 + t, which keeps eight lanes' 16-byte stores apart.
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -325,50 +355,52 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendP
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], o);
     __syncthreads();
+    constexpr int kStride = merge_stride<D>();
     float* mz = reinterpret_cast<float*>(smem);
-    float* mlm = mz + kAttendWarps * kTile * D;
+    float* mlm = mz + kAttendWarps * kTile * kStride;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int row = j * 8 + 2 * t + c;
-        float* dst = mz + (warp * kTile + row) * D + g * (D / 8);
+        const int at = warp * kTile + j * 8 + c * 4 + t;
+        float4* dst = reinterpret_cast<float4*>(mz + at * kStride + g * (D / 8));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          dst[2 * i] = z[j][i][c];
-          dst[2 * i + 1] = z[j][i][c + 2];
-        }
+        for (int i = 0; i < D / 32; ++i)
+          dst[i] = make_float4(z[j][2 * i][c], z[j][2 * i][c + 2], z[j][2 * i + 1][c], z[j][2 * i + 1][c + 2]);
         if (g == 0) {
-          mlm[(warp * kTile + row) * 2] = l[j][c];
-          mlm[(warp * kTile + row) * 2 + 1] = m[j][c];
+          mlm[at * 2] = l[j][c];
+          mlm[at * 2 + 1] = m[j][c];
         }
       }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == tile_chunks;
-    float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kTile * (D + 2);
-    for (int idx = threadIdx.x; idx < kTile * D; idx += kAttendThreads) {
-      const int row = idx / D, col = idx % D;
+    const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kTile;
+    for (int idx = threadIdx.x; idx < kTile * (D / 4); idx += kAttendThreads) {
+      const int row = idx / (D / 4), col = idx % (D / 4) * 4;
+      const int at = (row & ~7) + (row & 1) * 4 + ((row & 7) >> 1);
       float mx = kNoMax;
 #pragma unroll
-      for (int w = 0; w < kAttendWarps; ++w) mx = fmaxf(mx, mlm[(w * kTile + row) * 2 + 1]);
-      float zs = 0.0f, ls = 0.0f;
+      for (int w = 0; w < kAttendWarps; ++w) mx = fmaxf(mx, mlm[(w * kTile + at) * 2 + 1]);
+      float4 zs = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float ls = 0.0f;
 #pragma unroll
       for (int w = 0; w < kAttendWarps; ++w) {
-        const float f = ex2(mlm[(w * kTile + row) * 2 + 1] - mx);
-        zs = fmaf(f, mz[(w * kTile + row) * D + col], zs);
-        ls = fmaf(f, mlm[(w * kTile + row) * 2], ls);
+        const float f = ex2(mlm[(w * kTile + at) * 2 + 1] - mx);
+        const float4 x = *reinterpret_cast<const float4*>(mz + (w * kTile + at) * kStride + col);
+        zs.x = fmaf(f, x.x, zs.x);
+        zs.y = fmaf(f, x.y, zs.y);
+        zs.z = fmaf(f, x.z, zs.z);
+        zs.w = fmaf(f, x.w, zs.w);
+        ls = fmaf(f, mlm[(w * kTile + at) * 2], ls);
       }
       const int r = pl.rt * kTile + row;
       if (whole) {
         if (r < geo.R)
-          write_out<kBf16>(p, D, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), col, zs, ls, mx,
-                           r / geo.G < cnt);
+          write_out<kBf16, D>(p, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), col, zs, ls, mx,
+                              r / geo.G < cnt);
       } else {
-        part[row * (D + 2) + col] = zs;
-        if (col == 0) {
-          part[row * (D + 2) + D] = ls;
-          part[row * (D + 2) + D + 1] = mx;
-        }
+        *reinterpret_cast<float4*>(p.part_z + (slot + row) * D + col) = zs;
+        if (col == 0) *reinterpret_cast<float2*>(p.part_lm + (slot + row) * 2) = make_float2(ls, mx);
       }
     }
     if (pl.start + tile_chunks >= u1) break;
@@ -378,78 +410,109 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendP
 }
 
 // Joins the parts of tiles that several CTAs shared, and writes tiles that see no key at all.
-// One CTA a tile.
+// One warp a row, eight rows a CTA.
+constexpr int kJoinWarps = 8;
 template <bool kBf16, int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendParams p) {
+  constexpr int kCols = D / 32;  // columns of a lane
   const Geometry& geo = p.geo;
-  int64_t id = blockIdx.x;
+  int id = blockIdx.x;
   Place pl;
-  pl.rt = static_cast<int>(id % geo.tiles);
+  pl.rt = id % geo.tiles;
   id /= geo.tiles;
-  pl.hk = static_cast<int>(id % geo.Hk);
-  pl.b = static_cast<int>(id / geo.Hk);
+  pl.hk = id % geo.Hk;
+  pl.b = id / geo.Hk;
+  const int lane = lane_id();
+  const int row = blockIdx.y * kJoinWarps + warp_id(), r = pl.rt * geo.tile + row;
   const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
-  if (pl.rt == 0 && pl.hk == 0 && threadIdx.x == 0)
+  if (pl.rt == 0 && pl.hk == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
   pl.keys = tile_keys(geo, len, cnt, pl.rt);
-  const int r0 = pl.rt * geo.tile, rows = min(geo.tile, geo.R - r0);
-  if (pl.keys == 0) {
-    for (int idx = threadIdx.x; idx < rows * D; idx += blockDim.x) {
-      const int r = r0 + idx / D;
-      write_out<kBf16>(p, D, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), idx % D, 0.0f, 0.0f,
-                       0.0f, r / geo.G < cnt);
-    }
-    return;
+  int64_t first = 0, last = 0;
+  if (pl.keys > 0) {
+    int64_t total;
+    locate(geo, pl, total);
+    const int64_t per = run_length(total, p.ctas, p.min_chunks);
+    first = pl.start / per;
+    last = (pl.start + chunks_of(pl.keys) - 1) / per;
   }
-  const int64_t per = run_length(total_chunks(geo), ctas, p.min_chunks);
-  int64_t start = sequence_start(geo, pl.b) + pl.hk * head_chunks(geo, pl.b);
-  for (int rt = 0; rt < pl.rt; ++rt) start += chunks_of(tile_keys(geo, len, cnt, rt));
-  const int64_t end = start + chunks_of(pl.keys);
-  const int64_t first = start / per, last = (end - 1) / per;
-  if (first == last) return;
-  for (int idx = threadIdx.x; idx < rows * D; idx += blockDim.x) {
-    const int row = idx / D, col = idx % D, r = r0 + row;
-    float mx = kNoMax, zs = 0.0f, ls = 0.0f;
-    for (int64_t c = first; c <= last; ++c) {
-      const float* part = p.part + ((2 * c + (c == first ? 1 : 0)) * geo.tile + row) * (D + 2);
-      mx = fmaxf(mx, part[D + 1]);
+  grid_dependency_wait();  // by every warp: what follows on the stream may rely on this kernel
+  if (r >= geo.R || (pl.keys > 0 && first == last)) return;  // or one CTA held the tile whole
+  float mx = kNoMax, l = 0.0f;
+  float z[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
+  if (pl.keys > 0) {
+    // Place 1 of the first CTA (the tile starts there), place 0 of the others.
+    for (int64_t c0 = first; c0 <= last; c0 += 32) {
+      const int parts = static_cast<int>(min(last - c0 + 1, static_cast<int64_t>(32)));
+      float2 lm = make_float2(0.0f, kNoMax);
+      if (lane < parts) {
+        const int64_t slot = 2 * (c0 + lane) + (c0 + lane == first ? 1 : 0);
+        lm = *reinterpret_cast<const float2*>(p.part_lm + (slot * geo.tile + row) * 2);
+      }
+      const float mn = fmaxf(mx, warp_max(lm.y)), old = ex2(mx - mn);
+      mx = mn;
+      const float f = ex2(lm.y - mx);
+      float ls = f * lm.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
+      l = fmaf(l, old, ls);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) z[i] *= old;
+#pragma unroll 4
+      for (int c = 0; c < parts; ++c) {
+        const int64_t slot = 2 * (c0 + c) + (c0 + c == first ? 1 : 0);
+        const float* src = p.part_z + (slot * geo.tile + row) * D + lane * kCols;
+        const float w = __shfl_sync(0xFFFFFFFFu, f, c);
+        if constexpr (kCols == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          z[0] = fmaf(w, x.x, z[0]), z[1] = fmaf(w, x.y, z[1]);
+          z[2] = fmaf(w, x.z, z[2]), z[3] = fmaf(w, x.w, z[3]);
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          z[0] = fmaf(w, x.x, z[0]), z[1] = fmaf(w, x.y, z[1]);
+        }
+      }
     }
-    for (int64_t c = first; c <= last; ++c) {
-      const float* part = p.part + ((2 * c + (c == first ? 1 : 0)) * geo.tile + row) * (D + 2);
-      const float f = ex2(part[D + 1] - mx);
-      zs = fmaf(f, part[col], zs);
-      ls = fmaf(f, part[D], ls);
-    }
-    write_out<kBf16>(p, D, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), col, zs, ls, mx,
-                     r / geo.G < cnt);
   }
+  float4 out = make_float4(z[0], z[1], 0.0f, 0.0f);
+  if constexpr (kCols == 4) {
+    out.z = z[2], out.w = z[3];
+  } else {  // two lanes' columns make one store
+    out.z = __shfl_down_sync(0xFFFFFFFFu, z[0], 1);
+    out.w = __shfl_down_sync(0xFFFFFFFFu, z[1], 1);
+    if (lane & 1) return;
+  }
+  write_out<kBf16, D>(p, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), lane * kCols, out, l, mx,
+                      r / geo.G < cnt);
 }
 
 inline int rows_per_tile(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 
 template <bool kBf16, int D, int NT>
-cudaError_t launch_attend(const AttendParams& p, int ctas, cudaStream_t s) {
-  constexpr size_t smem = ring_bytes<D>() > merge_bytes<D, NT>() ? ring_bytes<D>() : merge_bytes<D, NT>();
+cudaError_t launch_attend(AttendParams p, int sms, cudaStream_t s) {
+  constexpr size_t smem = ring_bytes<D, NT>() > merge_bytes<D, NT>() ? ring_bytes<D, NT>() : merge_bytes<D, NT>();
   auto* kernel = attend_kernel<kBf16, D, NT>;
-  const cudaError_t attr = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (attr != cudaSuccess) return attr;
-  AttendParams pp = p;
-  void* args[] = {&pp};
-  cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(ctas),
-                                   dim3(kAttendThreads), args, smem, s);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  void* jargs[] = {&pp, &ctas};
-  return cudaLaunchKernel(reinterpret_cast<const void*>(attend_join_kernel<kBf16, D>),
-                          dim3(static_cast<unsigned>(p.geo.B) * p.geo.Hk * p.geo.tiles), dim3(128),
-                          jargs, 0, s);
+  const unsigned tiles = static_cast<unsigned>(p.geo.B) * p.geo.Hk * p.geo.tiles;
+  const bool aligned = p.geo.cap <= kAlignedCap;
+  p.ctas = aligned ? 0 : sms * attend_ctas_per_sm<NT>();
+  void* args[] = {&p};
+  e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(aligned ? tiles : p.ctas),
+                       dim3(kAttendThreads), args, smem, s);
+  if (e != cudaSuccess || aligned) return e;
+  return launch_after(reinterpret_cast<const void*>(attend_join_kernel<kBf16, D>),
+                      dim3(tiles, p.geo.tile / kJoinWarps), dim3(kJoinWarps * 32), args, s);
 }
 
 template <bool kBf16, int D>
-cudaError_t launch_attend_nt(const AttendParams& p, int ctas, cudaStream_t s) {
-  if (p.geo.tile == 8) return launch_attend<kBf16, D, 1>(p, ctas, s);
-  if (p.geo.tile == 16) return launch_attend<kBf16, D, 2>(p, ctas, s);
-  return launch_attend<kBf16, D, 4>(p, ctas, s);
+cudaError_t launch_attend_nt(const AttendParams& p, int sms, cudaStream_t s) {
+  if (p.geo.tile == 8) return launch_attend<kBf16, D, 1>(p, sms, s);
+  if (p.geo.tile == 16) return launch_attend<kBf16, D, 2>(p, sms, s);
+  return launch_attend<kBf16, D, 4>(p, sms, s);
 }
 
 }  // namespace kv8
@@ -457,7 +520,7 @@ cudaError_t launch_attend_nt(const AttendParams& p, int ctas, cudaStream_t s) {
 size_t kv8_attend_workspace_bytes(int, int, int G, int n, int d, int sms) {
   const int64_t R = static_cast<int64_t>(G) * n;
   const int tile = kv8::rows_per_tile(R > 32 ? 32 : static_cast<int>(R));
-  return static_cast<size_t>(2) * sms * tile * (d + 2) * sizeof(float);
+  return static_cast<size_t>(2) * sms * kv8::kMostCtas * tile * (d + 2) * sizeof(float);
 }
 
 int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
@@ -473,15 +536,15 @@ int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   p.v_scales = a.v_scales;
   p.o = static_cast<uint16_t*>(a.o);
   p.lse = a.lse;
-  p.part = static_cast<float*>(a.workspace);
+  p.part_z = static_cast<float*>(a.workspace);
+  p.part_lm = p.part_z + static_cast<size_t>(2) * a.sms * kv8::kMostCtas * tile * a.d;
   p.min_chunks = 2 * kv8::kAttendWarps;
   p.status = a.status;
-  const int ctas = a.sms;
   cudaError_t e;
   if (a.bf16)
-    e = a.d == 128 ? kv8::launch_attend_nt<true, 128>(p, ctas, s) : kv8::launch_attend_nt<true, 64>(p, ctas, s);
+    e = a.d == 128 ? kv8::launch_attend_nt<true, 128>(p, a.sms, s) : kv8::launch_attend_nt<true, 64>(p, a.sms, s);
   else
-    e = a.d == 128 ? kv8::launch_attend_nt<false, 128>(p, ctas, s) : kv8::launch_attend_nt<false, 64>(p, ctas, s);
+    e = a.d == 128 ? kv8::launch_attend_nt<false, 128>(p, a.sms, s) : kv8::launch_attend_nt<false, 64>(p, a.sms, s);
   if (e != cudaSuccess) {
     err = std::string("kv8 attention launch: ") + cudaGetErrorString(e);
     return -5;

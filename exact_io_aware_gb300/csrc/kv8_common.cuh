@@ -21,6 +21,30 @@ namespace kv8 {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// ------------------------------------------------------------------ launches in sequence
+
+// A kernel launched with launch_after may start while the one before it still runs.  The first
+// lets it (grid_launch_dependents) and the second waits, before it touches what the first
+// writes, until the first has finished and its writes are visible (grid_dependency_wait).
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+inline cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
 // ------------------------------------------------------------------ sequences
 
 // Length and new-token count of sequence b, clamped to the buffers they index; a value outside

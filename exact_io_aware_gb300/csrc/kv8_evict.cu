@@ -5,17 +5,25 @@
 // counts as -inf).  The kept tokens keep their order.  Their dequantised values form the
 // destination's blocks, each with the least power-of-two scale that holds them.
 //
-// Two launches.  select: one CTA for each (sequence, head) finds the weight of the last token
-// taken, by a radix descent of 8 bits a pass over order-preserving integer keys, then compacts
-// the kept positions with a scan.  move: as the append kernel, 128 destination positions a CTA
-// and 16 a warp, values in registers between the block's maximum and the conversion.  The move
-// is memory-bound (each kept row is read and written once).
+// Two launches.  select: a cluster of CTAs for each (sequence, head) finds the weight of the last
+// token taken, by a radix descent of 11, 11 and 10 bits over order-preserving integer keys (each
+// CTA counts its share of the tokens; the counts are added through distributed shared memory),
+// then compacts the kept positions: ballots inside a warp, a scan over warps, and the lower
+// CTAs' totals.  move: as the append kernel, 128 destination positions a CTA and 16 a warp,
+// values in registers between the block's maximum and the conversion.  The move is memory-bound
+// (each kept row is read and written once).
+#include <cooperative_groups.h>
+
 #include "kv8_common.cuh"
 
 namespace ea {
 namespace kv8 {
 
+namespace cg = cooperative_groups;
+
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 
 struct EvictParams {
@@ -39,92 +47,137 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the CTA of two counts packed in one word's halves of 64 bits.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red, uint64_t& total) {
+// Exclusive sum of v over the CTA's threads.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red) {
   const int lane = lane_id(), warp = warp_id();
-  uint64_t x = v;
+  uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint64_t t = red[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, t, o);
-      if (lane >= o) t += y;
-    }
-    red[lane] = t;
-  }
-  __syncthreads();
-  total = red[31];
-  return x - v + (warp ? red[warp - 1] : 0);
+  const uint32_t w = lane < warp ? red[lane] : 0u;
+  return x - v + __reduce_add_sync(0xFFFFFFFFu, w);
 }
 
+struct SelectSmem {
+  uint32_t hist[3][kBins];
+  uint32_t red[3][kSelWarps];
+  uint32_t digit[3], left[3];
+  uint32_t above[kSelWarps], equal[kSelWarps];
+  uint32_t total[2];
+};
+
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint64_t red[32];
-  __shared__ uint32_t s_digit, s_left;
-  const int bh = blockIdx.x, b = bh / p.Hk, tid = threadIdx.x;
-  if (bh % p.Hk == 0 && tid == 0) check_seq(p.lengths, nullptr, b, p.cap, 0, p.status);
+  __shared__ SelectSmem sm;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int bh = blockIdx.x / ranks, b = bh / p.Hk, tid = threadIdx.x;
+  const int lane = lane_id(), warp = warp_id();
+  grid_launch_dependents();
+  if (bh % p.Hk == 0 && rank == 0 && tid == 0) check_seq(p.lengths, nullptr, b, p.cap, 0, p.status);
   const int len = seq_len(p.lengths, b, p.cap);
   int32_t* kept = p.kept + static_cast<int64_t>(bh) * p.keep;
   const float* w = p.weights + static_cast<int64_t>(bh) * p.cap;
   if (len <= p.keep) {
-    for (int i = tid; i < p.keep; i += kSelThreads) kept[i] = i < len ? i : -1;
+    for (int i = rank * kSelThreads + tid; i < p.keep; i += ranks * kSelThreads) kept[i] = i < len ? i : -1;
     return;
   }
-  const int lo = p.sink, hi = len - p.recent;  // the middle; hi - lo > want
-  const uint32_t want = p.keep - p.sink - p.recent;
+  // This CTA's share of the tokens, and of the middle ones that compete.
+  const int share = (len + ranks - 1) / ranks;
+  const int i0 = min(rank * share, len), i1 = min(i0 + share, len);
+  const int lo = max(i0, p.sink), hi = min(i1, len - p.recent);
+  const uint32_t want = p.keep - p.sink - p.recent;  // below the middle's size
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
+  __syncthreads();
   uint32_t prefix = 0, left = want;
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t k = order_key(w[i]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&hist[(k >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t l = left;
-        int dgt = 255;
-        while (dgt > 0 && hist[dgt] < l) l -= hist[dgt--];
-        s_digit = dgt;
-        s_left = l;
-      }
-      __syncthreads();
-      prefix |= s_digit << shift;
-      left = s_left;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bins = pass == 2 ? 1024 : 2048;
+    uint32_t* hist = sm.hist[pass];
+#pragma unroll 4
+    for (int i = lo + tid; i < hi; i += kSelThreads) {
+      const uint32_t k = order_key(__ldg(w + i));
+      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
+        atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
     }
-  }
-  // Keys above `prefix` are kept, and the first `left` of those equal to it.
-  uint32_t base_above = 0, base_equal = 0;
-  for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    bool above = false, equal = false;
-    if (i < len) {
-      if (i < lo || i >= hi) {
-        above = true;
-      } else if (want > 0) {
-        const uint32_t k = order_key(w[i]);
-        above = k > prefix;
-        equal = k == prefix;
+    cluster.sync();
+    // Thread t: the counts of the t-th pair of bins from the top, over the whole cluster.
+    uint32_t h0 = 0, h1 = 0;
+    const uint32_t top = bins - 1 - 2 * tid;
+    if (2 * tid < static_cast<int>(bins)) {
+      for (int r = 0; r < ranks; ++r) {
+        const uint32_t* rh = cluster.map_shared_rank(hist, r);
+        h0 += rh[top];
+        h1 += rh[top - 1];
       }
     }
-    uint64_t total;
-    const uint64_t ex = block_scan((static_cast<uint64_t>(equal) << 32) | above, red, total);
-    const uint32_t eq = base_equal + static_cast<uint32_t>(ex >> 32);
-    const uint32_t ab = base_above + static_cast<uint32_t>(ex);
-    if (above || (equal && eq < left)) kept[ab + min(eq, left)] = i;
-    base_above += static_cast<uint32_t>(total);
-    base_equal += static_cast<uint32_t>(total >> 32);
+    const uint32_t ex = block_scan(h0 + h1, sm.red[pass]);
+    if (ex < left && left <= ex + h0 + h1) {
+      const bool second = left > ex + h0;
+      sm.digit[pass] = top - (second ? 1 : 0);
+      sm.left[pass] = left - ex - (second ? h0 : 0);
+    }
+    __syncthreads();
+    if (want > 0) {
+      prefix |= sm.digit[pass] << shift;
+      left = sm.left[pass];
+    }
   }
+  // Keys above `prefix` are kept, and the first `left` of those equal to it.  A warp takes
+  // consecutive tokens of the CTA's share, 32 at a time.
+  const int per_warp = ((i1 - i0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int w0 = min(i0 + warp * per_warp, i1), w1 = min(w0 + per_warp, i1);
+  auto judge = [&](int i, bool& above, bool& equal) {
+    above = equal = false;
+    if (i >= w1) return;
+    if (i < p.sink || i >= len - p.recent) {
+      above = true;
+    } else if (want > 0) {
+      const uint32_t k = order_key(__ldg(w + i));
+      above = k > prefix;
+      equal = k == prefix;
+    }
+  };
+  uint32_t na = 0, ne = 0;
+#pragma unroll 4
+  for (int i = w0; i < w1; i += 32) {
+    bool above, equal;
+    judge(i + lane, above, equal);
+    na += __popc(__ballot_sync(0xFFFFFFFFu, above));
+    ne += __popc(__ballot_sync(0xFFFFFFFFu, equal));
+  }
+  if (lane == 0) sm.above[warp] = na, sm.equal[warp] = ne;
+  __syncthreads();
+  uint32_t xa = sm.above[lane], xe = sm.equal[lane];
+  uint32_t ab = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? xa : 0u);
+  uint32_t eq = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? xe : 0u);
+  if (warp == 0) {
+    xa = __reduce_add_sync(0xFFFFFFFFu, xa);
+    xe = __reduce_add_sync(0xFFFFFFFFu, xe);
+    if (lane == 0) sm.total[0] = xa, sm.total[1] = xe;
+  }
+  cluster.sync();
+  for (int r = 0; r < rank; ++r) {
+    const uint32_t* t = cluster.map_shared_rank(sm.total, r);
+    ab += t[0];
+    eq += t[1];
+  }
+#pragma unroll 2
+  for (int i = w0; i < w1; i += 32) {
+    bool above, equal;
+    judge(i + lane, above, equal);
+    const uint32_t ba = __ballot_sync(0xFFFFFFFFu, above), be = __ballot_sync(0xFFFFFFFFu, equal);
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t ma = ab + __popc(ba & below), me = eq + __popc(be & below);
+    if (above || (equal && me < left)) kept[ma + min(me, left)] = i + lane;
+    ab += __popc(ba);
+    eq += __popc(be);
+  }
+  cluster.sync();  // no CTA leaves while its counts may be read
 }
 
 template <int D>
@@ -136,6 +189,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
   const int lane = lane_id(), warp = warp_id();
   const int bh = blockIdx.y, b = bh / p.Hk, side = blockIdx.z;
   const int live = min(seq_len(p.lengths, b, p.cap), p.keep);
+  grid_dependency_wait();
   if (blockIdx.x == 0 && side == 0 && bh % p.Hk == 0 && threadIdx.x == 0) p.lengths_out[b] = live;
   const int s0 = blockIdx.x * 128;
   if (s0 >= live) return;
@@ -144,8 +198,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
   const int start = s0 + warp / wpb * p.block;
   const int sub = lane / kLanes, col = lane % kLanes * 16;
   const int32_t* kept = p.kept + static_cast<int64_t>(bh) * p.keep;
-  const uint8_t* src = p.codes[side] + static_cast<int64_t>(bh) * p.cap * D;
-  const float* src_scale = p.scales[side] + static_cast<int64_t>(bh) * (p.cap / p.block);
+  const uint8_t* src = (side ? p.codes[1] : p.codes[0]) + static_cast<int64_t>(bh) * p.cap * D;
+  const float* src_scale = (side ? p.scales[1] : p.scales[0]) + static_cast<int64_t>(bh) * (p.cap / p.block);
 
   uint4 raw[kIters];
   float sc[kIters];
@@ -181,8 +235,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
   const float s = pow2(scale_exp(amax));
   const float inv = 1.0f / s;
   if (warp == w0 && lane == 0)
-    p.scales_out[side][static_cast<int64_t>(bh) * (p.cap_out / p.block) + start / p.block] = s;
-  uint8_t* dst = p.codes_out[side] + static_cast<int64_t>(bh) * p.cap_out * D;
+    (side ? p.scales_out[1] : p.scales_out[0])[static_cast<int64_t>(bh) * (p.cap_out / p.block) + start / p.block] = s;
+  uint8_t* dst = (side ? p.codes_out[1] : p.codes_out[0]) + static_cast<int64_t>(bh) * p.cap_out * D;
 #pragma unroll
   for (int it = 0; it < kIters; ++it) {
     const int pos = p0 + it * kRowsIt + sub;
@@ -215,15 +269,26 @@ int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s, std::string& err) {
                      {a.k8_out, a.v8_out}, {a.k_scales_out, a.v_scales_out}, a.weights_out,
                      a.lengths_out, a.kept, a.status};
   void* args[] = {&p};
-  cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(kv8::evict_select_kernel),
-                                   dim3(static_cast<unsigned>(a.B * a.Hk)), dim3(kv8::kSelThreads),
-                                   args, 0, s);
+  // CTAs of a head's cluster: doubled (to the portable 8) while a CTA has more than 4096 tokens
+  // to look at and the clusters leave multiprocessors idle.
+  const int heads = a.B * a.Hk;
+  int ranks = 1;
+  while (ranks < 8 && a.cap > 4096 * ranks && heads * ranks * 2 <= 2 * a.sms) ranks *= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads * ranks));
+  cfg.blockDim = dim3(kv8::kSelThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kv8::evict_select_kernel), args);
   if (e == cudaSuccess) {
     const int most = a.keep < a.cap ? a.keep : a.cap;
-    const dim3 grid(static_cast<unsigned>((most + 127) / 128), static_cast<unsigned>(a.B * a.Hk), 2);
+    const dim3 grid(static_cast<unsigned>((most + 127) / 128), static_cast<unsigned>(heads), 2);
     auto* kernel = a.d == 128 ? kv8::evict_move_kernel<128> : kv8::evict_move_kernel<64>;
-    e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kv8::kMoveThreads), args,
-                         0, s);
+    e = kv8::launch_after(reinterpret_cast<const void*>(kernel), grid, dim3(kv8::kMoveThreads), args, s);
   }
   if (e != cudaSuccess) {
     err = std::string("kv8 evict launch: ") + cudaGetErrorString(e);

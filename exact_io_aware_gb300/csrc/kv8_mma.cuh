@@ -208,63 +208,77 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-// The work list is every chunk of every (sequence, head, row tile), in that order.  One warp
-// (all lanes) gets its length, and the place of an item in it.
-__device__ __forceinline__ int64_t total_chunks(const Geometry& g) {
-  int64_t u = 0;
-  for (int b = lane_id(); b < g.B; b += 32) u += head_chunks(g, b);
-  return g.Hk * warp_sum(u);
-}
-
+// The work list is every chunk of every (sequence, head, row tile), in that order.  It is cut
+// into equal runs, one a CTA, whatever the sequences' lengths.
 struct Place {
   int b, hk, rt;
   int keys;       // keys of the tile
   int64_t start;  // work-list index of the tile's first chunk
 };
 
-// Work-list index of the first chunk of sequence b.
-__device__ __forceinline__ int64_t sequence_start(const Geometry& g, int b) {
-  int64_t u = 0;
-  for (int i = lane_id(); i < b; i += 32) u += head_chunks(g, i);
-  return g.Hk * warp_sum(u);
+__device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int min_chunks) {
+  const int64_t per = (total + ctas - 1) / ctas;
+  return per < min_chunks ? min_chunks : per;
 }
 
-// The tile that item u (below the total) lies in.
-__device__ __forceinline__ Place place_of(const Geometry& g, int64_t u) {
-  Place p{0, 0, 0, 0, 0};
+// The run of CTA `cta` (u0 .. u1 - 1, empty for u0 >= u1) and the tile u0 lies in.  Executed by
+// whole warps; lanes take a sequence each.
+__device__ __forceinline__ Place plan_run(const Geometry& g, int cta, int ctas, int min_chunks,
+                                          int64_t& u0, int64_t& u1) {
   const int lane = lane_id();
-  int64_t base = 0, per = 0;
+  const int64_t v0 = lane < g.B ? head_chunks(g, lane) * g.Hk : 0;
+  int64_t sum = v0;
+  for (int b = lane + 32; b < g.B; b += 32) sum += head_chunks(g, b) * g.Hk;
+  const int64_t total = warp_sum(sum);
+  const int64_t per = run_length(total, ctas, min_chunks);
+  u0 = cta * per;
+  u1 = min(u0 + per, total);
+  Place p{0, 0, 0, 0, 0};
+  if (u0 >= u1) return p;
+  int64_t base = 0, head = 0;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int64_t v = b0 + lane < g.B ? head_chunks(g, b0 + lane) * g.Hk : 0;
+    const int64_t v = b0 == 0 ? v0 : b0 + lane < g.B ? head_chunks(g, b0 + lane) * g.Hk : 0;
     int64_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + x > u);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + x > u0);
     if (past) {
       const int l = __ffs(past) - 1;
       p.b = b0 + l;
-      per = __shfl_sync(0xFFFFFFFFu, v, l) / g.Hk;
+      head = __shfl_sync(0xFFFFFFFFu, v, l) / g.Hk;
       base += __shfl_sync(0xFFFFFFFFu, x - v, l);
       break;
     }
     base += __shfl_sync(0xFFFFFFFFu, x, 31);
   }
   const int len = seq_len(g.lengths, p.b, g.cap), cnt = seq_count(g.counts, p.b, g.n);
-  if (per > 0) {
-    p.hk = static_cast<int>((u - base) / per);
-    base += p.hk * per;
-  }
+  p.hk = static_cast<int>((u0 - base) / head);
+  base += p.hk * head;
   for (;; ++p.rt) {
     p.keys = tile_keys(g, len, cnt, p.rt);
     const int c = chunks_of(p.keys);
-    if (u < base + c || p.rt + 1 >= g.tiles) break;
+    if (u0 < base + c || p.rt + 1 >= g.tiles) break;
     base += c;
   }
   p.start = base;
   return p;
+}
+
+// Work-list index of the first chunk of tile p, and the list's length.  Executed by whole warps.
+__device__ __forceinline__ void locate(const Geometry& g, Place& p, int64_t& total) {
+  int64_t before = 0, all = 0;
+  for (int b = lane_id(); b < g.B; b += 32) {
+    const int64_t u = head_chunks(g, b);
+    all += u;
+    if (b < p.b) before += u;
+  }
+  total = g.Hk * warp_sum(all);
+  p.start = g.Hk * warp_sum(before) + p.hk * head_chunks(g, p.b);
+  const int len = seq_len(g.lengths, p.b, g.cap), cnt = seq_count(g.counts, p.b, g.n);
+  for (int rt = 0; rt < p.rt; ++rt) p.start += chunks_of(tile_keys(g, len, cnt, rt));
 }
 
 // The next tile of the list with at least one chunk (the caller knows that there is one).

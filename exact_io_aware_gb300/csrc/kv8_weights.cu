@@ -5,17 +5,17 @@
 //
 // The scores are formed as in the attention kernel (S^T = K Q^T, a warp to 32 keys), but here
 // a chunk's keys stay in registers as the A operand while all rows pass, eight at a time, from
-// shared memory: the codes are read and widened once for up to 256 rows.  For few rows the
+// shared memory: the codes are read and widened once for up to 128 rows.  For few rows the
 // kernel is bound by reading the codes, for many by the exponentials and products.
 #include "kv8_mma.cuh"
 
 namespace ea {
 namespace kv8 {
 
-constexpr int kWeightsWarps = 8;
+constexpr int kWeightsWarps = 4;
 constexpr int kWeightsThreads = kWeightsWarps * 32;
 constexpr int kWeightsStages = 4;
-constexpr int kWeightsRows = 256;  // rows held in shared memory at once
+constexpr int kWeightsRows = 128;  // rows held in shared memory at once
 
 struct WeightsParams {
   Geometry geo;  // one tile of all rows
@@ -31,7 +31,7 @@ struct WeightsParams {
 };
 
 template <int D>
-constexpr int weights_stage_bytes() { return Chunk<D>::kBytes + 16; }
+constexpr int weights_stage_bytes() { return Chunk<D>::kBytes + 16 + 4 * kChunk; }  // K, scales, sums
 template <int D>
 constexpr int q_row_bytes() { return 2 * D + 16; }  // the pad keeps eight lanes' loads apart
 
@@ -46,14 +46,13 @@ struct WeightsSmem {
 };
 
 template <bool kBf16, int D>
-__global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const WeightsParams p) {
+__global__ void __launch_bounds__(kWeightsThreads, 2) weights_kernel(const WeightsParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   WeightsSmem<D>& sm = *reinterpret_cast<WeightsSmem<D>*>(smem_raw);
   const int lane = lane_id(), warp = warp_id(), g = lane >> 2, t = lane & 3;
   const Geometry& geo = p.geo;
-  const int64_t total = total_chunks(geo);
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, total);
+  int64_t u0, u1;
+  Place pl = plan_run(geo, blockIdx.x, gridDim.x, 1, u0, u1);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < geo.B; b += kWeightsThreads)
       check_seq(geo.lengths, geo.counts, b, geo.cap, geo.n, p.status);
@@ -61,7 +60,6 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const Weigh
   uint8_t* ring = sm.ring + warp * (kWeightsStages * weights_stage_bytes<D>());
   const int nblk = geo.cap / p.block;
 
-  Place pl = place_of(geo, u0);
   for (;;) {
     const int tile_chunks = chunks_of(pl.keys);
     const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
@@ -73,6 +71,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const Weigh
 
     for (int rbase = 0; rbase < geo.R; rbase += kWeightsRows) {
       const int rows = min(kWeightsRows, geo.R - rbase), blocks = (rows + 7) / 8;
+      const float* w_in = rbase ? p.w_out : p.w_in;  // later passes add to the first's
       auto issue = [&](int ch, int stage) {
         if (ch < c1) {
           const uint32_t s = smem_u32(ring + stage * weights_stage_bytes<D>());
@@ -82,6 +81,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const Weigh
             const int key = key0 + lane * 16;
             cp_async4(s + Chunk<D>::kBytes + lane * 4, ksp + (key < len ? key : key0) / p.block);
           }
+          if (w_in && key0 + lane < len)
+            cp_async4(s + Chunk<D>::kBytes + 16 + lane * 4, w_in + bh * geo.cap + key0 + lane);
         }
         cp_async_commit();
       };
@@ -139,8 +140,6 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const Weigh
       }
       __syncthreads();
       const float kmul = p.c2 / qmul;
-      const float* w_in = rbase ? p.w_out : p.w_in;
-
       int stage = 0;
       for (int ch = c0 + warp; ch < c1; ch += kWeightsWarps) {
         cp_async_wait<kWeightsStages - 2>();
@@ -216,10 +215,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const Weigh
             s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
             s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
             const int key = key0 + mt * 16 + e * 8 + Chunk<D>::key_of_slot(g);
-            if (t == 0 && key < len) {
-              const int64_t at = bh * geo.cap + key;
-              p.w_out[at] = (w_in ? w_in[at] : 0.0f) + s;
-            }
+            if (t == 0 && key < len)
+              p.w_out[bh * geo.cap + key] = (w_in ? sc[4 + key - key0] : 0.0f) + s;
           }
         __syncwarp();
         stage = stage + 1 == kWeightsStages ? 0 : stage + 1;
@@ -232,13 +229,13 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) weights_kernel(const Weigh
 }
 
 template <bool kBf16, int D>
-cudaError_t launch_weights(WeightsParams p, int ctas, cudaStream_t s) {
+cudaError_t launch_weights(WeightsParams p, int sms, cudaStream_t s) {
   auto* kernel = weights_kernel<kBf16, D>;
   const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(sizeof(WeightsSmem<D>)));
   if (attr != cudaSuccess) return attr;
   void* args[] = {&p};
-  return cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(ctas), dim3(kWeightsThreads),
+  return cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(2 * sms), dim3(kWeightsThreads),
                           args, sizeof(WeightsSmem<D>), s);
 }
 
