@@ -508,13 +508,15 @@ def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="n
             _kv8_array(lse, f32, (B, H, n), "lse", dev)
         if workspace is None:
             size = lib.attn_fwd_kv8_workspace_bytes(code, B, H, Hk, n, d, cap)
-            workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+            if size > 0:
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the call's device")
         else:
             size = workspace.numel() * workspace.element_size()
         _check(lib.attn_fwd_kv8(code, B, H, Hk, n, d, cap, block, c, *ptrs, kind, o.data_ptr(),
-                                lse.data_ptr(), workspace.data_ptr(), size, s))
+                                lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                                size, s))
     return o, lse
 
 

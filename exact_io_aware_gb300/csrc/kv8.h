@@ -60,6 +60,6 @@ int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err);
 int launch_kv8_weights(const Kv8Args& a, cudaStream_t s, std::string& err);
 int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s, std::string& err);
 
-size_t kv8_attend_workspace_bytes(int B, int Hk, int G, int n, int d, int sms);
+size_t kv8_attend_workspace_bytes(int B, int Hk, int G, int n, int d, int cap, int sms);
 
 }  // namespace ea

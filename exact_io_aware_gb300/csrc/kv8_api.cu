@@ -139,7 +139,7 @@ size_t attn_fwd_kv8_workspace_bytes(int dtype, int B, int H, int H_kv, int n_q, 
   if (dtype < ATTN_F16 || dtype > ATTN_BF16 || B < 1 || H < 1 || H_kv < 1 || n_q < 1 || cap < 1 ||
       H % H_kv != 0 || (d != 64 && d != 128))
     return 0;
-  return ea::kv8_attend_workspace_bytes(B, H_kv, H / H_kv, n_q, d, ea::device_sm_count());
+  return ea::kv8_attend_workspace_bytes(B, H_kv, H / H_kv, n_q, d, cap, ea::device_sm_count());
 }
 
 int attn_fwd_kv8(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int block, float c,
@@ -155,8 +155,8 @@ int attn_fwd_kv8(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int
     if (int rc = check_query(H, H_kv, n_q, mask_kind, counts)) return rc;
     ea::Kv8Args a = cache_args(B, H_kv, H / H_kv, n_q, d, cap, block, lengths, counts);
     a.sms = ea::device_sm_count();
-    const size_t need = ea::kv8_attend_workspace_bytes(B, H_kv, a.G, n_q, d, a.sms);
-    if (!workspace || workspace_bytes < need)
+    const size_t need = ea::kv8_attend_workspace_bytes(B, H_kv, a.G, n_q, d, cap, a.sms);
+    if (need > 0 && (!workspace || workspace_bytes < need))
       return fail(ATTN_ERR_WORKSPACE, "workspace missing or smaller than attn_fwd_kv8_workspace_bytes");
     if (misaligned(workspace, 16)) return fail(ATTN_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
     if (int rc = ea::device_status_word(&a.status)) return rc;

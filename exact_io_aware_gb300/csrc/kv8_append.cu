@@ -29,11 +29,16 @@ struct AppendParams {
   uint32_t* status;
 };
 
+// Largest magnitude of a 16-bit pair as bit patterns (ordered as the values are, not finite above
+// all that is); `most` accumulates both halves.
+__device__ __forceinline__ void pair_max(uint32_t& most, uint32_t w) { most = __vmaxu2(most, w & 0x7FFF7FFFu); }
+
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
   constexpr int kLanes = D / 8;            // lanes of one row (16 bytes of input each)
   constexpr int kRowsIt = 32 / kLanes;     // rows a warp takes at once
   constexpr int kIters = 16 / kRowsIt;
+  constexpr uint32_t kInf = kBf16 ? 0x7F80u : 0x7C00u;
   __shared__ float red[kAppendThreads / 32];
   const int lane = lane_id(), warp = warp_id();
   const int bh = blockIdx.y, b = bh / p.Hk, side = blockIdx.z;
@@ -60,7 +65,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
 
   const float old = holds ? *scale : 0.0f;
   uint4 raw[kIters];
-  float amax = 0.0f;
+  uint32_t most = 0;
 #pragma unroll
   for (int it = 0; it < kIters; ++it) {
     const int pos = p0 + it * kRowsIt + sub;
@@ -70,14 +75,29 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
   }
 #pragma unroll
   for (int it = 0; it < kIters; ++it) {
-    const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack16<kBf16>(w[i]);
-      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
-    }
+    pair_max(most, raw[it].x);
+    pair_max(most, raw[it].y);
+    pair_max(most, raw[it].z);
+    pair_max(most, raw[it].w);
   }
-  amax = warp_max(amax);
+  most = __reduce_max_sync(0xFFFFFFFFu, max(most >> 16, most & 0xFFFFu));
+  const bool strange = most >= kInf;  // of the whole warp: some value is not finite
+  float amax;
+  if (!strange) {
+    amax = unpack16<kBf16>(most).x;
+  } else {
+    amax = 0.0f;
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<kBf16>(w[i]);
+        amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+      }
+    }
+    amax = warp_max(amax);
+  }
   if (lane == 0) red[warp] = amax;
   __syncthreads();
   if (!takes) return;
@@ -100,11 +120,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f[i] = unpack16<kBf16>(w[i]);
+        if (strange) {
+          f[i].x = nan_unless_finite(f[i].x);
+          f[i].y = nan_unless_finite(f[i].y);
+        }
         f[i].x *= inv;
         f[i].y *= inv;
       }
-      *out = make_uint2(pack_codes(f[0].x, f[0].y, f[1].x, f[1].y),
-                        pack_codes(f[2].x, f[2].y, f[3].x, f[3].y));
+      *out = make_uint2(pack4_e4m3(f[0].x, f[0].y, f[1].x, f[1].y),
+                        pack4_e4m3(f[2].x, f[2].y, f[3].x, f[3].y));
     } else if (grow && pos >= start && pos < from) {
       const uint2 c = *out;
       float u[4], v[4];

@@ -517,7 +517,8 @@ cudaError_t launch_attend_nt(const AttendParams& p, int sms, cudaStream_t s) {
 
 }  // namespace kv8
 
-size_t kv8_attend_workspace_bytes(int, int, int G, int n, int d, int sms) {
+size_t kv8_attend_workspace_bytes(int, int, int G, int n, int d, int cap, int sms) {
+  if (cap <= kv8::kAlignedCap) return 0;  // nothing to join
   const int64_t R = static_cast<int64_t>(G) * n;
   const int tile = kv8::rows_per_tile(R > 32 ? 32 : static_cast<int>(R));
   return static_cast<size_t>(2) * sms * kv8::kMostCtas * tile * (d + 2) * sizeof(float);

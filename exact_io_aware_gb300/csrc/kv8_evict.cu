@@ -21,8 +21,6 @@ namespace kv8 {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 
@@ -58,24 +56,32 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red) {
   }
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  const uint32_t w = lane < warp ? red[lane] : 0u;
+  const uint32_t w = lane < warp ? red[lane] : 0u;  // at most 32 warps
   return x - v + __reduce_add_sync(0xFFFFFFFFu, w);
 }
 
 struct SelectSmem {
   uint32_t hist[3][kBins];
-  uint32_t red[3][kSelWarps];
+  uint32_t red[3][32];
   uint32_t digit[3], left[3];
-  uint32_t above[kSelWarps], equal[kSelWarps];
+  uint32_t above[32], equal[32];
   uint32_t total[2];
 };
 
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p) {
+  constexpr int kSelWarps = kSelThreads / 32;
   __shared__ SelectSmem sm;
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int bh = blockIdx.x / ranks, b = bh / p.Hk, tid = threadIdx.x;
   const int lane = lane_id(), warp = warp_id();
+  auto sync_cluster = [&] {
+    if (ranks > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
   grid_launch_dependents();
   if (bh % p.Hk == 0 && rank == 0 && tid == 0) check_seq(p.lengths, nullptr, b, p.cap, 0, p.status);
   const int len = seq_len(p.lengths, b, p.cap);
@@ -104,22 +110,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
         atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
     }
-    cluster.sync();
-    // Thread t: the counts of the t-th pair of bins from the top, over the whole cluster.
-    uint32_t h0 = 0, h1 = 0;
-    const uint32_t top = bins - 1 - 2 * tid;
-    if (2 * tid < static_cast<int>(bins)) {
-      for (int r = 0; r < ranks; ++r) {
-        const uint32_t* rh = cluster.map_shared_rank(hist, r);
-        h0 += rh[top];
-        h1 += rh[top - 1];
-      }
+    sync_cluster();
+    // Thread t: the counts of its share of the bins, from the top, over the whole cluster.
+    constexpr int kMost = kBins / kSelThreads;
+    const int mine = pass == 2 ? kMost / 2 : kMost;
+    const uint32_t top = bins - 1 - mine * tid;
+    uint32_t h[kMost], sum = 0;
+#pragma unroll
+    for (int i = 0; i < mine; ++i) {
+      h[i] = hist[top - i];
+      for (int r = 1; r < ranks; ++r) h[i] += cluster.map_shared_rank(hist, (rank + r) % ranks)[top - i];
+      sum += h[i];
     }
-    const uint32_t ex = block_scan(h0 + h1, sm.red[pass]);
-    if (ex < left && left <= ex + h0 + h1) {
-      const bool second = left > ex + h0;
-      sm.digit[pass] = top - (second ? 1 : 0);
-      sm.left[pass] = left - ex - (second ? h0 : 0);
+    uint32_t ex = block_scan(sum, sm.red[pass]);
+#pragma unroll
+    for (int i = 0; i < mine; ++i) {
+      if (ex < left && left <= ex + h[i]) {
+        sm.digit[pass] = top - i;
+        sm.left[pass] = left - ex;
+      }
+      ex += h[i];
     }
     __syncthreads();
     if (want > 0) {
@@ -152,7 +162,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   }
   if (lane == 0) sm.above[warp] = na, sm.equal[warp] = ne;
   __syncthreads();
-  uint32_t xa = sm.above[lane], xe = sm.equal[lane];
+  uint32_t xa = lane < kSelWarps ? sm.above[lane] : 0u, xe = lane < kSelWarps ? sm.equal[lane] : 0u;
   uint32_t ab = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? xa : 0u);
   uint32_t eq = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? xe : 0u);
   if (warp == 0) {
@@ -160,7 +170,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     xe = __reduce_add_sync(0xFFFFFFFFu, xe);
     if (lane == 0) sm.total[0] = xa, sm.total[1] = xe;
   }
-  cluster.sync();
+  sync_cluster();
   for (int r = 0; r < rank; ++r) {
     const uint32_t* t = cluster.map_shared_rank(sm.total, r);
     ab += t[0];
@@ -177,7 +187,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     ab += __popc(ba);
     eq += __popc(be);
   }
-  cluster.sync();  // no CTA leaves while its counts may be read
+  if (ranks > 1) cluster.sync();  // no CTA leaves while its counts may be read
+}
+
+// Codes times scale / s as codes again: the general rule, for any scales.
+__device__ __forceinline__ uint32_t requantize4(uint32_t w, float scale, float inv) {
+  float x[4];
+  codes_to_float4(w, x);
+  return pack_codes(x[0] * scale * inv, x[1] * scale * inv, x[2] * scale * inv, x[3] * scale * inv);
+}
+// The same where scale / s is a power of two 2^-14 .. 2^15, given as two fp16 values: the product
+// is exact in fp16 wherever its E4M3 value is not zero, and rounds once.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, uint32_t ratio2) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c = h ? hi_codes(w) : lo_codes(w);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&ratio2));
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+    out |= static_cast<uint32_t>(e) << (16 * h);
+  }
+  return out;
 }
 
 template <int D>
@@ -185,12 +216,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
   constexpr int kLanes = D / 16;           // lanes of one row (16 codes each)
   constexpr int kRowsIt = 32 / kLanes;
   constexpr int kIters = 16 / kRowsIt;
-  __shared__ float red[kMoveThreads / 32];
+  __shared__ float red[2][kMoveThreads / 32];
   const int lane = lane_id(), warp = warp_id();
-  const int bh = blockIdx.y, b = bh / p.Hk, side = blockIdx.z;
+  const int bh = blockIdx.y, b = bh / p.Hk;
   const int live = min(seq_len(p.lengths, b, p.cap), p.keep);
   grid_dependency_wait();
-  if (blockIdx.x == 0 && side == 0 && bh % p.Hk == 0 && threadIdx.x == 0) p.lengths_out[b] = live;
+  if (blockIdx.x == 0 && bh % p.Hk == 0 && threadIdx.x == 0) p.lengths_out[b] = live;
   const int s0 = blockIdx.x * 128;
   if (s0 >= live) return;
   const int p0 = s0 + 16 * warp;
@@ -198,66 +229,96 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
   const int start = s0 + warp / wpb * p.block;
   const int sub = lane / kLanes, col = lane % kLanes * 16;
   const int32_t* kept = p.kept + static_cast<int64_t>(bh) * p.keep;
-  const uint8_t* src = (side ? p.codes[1] : p.codes[0]) + static_cast<int64_t>(bh) * p.cap * D;
-  const float* src_scale = (side ? p.scales[1] : p.scales[0]) + static_cast<int64_t>(bh) * (p.cap / p.block);
+  const int shift = 31 - __clz(p.block);
 
-  uint4 raw[kIters];
-  float sc[kIters];
-  float amax = 0.0f;
+  uint4 raw[2][kIters];
+  float sc[2][kIters];
+  {
+    const int from16 = p0 + (lane & 15) < live ? kept[p0 + (lane & 15)] : -1;
+    if (lane < 16 && from16 >= 0)
+      p.weights_out[static_cast<int64_t>(bh) * p.cap_out + p0 + lane] =
+          __ldg(p.weights + static_cast<int64_t>(bh) * p.cap + from16);
 #pragma unroll
-  for (int it = 0; it < kIters; ++it) {
-    const int pos = p0 + it * kRowsIt + sub;
-    raw[it] = make_uint4(0, 0, 0, 0);
-    sc[it] = 0.0f;
-    if (pos < live) {
-      const int from = kept[pos];
-      raw[it] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(from) * D + col));
-      sc[it] = __ldg(src_scale + from / p.block);
+    for (int it = 0; it < kIters; ++it) {
+      const int from = __shfl_sync(0xFFFFFFFFu, from16, it * kRowsIt + sub);
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        raw[side][it] = make_uint4(0, 0, 0, 0);
+        sc[side][it] = 0.0f;
+        if (from >= 0) {
+          const uint8_t* src = p.codes[side] + (static_cast<int64_t>(bh) * p.cap + from) * D + col;
+          raw[side][it] = __ldg(reinterpret_cast<const uint4*>(src));
+          sc[side][it] = __ldg(p.scales[side] + static_cast<int64_t>(bh) * (p.cap >> shift) + (from >> shift));
+        }
+      }
     }
   }
+  float amax[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int it = 0; it < kIters; ++it) {
-    const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+  for (int side = 0; side < 2; ++side)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x[4];
-      codes_to_float4(w[i], x);
+    for (int it = 0; it < kIters; ++it) {
+      // Magnitudes are ordered as their 7-bit codes, so the row piece's largest is found on bytes
+      // (0x7F, NaN, is looked at by value).
+      const uint4 u = raw[side][it];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, finite_abs(x[e] * sc[it]));
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(w[i] & 0x7F007F00u, (w[i] & 0x007F007Fu) << 8));
+      m = max(m >> 24, (m >> 8) & 0xFFu);
+      if (m == 0x7Fu) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          float x[4];
+          codes_to_float4(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w, x);
+          for (int e = 0; e < 4; ++e) amax[side] = fmaxf(amax[side], finite_abs(x[e] * sc[side][it]));
+        }
+      } else {
+        const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(m));
+        amax[side] = fmaxf(amax[side], finite_abs(__half2float(__ushort_as_half(h & 0xFFFFu)) * sc[side][it]));
+      }
     }
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    amax[side] = warp_max(amax[side]);
+    if (lane == 0) red[side][warp] = amax[side];
   }
-  amax = warp_max(amax);
-  if (lane == 0) red[warp] = amax;
   __syncthreads();
   if (start >= live) return;
   const int w0 = warp / wpb * wpb;
-  for (int w = w0; w < w0 + wpb; ++w) amax = fmaxf(amax, red[w]);
-  const float s = pow2(scale_exp(amax));
-  const float inv = 1.0f / s;
-  if (warp == w0 && lane == 0)
-    (side ? p.scales_out[1] : p.scales_out[0])[static_cast<int64_t>(bh) * (p.cap_out / p.block) + start / p.block] = s;
-  uint8_t* dst = (side ? p.codes_out[1] : p.codes_out[0]) + static_cast<int64_t>(bh) * p.cap_out * D;
 #pragma unroll
-  for (int it = 0; it < kIters; ++it) {
-    const int pos = p0 + it * kRowsIt + sub;
-    if (pos >= live) continue;
-    const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
-    uint32_t out[4];
+  for (int side = 0; side < 2; ++side) {
+    float a = amax[side];
+    for (int w = w0; w < w0 + wpb; ++w) a = fmaxf(a, red[side][w]);
+    const int e = scale_exp(a);
+    const float s = pow2(e), inv = pow2(-e);
+    if (warp == w0 && lane == 0)
+      p.scales_out[side][static_cast<int64_t>(bh) * (p.cap_out >> shift) + (start >> shift)] = s;
+    uint8_t* dst = p.codes_out[side] + static_cast<int64_t>(bh) * p.cap_out * D;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x[4];
-      codes_to_float4(w[i], x);
-      out[i] = pack_codes(x[0] * sc[it] * inv, x[1] * sc[it] * inv, x[2] * sc[it] * inv,
-                          x[3] * sc[it] * inv);
+    for (int it = 0; it < kIters; ++it) {
+      const int pos = p0 + it * kRowsIt + sub;
+      const float scale = sc[side][it];
+      // Both scales powers of two (mantissa zero) and their ratio within fp16: rescale4.  Scales
+      // past 2^118, whose values may pass float32's range, go by value.
+      const uint32_t su = __float_as_uint(scale);
+      const int k = static_cast<int>(su >> 23) - 127 - e;
+      const bool quick = (su & 0x7FFFFFu) == 0 && su < (245u << 23) && k >= -14 && k <= 15;
+      uint4 u = raw[side][it];
+      if (pos >= live) continue;
+      if (quick) {
+        if (k != 0) {
+          const uint32_t h = static_cast<uint32_t>(k + 15) << 10;  // 2^k
+          const uint32_t ratio2 = h | (h << 16);
+          u = make_uint4(rescale4(u.x, ratio2), rescale4(u.y, ratio2), rescale4(u.z, ratio2),
+                         rescale4(u.w, ratio2));
+        }
+      } else {
+        u = make_uint4(requantize4(u.x, scale, inv), requantize4(u.y, scale, inv),
+                       requantize4(u.z, scale, inv), requantize4(u.w, scale, inv));
+      }
+      *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(pos) * D + col) = u;
     }
-    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(pos) * D + col) =
-        make_uint4(out[0], out[1], out[2], out[3]);
-  }
-  if (side == 0) {
-    const int pos = p0 + lane;
-    if (lane < 16 && pos < live)
-      p.weights_out[static_cast<int64_t>(bh) * p.cap_out + pos] =
-          p.weights[static_cast<int64_t>(bh) * p.cap + kept[pos]];
   }
 }
 
@@ -272,6 +333,7 @@ int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s, std::string& err) {
   // CTAs of a head's cluster: doubled (to the portable 8) while a CTA has more than 4096 tokens
   // to look at and the clusters leave multiprocessors idle.
   const int heads = a.B * a.Hk;
+  const bool small = a.cap <= 4096;
   int ranks = 1;
   while (ranks < 8 && a.cap > 4096 * ranks && heads * ranks * 2 <= 2 * a.sms) ranks *= 2;
   cudaLaunchAttribute attr[1];
@@ -279,14 +341,15 @@ int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s, std::string& err) {
   attr[0].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads * ranks));
-  cfg.blockDim = dim3(kv8::kSelThreads);
+  cfg.blockDim = dim3(small ? 256 : 1024);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kv8::evict_select_kernel), args);
+  auto* select = small ? kv8::evict_select_kernel<256> : kv8::evict_select_kernel<1024>;
+  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(select), args);
   if (e == cudaSuccess) {
     const int most = a.keep < a.cap ? a.keep : a.cap;
-    const dim3 grid(static_cast<unsigned>((most + 127) / 128), static_cast<unsigned>(heads), 2);
+    const dim3 grid(static_cast<unsigned>((most + 127) / 128), static_cast<unsigned>(heads));
     auto* kernel = a.d == 128 ? kv8::evict_move_kernel<128> : kv8::evict_move_kernel<64>;
     e = kv8::launch_after(reinterpret_cast<const void*>(kernel), grid, dim3(kv8::kMoveThreads), args, s);
   }

@@ -292,7 +292,8 @@ int attn_fwd_kv8(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int
                  int mask_kind, void* o, float* lse, void* workspace, size_t workspace_bytes,
                  void* stream);
 
-/* Bytes of workspace attn_fwd_kv8 needs on the current device (0 for sizes it refuses). */
+/* Bytes of workspace attn_fwd_kv8 needs on the current device (0 for sizes that need none, and
+ * for sizes it refuses). */
 size_t attn_fwd_kv8_workspace_bytes(int dtype, int B, int H, int H_kv, int n_q, int d, int cap);
 
 /*
