@@ -17,6 +17,7 @@
 // each with its own z, l and m.  At the end of a tile the warps' states are merged; a tile that
 // one CTA holds whole is written at once, and a CTA's part of a tile shared with others (at most
 // one at each end of its run) goes to the workspace as (z, l, m), joined by a second kernel.
+#include "kv8_attend.cuh"
 #include "kv8_mma.cuh"
 
 namespace ea {
@@ -24,31 +25,10 @@ namespace kv8 {
 
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = kAttendWarps * 32;
-constexpr float kTop = 6.0f;     // log2 of the largest P when m is set
-constexpr float kRaise = 14.0f;  // a larger log2 P raises m
-constexpr float kNoMax = -3.0e38f;
 // A cache of at most this many tokens a sequence is not cut: each tile is one CTA's, and there is
 // nothing to join.
 constexpr int kAlignedCap = 512;
 constexpr int kMostCtas = 3;  // of any variant, on a multiprocessor
-
-struct AttendParams {
-  Geometry geo;
-  int block;
-  float c2;  // c log2(e)
-  const uint16_t* q;
-  const uint8_t* k8;
-  const uint8_t* v8;
-  const float* k_scales;
-  const float* v_scales;
-  uint16_t* o;
-  float* lse;
-  float* part_z;   // [2 ctas][tile][D]: parts of shared tiles, two places a CTA
-  float* part_lm;  // [2 ctas][tile][2]: their l and m
-  int ctas;        // runs the work is cut into; 0: one CTA a tile, and no parts
-  int min_chunks;  // a run has at least this many
-  uint32_t* status;
-};
 
 // CTAs resident on a multiprocessor (registers and shared memory are sized for them): while one
 // starts on a tile or merges its warps, the others stream.
@@ -69,28 +49,6 @@ constexpr int merge_stride() { return D + 4; }
 template <int D, int NT>
 constexpr size_t merge_bytes() {
   return static_cast<size_t>(kAttendWarps) * NT * 8 * (merge_stride<D>() + 2) * sizeof(float);
-}
-
-// Writes four columns of a finished row and, with the first of them, its LSE.  l = 0 is a row
-// that sees no key: O = 0, LSE = -inf.
-template <bool kBf16, int D>
-__device__ __forceinline__ void write_out(const AttendParams& p, int64_t row, int col, float4 z,
-                                          float l, float m, bool real) {
-  const bool none = l == 0.0f || !real;
-  const float inv = none ? 0.0f : 1.0f / l;
-  uint2 w;
-  if constexpr (kBf16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(z.x * inv, z.y * inv), b = __floats2bfloat162_rn(z.z * inv, z.w * inv);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    w = make_uint2(pack_f16(z.x * inv, z.y * inv), pack_f16(z.z * inv, z.w * inv));
-  }
-  if (none) w = make_uint2(0u, 0u);
-  *reinterpret_cast<uint2*>(p.o + row * D + col) = w;
-  if (col == 0) {
-    p.lse[row] = none ? -INFINITY : kLn2 * (m + log2f(l));
-    if (none && real) raise_empty_row(p.status);
-  }
 }
 
 // One chunk of 32 keys against the tile's rows.
@@ -229,12 +187,12 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
 
 template <bool kBf16, int D, int NT>
 __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
-    attend_kernel(const AttendParams p) {
+    attend_kernel(const AttendParams<ByQuery> p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kStages = attend_stages<D, NT>();
   constexpr int kTile = NT * 8;
   const int lane = lane_id(), warp = warp_id(), g = lane >> 2, t = lane & 3;
-  const Geometry& geo = p.geo;
+  const ByQuery& geo = p.geo;
   grid_launch_dependents();
   uint8_t* ring = smem + warp * (kStages * stage_bytes<D>());
   const int nblk = geo.cap / p.block;
@@ -252,12 +210,12 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
     pl.start = u0 = 0;
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
     pl.keys = tile_keys(geo, len, cnt, pl.rt);
-    u1 = chunks_of(pl.keys);
+    u1 = chunks_of(geo, pl.keys);
     if (pl.rt == 0 && pl.hk == 0 && threadIdx.x == 0)
       check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
   }
   for (;;) {
-    const int tile_chunks = chunks_of(pl.keys);
+    const int tile_chunks = chunks_of(geo, pl.keys);
     const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
     const int c1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(tile_chunks)));
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
@@ -299,7 +257,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
           const int r = pl.rt * kTile + j * 8 + g;
           float x[D / 4];
           load_q_row<kBf16, D>(
-              r < geo.R ? p.q + row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r) * D : nullptr, x);
+              r < geo.R ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
           if (pass) {
             pack_q<D>(x, qmul, q[j]);
           } else {
@@ -313,8 +271,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = pl.rt * kTile + j * 8 + 2 * t + c;
-          const bool real = r < geo.R && r / geo.G < cnt;
-          lim[j][c] = real ? row_keys(geo, len, cnt, r) : len;
+          const bool real = r < geo.R && geo.query(r) < cnt;
+          lim[j][c] = real ? query_keys(geo, len, cnt, geo.query(r)) : len;
           least = min(least, lim[j][c]);
         }
       least = __reduce_min_sync(0xFFFFFFFFu, least);
@@ -396,8 +354,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       const int r = pl.rt * kTile + row;
       if (whole) {
         if (r < geo.R)
-          write_out<kBf16, D>(p, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), col, zs, ls, mx,
-                              r / geo.G < cnt);
+          write_out<kBf16, D, ByQuery>(p, geo.row_offset(pl.b, pl.hk, r), col, zs, ls, mx,
+                              geo.query(r) < cnt);
       } else {
         *reinterpret_cast<float4*>(p.part_z + (slot + row) * D + col) = zs;
         if (col == 0) *reinterpret_cast<float2*>(p.part_lm + (slot + row) * 2) = make_float2(ls, mx);
@@ -409,89 +367,10 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
   }
 }
 
-// Joins the parts of tiles that several CTAs shared, and writes tiles that see no key at all.
-// One warp a row, eight rows a CTA.
-constexpr int kJoinWarps = 8;
-template <bool kBf16, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendParams p) {
-  constexpr int kCols = D / 32;  // columns of a lane
-  const Geometry& geo = p.geo;
-  int id = blockIdx.x;
-  Place pl;
-  pl.rt = id % geo.tiles;
-  id /= geo.tiles;
-  pl.hk = id % geo.Hk;
-  pl.b = id / geo.Hk;
-  const int lane = lane_id();
-  const int row = blockIdx.y * kJoinWarps + warp_id(), r = pl.rt * geo.tile + row;
-  const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
-  if (pl.rt == 0 && pl.hk == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-    check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
-  pl.keys = tile_keys(geo, len, cnt, pl.rt);
-  int64_t first = 0, last = 0;
-  if (pl.keys > 0) {
-    int64_t total;
-    locate(geo, pl, total);
-    const int64_t per = run_length(total, p.ctas, p.min_chunks);
-    first = pl.start / per;
-    last = (pl.start + chunks_of(pl.keys) - 1) / per;
-  }
-  grid_dependency_wait();  // by every warp: what follows on the stream may rely on this kernel
-  if (r >= geo.R || (pl.keys > 0 && first == last)) return;  // or one CTA held the tile whole
-  float mx = kNoMax, l = 0.0f;
-  float z[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
-  if (pl.keys > 0) {
-    // Place 1 of the first CTA (the tile starts there), place 0 of the others.
-    for (int64_t c0 = first; c0 <= last; c0 += 32) {
-      const int parts = static_cast<int>(min(last - c0 + 1, static_cast<int64_t>(32)));
-      float2 lm = make_float2(0.0f, kNoMax);
-      if (lane < parts) {
-        const int64_t slot = 2 * (c0 + lane) + (c0 + lane == first ? 1 : 0);
-        lm = *reinterpret_cast<const float2*>(p.part_lm + (slot * geo.tile + row) * 2);
-      }
-      const float mn = fmaxf(mx, warp_max(lm.y)), old = ex2(mx - mn);
-      mx = mn;
-      const float f = ex2(lm.y - mx);
-      float ls = f * lm.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
-      l = fmaf(l, old, ls);
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) z[i] *= old;
-#pragma unroll 4
-      for (int c = 0; c < parts; ++c) {
-        const int64_t slot = 2 * (c0 + c) + (c0 + c == first ? 1 : 0);
-        const float* src = p.part_z + (slot * geo.tile + row) * D + lane * kCols;
-        const float w = __shfl_sync(0xFFFFFFFFu, f, c);
-        if constexpr (kCols == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          z[0] = fmaf(w, x.x, z[0]), z[1] = fmaf(w, x.y, z[1]);
-          z[2] = fmaf(w, x.z, z[2]), z[3] = fmaf(w, x.w, z[3]);
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          z[0] = fmaf(w, x.x, z[0]), z[1] = fmaf(w, x.y, z[1]);
-        }
-      }
-    }
-  }
-  float4 out = make_float4(z[0], z[1], 0.0f, 0.0f);
-  if constexpr (kCols == 4) {
-    out.z = z[2], out.w = z[3];
-  } else {  // two lanes' columns make one store
-    out.z = __shfl_down_sync(0xFFFFFFFFu, z[0], 1);
-    out.w = __shfl_down_sync(0xFFFFFFFFu, z[1], 1);
-    if (lane & 1) return;
-  }
-  write_out<kBf16, D>(p, row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, r), lane * kCols, out, l, mx,
-                      r / geo.G < cnt);
-}
-
 inline int rows_per_tile(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 
 template <bool kBf16, int D, int NT>
-cudaError_t launch_attend(AttendParams p, int sms, cudaStream_t s) {
+cudaError_t launch_attend(AttendParams<ByQuery> p, int sms, cudaStream_t s) {
   constexpr size_t smem = ring_bytes<D, NT>() > merge_bytes<D, NT>() ? ring_bytes<D, NT>() : merge_bytes<D, NT>();
   auto* kernel = attend_kernel<kBf16, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -504,12 +383,11 @@ cudaError_t launch_attend(AttendParams p, int sms, cudaStream_t s) {
   e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(aligned ? tiles : p.ctas),
                        dim3(kAttendThreads), args, smem, s);
   if (e != cudaSuccess || aligned) return e;
-  return launch_after(reinterpret_cast<const void*>(attend_join_kernel<kBf16, D>),
-                      dim3(tiles, p.geo.tile / kJoinWarps), dim3(kJoinWarps * 32), args, s);
+  return launch_join<kBf16, D>(p, s);
 }
 
 template <bool kBf16, int D>
-cudaError_t launch_attend_nt(const AttendParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_attend_nt(const AttendParams<ByQuery>& p, int sms, cudaStream_t s) {
   if (p.geo.tile == 8) return launch_attend<kBf16, D, 1>(p, sms, s);
   if (p.geo.tile == 16) return launch_attend<kBf16, D, 2>(p, sms, s);
   return launch_attend<kBf16, D, 4>(p, sms, s);
@@ -517,17 +395,26 @@ cudaError_t launch_attend_nt(const AttendParams& p, int sms, cudaStream_t s) {
 
 }  // namespace kv8
 
+// Rows per key/value head up to which the mma.sync kernel is used (see the measurements above).
+constexpr int kFewRows = 32;
+
 size_t kv8_attend_workspace_bytes(int, int, int G, int n, int d, int cap, int sms) {
-  if (cap <= kv8::kAlignedCap) return 0;  // nothing to join
   const int64_t R = static_cast<int64_t>(G) * n;
-  const int tile = kv8::rows_per_tile(R > 32 ? 32 : static_cast<int>(R));
-  return static_cast<size_t>(2) * sms * kv8::kMostCtas * tile * (d + 2) * sizeof(float);
+  size_t rows = 0;  // of the parts: two places a CTA
+  if (R > kFewRows)
+    rows = static_cast<size_t>(2) * sms * kTcTileRows;
+  else if (cap > kv8::kAlignedCap)
+    rows = static_cast<size_t>(2) * sms * kv8::kMostCtas * kv8::rows_per_tile(static_cast<int>(R));
+  return rows * (d + 2) * sizeof(float);
 }
 
-int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
-  kv8::AttendParams p{};
-  const int R = a.G * a.n, tile = kv8::rows_per_tile(R);
-  p.geo = {a.B, a.Hk, a.G, a.n, a.cap, R, tile, (R + tile - 1) / tile, a.causal, a.lengths, a.counts, false};
+namespace {
+
+template <class Geo>
+kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int tile, int ctas) {
+  kv8::AttendParams<Geo> p{};
+  const int R = a.G * a.n;
+  p.geo = {{a.B, a.Hk, a.G, a.n, a.cap, R, tile, (R + tile - 1) / tile, a.causal, a.lengths, a.counts, false}};
   p.block = a.block;
   p.c2 = a.c * kv8::kLog2e;
   p.q = static_cast<const uint16_t*>(a.q);
@@ -538,14 +425,32 @@ int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   p.o = static_cast<uint16_t*>(a.o);
   p.lse = a.lse;
   p.part_z = static_cast<float*>(a.workspace);
-  p.part_lm = p.part_z + static_cast<size_t>(2) * a.sms * kv8::kMostCtas * tile * a.d;
-  p.min_chunks = 2 * kv8::kAttendWarps;
+  p.part_lm = p.part_z + static_cast<size_t>(2) * ctas * tile * a.d;
+  p.ctas = ctas;
   p.status = a.status;
+  return p;
+}
+
+}  // namespace
+
+int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
+  const int64_t R = static_cast<int64_t>(a.G) * a.n;
   cudaError_t e;
-  if (a.bf16)
-    e = a.d == 128 ? kv8::launch_attend_nt<true, 128>(p, a.sms, s) : kv8::launch_attend_nt<true, 64>(p, a.sms, s);
-  else
-    e = a.d == 128 ? kv8::launch_attend_nt<false, 128>(p, a.sms, s) : kv8::launch_attend_nt<false, 64>(p, a.sms, s);
+  if (R > kFewRows) {
+    auto p = attend_params<kv8::ByHead>(a, kTcTileRows, a.sms);
+    p.min_chunks = 2;
+    if (a.bf16)
+      e = a.d == 128 ? launch_kv8_tc<true, 128>(p, s) : launch_kv8_tc<true, 64>(p, s);
+    else
+      e = a.d == 128 ? launch_kv8_tc<false, 128>(p, s) : launch_kv8_tc<false, 64>(p, s);
+  } else {
+    auto p = attend_params<kv8::ByQuery>(a, kv8::rows_per_tile(static_cast<int>(R)), kv8::kMostCtas * a.sms);
+    p.min_chunks = 2 * kv8::kAttendWarps;
+    if (a.bf16)
+      e = a.d == 128 ? kv8::launch_attend_nt<true, 128>(p, a.sms, s) : kv8::launch_attend_nt<true, 64>(p, a.sms, s);
+    else
+      e = a.d == 128 ? kv8::launch_attend_nt<false, 128>(p, a.sms, s) : kv8::launch_attend_nt<false, 64>(p, a.sms, s);
+  }
   if (e != cudaSuccess) {
     err = std::string("kv8 attention launch: ") + cudaGetErrorString(e);
     return -5;

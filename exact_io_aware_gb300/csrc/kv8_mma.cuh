@@ -14,12 +14,10 @@
 //   * slot s of a group of 8 keys is key key_of_slot(s);
 //   * of V it holds columns D/8 g .. of the rows of slots 2t, 2t + 1, 2t + 8, 2t + 9.
 #pragma once
-#include "kv8_common.cuh"
+#include "kv8_plan.cuh"
 
 namespace ea {
 namespace kv8 {
-
-constexpr int kChunk = 32;  // keys of a warp's step
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -97,12 +95,6 @@ struct QFrag {
   uint32_t b[D / 16][2];
 };
 
-// Row r of a key/value head is query i = r / G of head g = r % G.  Returns the row's offset in
-// q and o, [B][Hk G][n][D], in rows.
-__device__ __forceinline__ int64_t row_offset(int b, int hk, int Hk, int G, int n, int r) {
-  return (static_cast<int64_t>(b) * Hk * G + static_cast<int64_t>(hk) * G + r % G) * n + r / G;
-}
-
 // The lane's share of row `row` (null: zeros): columns 64 h + 16 t .. + 15 of each half h.
 template <bool kBf16, int D>
 __device__ __forceinline__ void load_q_row(const uint16_t* row, float (&x)[D / 4]) {
@@ -165,135 +157,6 @@ __device__ __forceinline__ void scores16(const uint8_t* kbase, int mt, const QFr
       for (int j = 0; j < NT; ++j)
         mma_f16(acc[j], a0, a1, a2, a3, q[j].b[h * 4 + s][0], q[j].b[h * 4 + s][1]);
     }
-  }
-}
-
-// Which keys the rows of a tile see, and the tile's place in the work list.
-struct Geometry {
-  int B, Hk, G, n, cap, R, tile, tiles;  // R = G n rows in tiles of `tile`
-  bool causal;
-  const int32_t* lengths;
-  const int32_t* counts;
-  bool all_keys;  // the work list covers every held key, not only those some row sees
-};
-
-// Keys row r sees: 0 for a padding row.
-__device__ __forceinline__ int row_keys(const Geometry& g, int len, int cnt, int r) {
-  const int i = r / g.G;
-  if (i >= cnt) return 0;
-  return g.causal ? min(max(len - cnt + i + 1, 0), len) : len;
-}
-// Keys any row of row tile rt sees (rows are ordered by query, so it is the last real row's).
-__device__ __forceinline__ int tile_keys(const Geometry& g, int len, int cnt, int rt) {
-  if (g.all_keys) return len;
-  const int first = rt * g.tile / g.G;
-  if (first >= cnt) return 0;
-  const int last = min((min((rt + 1) * g.tile, g.R) - 1) / g.G, cnt - 1);
-  return g.causal ? min(max(len - cnt + last + 1, 0), len) : len;
-}
-__device__ __forceinline__ int chunks_of(int keys) { return (keys + kChunk - 1) / kChunk; }
-
-// Chunks of all row tiles of one head of sequence b.
-__device__ __forceinline__ int64_t head_chunks(const Geometry& g, int b) {
-  const int len = seq_len(g.lengths, b, g.cap), cnt = seq_count(g.counts, b, g.n);
-  if (g.tiles == 1) return chunks_of(tile_keys(g, len, cnt, 0));
-  int64_t u = 0;
-  for (int rt = 0; rt < g.tiles; ++rt) u += chunks_of(tile_keys(g, len, cnt, rt));
-  return u;
-}
-
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-// The work list is every chunk of every (sequence, head, row tile), in that order.  It is cut
-// into equal runs, one a CTA, whatever the sequences' lengths.
-struct Place {
-  int b, hk, rt;
-  int keys;       // keys of the tile
-  int64_t start;  // work-list index of the tile's first chunk
-};
-
-__device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int min_chunks) {
-  const int64_t per = (total + ctas - 1) / ctas;
-  return per < min_chunks ? min_chunks : per;
-}
-
-// The run of CTA `cta` (u0 .. u1 - 1, empty for u0 >= u1) and the tile u0 lies in.  Executed by
-// whole warps; lanes take a sequence each.
-__device__ __forceinline__ Place plan_run(const Geometry& g, int cta, int ctas, int min_chunks,
-                                          int64_t& u0, int64_t& u1) {
-  const int lane = lane_id();
-  const int64_t v0 = lane < g.B ? head_chunks(g, lane) * g.Hk : 0;
-  int64_t sum = v0;
-  for (int b = lane + 32; b < g.B; b += 32) sum += head_chunks(g, b) * g.Hk;
-  const int64_t total = warp_sum(sum);
-  const int64_t per = run_length(total, ctas, min_chunks);
-  u0 = cta * per;
-  u1 = min(u0 + per, total);
-  Place p{0, 0, 0, 0, 0};
-  if (u0 >= u1) return p;
-  int64_t base = 0, head = 0;
-  for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int64_t v = b0 == 0 ? v0 : b0 + lane < g.B ? head_chunks(g, b0 + lane) * g.Hk : 0;
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + x > u0);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      p.b = b0 + l;
-      head = __shfl_sync(0xFFFFFFFFu, v, l) / g.Hk;
-      base += __shfl_sync(0xFFFFFFFFu, x - v, l);
-      break;
-    }
-    base += __shfl_sync(0xFFFFFFFFu, x, 31);
-  }
-  const int len = seq_len(g.lengths, p.b, g.cap), cnt = seq_count(g.counts, p.b, g.n);
-  p.hk = static_cast<int>((u0 - base) / head);
-  base += p.hk * head;
-  for (;; ++p.rt) {
-    p.keys = tile_keys(g, len, cnt, p.rt);
-    const int c = chunks_of(p.keys);
-    if (u0 < base + c || p.rt + 1 >= g.tiles) break;
-    base += c;
-  }
-  p.start = base;
-  return p;
-}
-
-// Work-list index of the first chunk of tile p, and the list's length.  Executed by whole warps.
-__device__ __forceinline__ void locate(const Geometry& g, Place& p, int64_t& total) {
-  int64_t before = 0, all = 0;
-  for (int b = lane_id(); b < g.B; b += 32) {
-    const int64_t u = head_chunks(g, b);
-    all += u;
-    if (b < p.b) before += u;
-  }
-  total = g.Hk * warp_sum(all);
-  p.start = g.Hk * warp_sum(before) + p.hk * head_chunks(g, p.b);
-  const int len = seq_len(g.lengths, p.b, g.cap), cnt = seq_count(g.counts, p.b, g.n);
-  for (int rt = 0; rt < p.rt; ++rt) p.start += chunks_of(tile_keys(g, len, cnt, rt));
-}
-
-// The next tile of the list with at least one chunk (the caller knows that there is one).
-__device__ __forceinline__ void next_place(const Geometry& g, Place& p) {
-  p.start += chunks_of(p.keys);
-  for (;;) {
-    if (++p.rt == g.tiles) {
-      p.rt = 0;
-      if (++p.hk == g.Hk) {
-        p.hk = 0;
-        if (++p.b == g.B) return;
-      }
-    }
-    p.keys = tile_keys(g, seq_len(g.lengths, p.b, g.cap), seq_count(g.counts, p.b, g.n), p.rt);
-    if (p.keys > 0) return;
   }
 }
 

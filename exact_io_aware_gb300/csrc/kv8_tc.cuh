@@ -1,0 +1,588 @@
+// Attention of many query rows over the 8-bit cache, on the tcgen05 tensor cores.
+//
+// The mathematics is that of kv8_attend.cu: in base 2, x_rj = log2(e) s_rj + log2(vs_j),
+// P_rj = 2^{x_rj - m_r} rounded to fp16, z = P V on the codes, l = sum P / vs.  Codes are widened
+// to fp16 on the way into shared memory (exact), queries enter as fp16 times a power of two of
+// their row, so both products are kind::f16 with float32 accumulation.
+//
+// One CTA holds a tile of 256 rows of a key/value head as two of 128 (rows ordered by head, so they
+// lie in a row in memory) and walks its run's blocks of 128 keys.  Warpgroups:
+//   0  warps 0, 1: MMA issuers of the two row tiles
+//   1, 2  softmax of row tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant)
+//   3  converters: read codes from global memory a block ahead into registers (and ask L2 for
+//      the blocks after that), widen them and write the swizzled K and V tiles, two stages each
+// Per block j each issuer does P V_{j-1}, then S_j = Q K_j^T, so the tensor core works on one row
+// tile while the other's softmax runs (the arrangement of fwd_tc.cuh).  S and P share TMEM
+// columns; O stays in TMEM for the length of a tile.
+//
+// The registers of 512 threads are dealt again: softmax holds a row's 128 scores, the issuers
+// need few (kRegs*: their sum over the warpgroups is what the block was launched with).
+#pragma once
+#include "kv8_attend.cuh"
+#include "tile.cuh"
+
+namespace ea {
+namespace kv8 {
+namespace tc {
+
+constexpr int kRows = 128;   // of a row tile
+constexpr int kTileRows = kTcTileRows;
+constexpr int kThreads = 512;
+constexpr int kStages = 2;   // of the K and the V tiles
+constexpr int kGroups = kBlockKeys / 16;  // scale groups of a block
+constexpr int kPrefetch = 4;
+constexpr int kRegsIssue = 56, kRegsSoftmax = 176, kRegsConvert = 104;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128, "more registers than launched");
+
+template <int D>
+struct Config {
+  using TQ = Tile<kRows, D>;
+  using TK = Tile<kBlockKeys, D>;
+  static constexpr int kOffK = 2 * TQ::kBytes;
+  static constexpr int kOffV = kOffK + kStages * TK::kBytes;
+  static constexpr int kBytes = kOffV + kStages * TK::kBytes;
+  static constexpr size_t kSmem = kBytes + 1024;
+};
+
+struct Scales {  // of one block, per 16 keys
+  float k[kGroups], log2_v[kGroups], inv_v[kGroups];
+};
+
+struct Shared {
+  uint64_t q_full, q_free;
+  uint64_t s_full[2], p_full[2], o_done[2], o_read[2];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint32_t tmem_base;
+  uint32_t nan_seen[4];             // by tile number mod 4: a masked block's V held NaN codes
+                                    // (cleared two tiles ahead, where its last reader is done)
+  float row_mul[2][kTileRows];      // by tile number mod 2: |c| log2(e) over the row's power of two
+  Scales scales[4];                 // by block number mod 4
+};
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// One tile of the run, as every role sees it.
+struct Seg {
+  int b, hk, len, cnt;
+  int r0;            // first row
+  int j0, steps;     // first block and number of blocks
+  bool whole;        // the tile is this CTA's alone
+  int slot;          // else where its part goes
+  int reach[2];      // blocks row tile t takes, counted from block 0
+  int least[2];      // keys every real row of row tile t sees (blocks past them are masked)
+};
+
+__device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t u0, int64_t u1, int cta) {
+  Seg s;
+  s.b = pl.b, s.hk = pl.hk;
+  s.len = seq_len(g.lengths, pl.b, g.cap);
+  s.cnt = seq_count(g.counts, pl.b, g.n);
+  s.r0 = pl.rt * kTileRows;
+  const int blocks = chunks_of(g, pl.keys);
+  s.j0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
+  const int j1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(blocks)));
+  s.steps = j1 - s.j0;
+  s.whole = s.j0 == 0 && j1 == blocks;
+  s.slot = 2 * cta + (s.j0 == 0 ? 1 : 0);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int a = s.r0 + t * kRows, z = min(a + kRows, g.R);
+    int lo, hi;
+    const bool any = a < g.R && g.span(a, z, s.cnt, lo, hi);
+    s.reach[t] = any ? chunks_of(g, query_keys(g, s.len, s.cnt, hi)) : 0;
+    s.least[t] = any ? query_keys(g, s.len, s.cnt, lo) : s.len;
+  }
+  return s;
+}
+
+// Sixteen codes to sixteen fp16 values.
+__device__ __forceinline__ void widen16(uint4 u, uint4& a, uint4& b) {
+  a = make_uint4(lo_codes(u.x), hi_codes(u.x), lo_codes(u.y), hi_codes(u.y));
+  b = make_uint4(lo_codes(u.z), hi_codes(u.z), lo_codes(u.w), hi_codes(u.w));
+}
+
+// A thread's pieces of one block of codes: rows (it 128 + tid) / (D / 16), zeros from key `len` on.
+template <int D>
+struct Pieces {
+  static constexpr int kN = D / 16;
+  uint4 u[kN];
+  __device__ __forceinline__ void load(const uint8_t* head, int key0, int len, int tid) {
+#pragma unroll
+    for (int it = 0; it < kN; ++it) {
+      const int idx = it * 128 + tid, key = key0 + idx / kN;
+      u[it] = make_uint4(0, 0, 0, 0);
+      if (key < len)
+        u[it] = __ldg(reinterpret_cast<const uint4*>(head + static_cast<int64_t>(key) * D + idx % kN * 16));
+    }
+  }
+  // Widened into a swizzled tile.  The two 16-byte halves of a piece are written in an order that
+  // alternates between the halves of a row, which keeps eight lanes' stores on different banks.
+  __device__ __forceinline__ void store(uint8_t* tile, int tid) const {
+    using T = Tile<kBlockKeys, D>;
+#pragma unroll
+    for (int it = 0; it < kN; ++it) {
+      const int idx = it * 128 + tid, row = idx / kN, col = idx % kN * 16;
+      uint4 a, b;
+      widen16(u[it], a, b);
+      const bool swap = (idx & 4) != 0;
+      *reinterpret_cast<uint4*>(tile + T::offset(row, col + (swap ? 8 : 0))) = swap ? b : a;
+      *reinterpret_cast<uint4*>(tile + T::offset(row, col + (swap ? 0 : 8))) = swap ? a : b;
+    }
+  }
+  // Takes NaN codes out (to 0); true if there were any.
+  __device__ __forceinline__ bool drop_nan() {
+    bool any = false;
+#pragma unroll
+    for (int it = 0; it < kN; ++it) {
+      uint32_t* w[4] = {&u[it].x, &u[it].y, &u[it].z, &u[it].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t bad = __vcmpeq4(*w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        any |= bad != 0;
+        *w[i] &= ~bad;
+      }
+    }
+    return any;
+  }
+};
+
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams<ByHead> p) {
+  using C = Config<D>;
+  using TQ = typename C::TQ;
+  using TK = typename C::TK;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+  __shared__ Shared sh;
+  const int warp = warp_id(), lane = lane_id(), group = warp >> 2;
+  const ByHead& geo = p.geo;
+  grid_launch_dependents();
+  int64_t u0, u1;
+  Place pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+  if (u0 >= u1) return;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.q_free, 2);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_full[t], 4);
+      mbar_init(&sh.o_done[t], 1);
+      mbar_init(&sh.o_read[t], 4);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sh.k_full[s], 4);
+      mbar_init(&sh.v_full[s], 4);
+      mbar_init(&sh.k_empty[s], 2);
+      mbar_init(&sh.v_empty[s], 2);
+    }
+    for (int i = 0; i < 4; ++i) sh.nan_seen[i] = 0;
+    fence_barrier_init();
+  }
+  constexpr uint32_t kTmem = 512;
+  if (warp == 0) tmem_alloc(&sh.tmem_base, kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;  // S_t (and P_t) at 128 t, O_t at 256 + D t
+
+  if (group == 0) {
+    regs_dec<kRegsIssue>();
+    if (warp < 2) {
+      // ------------------------------------------------------------ MMA issuer of row tile t
+      const int t = warp;
+      constexpr uint32_t id_s = idesc_f16(128, kBlockKeys, 0, 0, 0);
+      constexpr uint32_t id_o = idesc_f16(128, D, 0, 0, 1);
+      constexpr uint64_t kStage = TK::kBytes >> 4;
+      const uint64_t dq = TQ::desc_k(smem_u32(sQ + t * TQ::kBytes), 0);
+      const uint64_t dk0 = TK::desc_k(smem_u32(sK), 0);
+      const uint64_t dv0 = TK::desc_mn(smem_u32(sV), 0);
+      const uint32_t tS = tmem + t * kBlockKeys, tO = tmem + 2 * kBlockKeys + t * D;
+      uint32_t gi = 0, pph = 0;  // blocks before this tile; parity of the next p_full phase
+      // Tiles in which this row tile takes no block have no o_done and o_read phases.
+      uint32_t rph = 0;
+      bool owed = false, ok = true;  // the tile before's O is still to be read
+      for (int seg = 0; ok; ++seg) {
+        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+        const int reach = t ? sg.reach[1] : sg.reach[0];
+        ok = mbar_wait_warp(&sh.q_full, seg & 1, p.status, 0x21);
+        bool pend = false, started = false;
+        for (int i = 0; i <= sg.steps && ok; ++i) {
+          const uint32_t cur_i = gi + i, prev_i = cur_i - 1;
+          if (i > 0) {
+            ok = mbar_wait_warp(&sh.v_full[prev_i % kStages], (prev_i / kStages) & 1, p.status, 0x22);
+            if (!ok) break;
+          }
+          const bool cur = i < sg.steps && sg.j0 + i < reach;
+          if (i < sg.steps) {
+            ok = mbar_wait_warp(&sh.k_full[cur_i % kStages], (cur_i / kStages) & 1, p.status, 0x23);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          if (pend) {
+            ok = mbar_wait_warp(&sh.p_full[t], pph, p.status, 0x24);
+            if (!ok) break;
+            pph ^= 1u;
+            tc_fence_after();
+            const uint64_t dv = dv0 + (prev_i % kStages) * kStage;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kBlockKeys / 16; ++kk)
+                mma_ts(tO, tS + kk * 8, dv + TK::mn_step(kk), id_o, (started || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+            started = true;
+          }
+          if (cur) {
+            const uint64_t dk = dk0 + (cur_i % kStages) * kStage;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tS, dq + TQ::k_step(kk), dk + TK::k_step(kk), id_s, kk > 0 ? 1u : 0u);
+              mma_commit(&sh.s_full[t]);
+            }
+            __syncwarp();
+          }
+          if (i + 1 == sg.steps && owed) {
+            // Q is released for the next tile only when this row tile's last O has been read, so
+            // what softmax holds by tile number stays at most two tiles behind the converters.
+            ok = mbar_wait_warp(&sh.o_read[t], rph, p.status, 0x25);
+            if (!ok) break;
+            rph ^= 1u;
+            owed = false;
+          }
+          if (elect_one()) {
+            if (i < sg.steps) mma_commit(&sh.k_empty[cur_i % kStages]);
+            if (i + 1 == sg.steps) mma_commit(&sh.q_free);
+            if (i > 0) mma_commit(&sh.v_empty[prev_i % kStages]);
+          }
+          __syncwarp();
+          pend = cur;
+        }
+        if (!ok) break;
+        if (started) {
+          if (elect_one()) mma_commit(&sh.o_done[t]);
+          __syncwarp();
+          owed = true;
+        }
+        gi += sg.steps;
+        if (pl.start + chunks_of(geo, pl.keys) >= u1) break;
+        next_place(geo, pl);
+      }
+    }
+  } else if (group == 3) {
+    // ---------------------------------------------------------------- converters
+    regs_dec<kRegsConvert>();
+    const int tid = threadIdx.x - 3 * 128;
+    const int nblk = geo.cap / p.block;
+    const bool negative = p.c2 < 0.0f;
+    const float c2 = fabsf(p.c2);
+    uint32_t gi = 0;
+    for (int seg = 0;; ++seg) {
+      const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+      const int64_t bh = static_cast<int64_t>(sg.b) * geo.Hk + sg.hk;
+      const uint8_t* kp = p.k8 + bh * geo.cap * D;
+      const uint8_t* vp = p.v8 + bh * geo.cap * D;
+      const float* ksp = p.k_scales + bh * nblk;
+      const float* vsp = p.v_scales + bh * nblk;
+      const int least = min(sg.least[0], sg.least[1]);
+      Pieces<D> kx, vx;
+      kx.load(kp, sg.j0 * kBlockKeys, sg.len, tid);
+      bool ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
+      if (!ok) break;
+      if (tid == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
+      // Queries: D / 8 lanes a row.  Real rows of the tile only; the others are zeros.
+      {
+        constexpr int kLanes = D / 8, kIt = kTileRows * kLanes / 128;
+        const uint16_t* qp = p.q + (bh * geo.R + sg.r0) * D;
+        const int rows = min(kTileRows, geo.R - sg.r0);
+#pragma unroll 4
+        for (int it = 0; it < kIt; ++it) {
+          const int idx = it * 128 + tid, row = idx / kLanes, col = idx % kLanes * 8;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (row < rows) u = __ldg(reinterpret_cast<const uint4*>(qp + static_cast<int64_t>(row) * D + col));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          float x[8], amax = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack16<kBf16>(w[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          // The row's largest value becomes 2^14 .. 2^15, as in the kernel for few rows.
+          const int e = min(max(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), -100), 100);
+          const float mul = negative ? -pow2(e) : pow2(e);
+          uint4 h = make_uint4(pack2<false>(x[0] * mul, x[1] * mul), pack2<false>(x[2] * mul, x[3] * mul),
+                               pack2<false>(x[4] * mul, x[5] * mul), pack2<false>(x[6] * mul, x[7] * mul));
+          *reinterpret_cast<uint4*>(sQ + row / kRows * TQ::kBytes + TQ::offset(row % kRows, col)) = h;
+          if (idx % kLanes == 0) sh.row_mul[seg & 1][row] = c2 * pow2(-e);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+      }
+      // K_0, K_1, V_0, K_2, V_1, ...: each block's codes are loaded while the item before waits for
+      // its stage.
+      auto put_k = [&](int i) -> bool {
+        const uint32_t c = gi + i;
+        if (!mbar_wait_warp(&sh.k_empty[c % kStages], ((c / kStages) & 1) ^ 1, p.status, 0x27)) return false;
+        if (tid == 0 && i + kPrefetch < sg.steps) {
+          const int key0 = (sg.j0 + i + kPrefetch) * kBlockKeys;
+          const uint32_t bytes = min(kBlockKeys, sg.len - key0) * D;
+          prefetch_l2(kp + static_cast<int64_t>(key0) * D, bytes);
+          prefetch_l2(vp + static_cast<int64_t>(key0) * D, bytes);
+        }
+        if (tid < kGroups) {
+          const int key = (sg.j0 + i) * kBlockKeys + tid * 16;
+          const bool in = key < sg.len;
+          const float vs = in ? __ldg(vsp + key / p.block) : 1.0f;
+          Scales& sc = sh.scales[c & 3];
+          sc.k[tid] = in ? __ldg(ksp + key / p.block) : 1.0f;
+          sc.log2_v[tid] = log2f(vs);
+          sc.inv_v[tid] = 1.0f / vs;
+        }
+        kx.store(sK + (c % kStages) * TK::kBytes, tid);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full[c % kStages]);
+        return true;
+      };
+      auto put_v = [&](int i) -> bool {
+        const uint32_t c = gi + i;
+        if (!mbar_wait_warp(&sh.v_empty[c % kStages], ((c / kStages) & 1) ^ 1, p.status, 0x28)) return false;
+        if ((sg.j0 + i + 1) * kBlockKeys > least && vx.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
+        vx.store(sV + (c % kStages) * TK::kBytes, tid);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full[c % kStages]);
+        return true;
+      };
+      vx.load(vp, sg.j0 * kBlockKeys, sg.len, tid);
+      ok = put_k(0);
+      for (int i = 0; i < sg.steps && ok; ++i) {
+        if (i + 1 < sg.steps) {
+          kx.load(kp, (sg.j0 + i + 1) * kBlockKeys, sg.len, tid);
+          ok = put_k(i + 1);
+          if (!ok) break;
+        }
+        ok = put_v(i);
+        if (i + 1 < sg.steps) vx.load(vp, (sg.j0 + i + 1) * kBlockKeys, sg.len, tid);
+      }
+      gi += sg.steps;
+      if (!ok || pl.start + chunks_of(geo, pl.keys) >= u1) break;
+      next_place(geo, pl);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax of row tile t
+    regs_inc<kRegsSoftmax>();
+    const int t = group - 1, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + t * kBlockKeys + lane_off, tO = tmem + 2 * kBlockKeys + t * D + lane_off;
+    uint32_t gi = 0, s_phase = 0, o_phase = 0;
+    bool ok = true;
+    for (int seg = 0;; ++seg) {
+      const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+      const int row = sg.r0 + t * kRows + r;
+      const int query = geo.query(row < geo.R ? row : 0);
+      const bool real = row < geo.R && query < sg.cnt;
+      const int lim = real ? query_keys(geo, sg.len, sg.cnt, query) : sg.len;
+      const int reach = t ? sg.reach[1] : sg.reach[0], least = t ? sg.least[1] : sg.least[0];
+      const int steps = min(sg.steps, reach - sg.j0);  // the row tile's share, maybe none
+      float m = kNoMax, l = 0.0f, mul = 0.0f;
+      bool first = true;
+      for (int i = 0; i < steps; ++i) {
+        ok = mbar_wait_warp(&sh.s_full[t], s_phase, p.status, 0x29);
+        if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        if (first) mul = sh.row_mul[seg & 1][t * kRows + r];
+        const Scales& sc = sh.scales[(gi + i) & 3];
+        const int key0 = (sg.j0 + i) * kBlockKeys;
+        float sv[kBlockKeys];
+        {
+          uint32_t rr[kBlockKeys];
+#pragma unroll
+          for (int c0 = 0; c0 < kBlockKeys; c0 += 32)
+            tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(rr + c0));
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kBlockKeys; ++k) sv[k] = __uint_as_float(rr[k]);
+        }
+        if (__builtin_expect(key0 + kBlockKeys > least, 0)) {
+          const int seen = lim - key0;
+#pragma unroll
+          for (int k = 0; k < kBlockKeys; ++k)
+            if (k >= seen) sv[k] = -INFINITY;
+        }
+        // Largest x of the row: the scores' factor is uniform and positive in a scale group.
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          float a = fmax3(sv[16 * g], sv[16 * g + 1], sv[16 * g + 2]);
+          float b = fmax3(sv[16 * g + 3], sv[16 * g + 4], sv[16 * g + 5]);
+          a = fmax3(a, sv[16 * g + 6], sv[16 * g + 7]);
+          b = fmax3(b, sv[16 * g + 8], sv[16 * g + 9]);
+          a = fmax3(a, sv[16 * g + 10], sv[16 * g + 11]);
+          b = fmax3(b, sv[16 * g + 12], sv[16 * g + 13]);
+          a = fmax3(a, sv[16 * g + 14], sv[16 * g + 15]);
+          // a factor of 0 (c = 0) would turn masked scores to NaN
+          mx = fmaxf(mx, fmaf(fmaxf(a, b), fmaxf(sc.k[g] * mul, 1.17549435e-38f), sc.log2_v[g]));
+        }
+        float alpha = 1.0f;
+        if (mx - m > kRaise) {
+          const float mn = mx - kTop;
+          alpha = ex2(m - mn);
+          m = mn;
+          l *= alpha;
+        }
+        if (__builtin_expect(!first && __any_sync(0xFFFFFFFFu, alpha != 1.0f), 0)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t rr[16];
+            tmem_ld16(tO + c0, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) rr[k] = __float_as_uint(__uint_as_float(rr[k]) * alpha);
+            tmem_st16(tO + c0, rr);
+          }
+        }
+        first = false;
+#pragma unroll
+        for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int g = c0 / 16 + h;
+            const float f = fmaxf(sc.k[g] * mul, 1.17549435e-38f), shift = sc.log2_v[g] - m;
+            float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float p0 = ex2(fmaf(sv[c0 + 16 * h + 2 * k], f, shift));
+              const float p1 = ex2(fmaf(sv[c0 + 16 * h + 2 * k + 1], f, shift));
+              a0 += p0;
+              a1 += p1;
+              pk[8 * h + k] = pack2<false>(p0, p1);
+            }
+            l = fmaf(a0 + a1, sc.inv_v[g], l);
+          }
+          tmem_st16(tS + c0 / 2, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+      if (!ok) break;
+      const bool have = steps > 0;
+      if (have) {
+        ok = mbar_wait_warp(&sh.o_done[t], o_phase, p.status, 0x2A);
+        if (!ok) break;
+        o_phase ^= 1u;
+        tc_fence_after();
+      }
+      // A masked block's V held NaN codes, which were kept out of the product: the columns of the
+      // keys this row sees are NaN.
+      uint32_t bad[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) bad[i] = 0;
+      if (__builtin_expect(have && sh.nan_seen[seg & 3] != 0, 0)) {
+        const int all = min(sg.least[0], sg.least[1]);
+        const int k0 = max(all / kBlockKeys, sg.j0) * kBlockKeys;
+        const int k1 = min(lim, (sg.j0 + sg.steps) * kBlockKeys);
+        const uint32_t* vw = reinterpret_cast<const uint32_t*>(
+            p.v8 + ((static_cast<int64_t>(sg.b) * geo.Hk + sg.hk) * geo.cap) * D);
+        for (int key = k0; key < k1; ++key)
+          for (int w = 0; w < D / 4; ++w) {
+            const uint32_t x = __ldg(vw + static_cast<int64_t>(key) * (D / 4) + w);
+            const uint32_t eq = __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & 0x08040201u;
+            bad[w / 8] |= ((eq | eq >> 8 | eq >> 16 | eq >> 24) & 0xFu) << (4 * (w % 8));
+          }
+      }
+      const bool write = row < geo.R;
+      const int64_t orow = geo.row_offset(sg.b, sg.hk, row);
+      const int64_t prow = static_cast<int64_t>(sg.slot) * kTileRows + t * kRows + r;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t rr[32];
+        __syncwarp();
+        if (have) {
+          tmem_ld32(tO + c0, rr);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) rr[k] = 0u;
+        }
+        if (bad[c0 / 32]) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (bad[c0 / 32] >> k & 1u) rr[k] = 0x7FC00000u;
+        }
+        if (write) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 z = make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]),
+                                         __uint_as_float(rr[k + 2]), __uint_as_float(rr[k + 3]));
+            if (sg.whole)
+              write_out<kBf16, D, ByHead>(p, orow, c0 + k, z, l, m, real);
+            else
+              *reinterpret_cast<float4*>(p.part_z + prow * D + c0 + k) = z;
+          }
+        }
+      }
+      if (have) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_read[t]);
+      }
+      if (write && !sg.whole) *reinterpret_cast<float2*>(p.part_lm + prow * 2) = make_float2(l, m);
+      gi += sg.steps;
+      if (pl.start + chunks_of(geo, pl.keys) >= u1) break;
+      next_place(geo, pl);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+}  // namespace tc
+}  // namespace kv8
+
+template <bool kBf16, int D>
+cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
+  auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D>;
+  constexpr size_t smem = kv8::tc::Config<D>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  // The registers dealt inside the kernel are those it is launched with: were a compiler to give
+  // it fewer, the warpgroups that ask for more would wait for ever.
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return e;
+  if (4 * attr.numRegs < kv8::tc::kRegsIssue + 2 * kv8::tc::kRegsSoftmax + kv8::tc::kRegsConvert)
+    return cudaErrorInvalidConfiguration;
+  void* args[] = {&p};
+  e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas), dim3(kv8::tc::kThreads), args,
+                       smem, s);
+  if (e != cudaSuccess) return e;
+  return kv8::launch_join<kBf16, D>(p, s);
+}
+
+}  // namespace ea

@@ -18,7 +18,7 @@ constexpr int kWeightsStages = 4;
 constexpr int kWeightsRows = 128;  // rows held in shared memory at once
 
 struct WeightsParams {
-  Geometry geo;  // one tile of all rows
+  ByQuery geo;  // one tile of all rows
   int block;
   float c2;
   const uint16_t* q;
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 2) weights_kernel(const Weigh
   extern __shared__ __align__(128) uint8_t smem_raw[];
   WeightsSmem<D>& sm = *reinterpret_cast<WeightsSmem<D>*>(smem_raw);
   const int lane = lane_id(), warp = warp_id(), g = lane >> 2, t = lane & 3;
-  const Geometry& geo = p.geo;
+  const ByQuery& geo = p.geo;
   int64_t u0, u1;
   Place pl = plan_run(geo, blockIdx.x, gridDim.x, 1, u0, u1);
   if (blockIdx.x == 0)
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 2) weights_kernel(const Weigh
   const int nblk = geo.cap / p.block;
 
   for (;;) {
-    const int tile_chunks = chunks_of(pl.keys);
+    const int tile_chunks = chunks_of(geo, pl.keys);
     const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
     const int c1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(tile_chunks)));
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
@@ -94,13 +94,13 @@ __global__ void __launch_bounds__(kWeightsThreads, 2) weights_kernel(const Weigh
       float amax = 0.0f, qmul = 1.0f;
       for (int pass = 0; pass < 2; ++pass) {
         for (int r = warp; r < blocks * 8; r += kWeightsWarps) {
-          const bool real = r < rows && (rbase + r) / geo.G < cnt;
+          const bool real = r < rows && geo.query(rbase + r) < cnt;
           float x[kPer];
           int64_t off = 0;
 #pragma unroll
           for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
           if (real) {
-            off = row_offset(pl.b, pl.hk, geo.Hk, geo.G, geo.n, rbase + r);
+            off = geo.row_offset(pl.b, pl.hk, rbase + r);
 #pragma unroll
             for (int e = 0; e < kPer / 2; ++e) {
               const float2 f = unpack16<kBf16>(
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 2) weights_kernel(const Weigh
               const float lse = real ? p.lse[off] : -INFINITY;
               const bool counts = lse != -INFINITY;
               sm.lse2[r] = counts ? lse * kLog2e : INFINITY;
-              sm.lim[r] = real && counts ? row_keys(geo, len, cnt, rbase + r) : 0;
+              sm.lim[r] = real && counts ? query_keys(geo, len, cnt, geo.query(rbase + r)) : 0;
             }
           }
         }
@@ -245,7 +245,7 @@ int launch_kv8_weights(const Kv8Args& a, cudaStream_t s, std::string& err) {
   kv8::WeightsParams p{};
   const int R = a.G * a.n;
   // Every held key is on the work list, so that the sums of keys no row sees are carried over.
-  p.geo = {a.B, a.Hk, a.G, a.n, a.cap, R, R, 1, a.causal, a.lengths, a.counts, true};
+  p.geo = {{a.B, a.Hk, a.G, a.n, a.cap, R, R, 1, a.causal, a.lengths, a.counts, true}};
   p.block = a.block;
   p.c2 = a.c * kv8::kLog2e;
   p.q = static_cast<const uint16_t*>(a.q);
