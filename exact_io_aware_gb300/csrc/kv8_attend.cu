@@ -437,7 +437,9 @@ int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   const int64_t R = static_cast<int64_t>(a.G) * a.n;
   cudaError_t e;
   if (R > kFewRows) {
-    auto p = attend_params<kv8::ByHead>(a, kTcTileRows, a.sms);
+    // Two places a CTA for tiles of 256 rows; for 128, two and one for what tile 1 hands over.
+    auto p = attend_params<kv8::ByHead>(a, R > kTcTileRows / 2 ? kTcTileRows : kTcTileRows / 2, a.sms);
+    p.part_lm = p.part_z + static_cast<size_t>(2) * a.sms * kTcTileRows * a.d;
     p.min_chunks = 2;
     if (a.bf16)
       e = a.d == 128 ? launch_kv8_tc<true, 128>(p, s) : launch_kv8_tc<true, 64>(p, s);

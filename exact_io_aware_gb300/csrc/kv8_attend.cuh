@@ -86,13 +86,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
   if (pl.keys > 0) {
     // Place 1 of the first CTA (the tile starts there), place 0 of the others.
-    for (int64_t c0 = first; c0 <= last; c0 += 32) {
-      const int parts = static_cast<int>(min(last - c0 + 1, static_cast<int64_t>(32)));
+    const int64_t all = last - first + 1;
+    auto place = [&](int64_t q) { return (2 * (first + q) + (q == 0 ? 1 : 0)) * geo.tile + row; };
+    for (int64_t q0 = 0; q0 < all; q0 += 32) {
+      const int parts = static_cast<int>(min(all - q0, static_cast<int64_t>(32)));
       float2 lm = make_float2(0.0f, kNoMax);
-      if (lane < parts) {
-        const int64_t slot = 2 * (c0 + lane) + (c0 + lane == first ? 1 : 0);
-        lm = *reinterpret_cast<const float2*>(p.part_lm + (slot * geo.tile + row) * 2);
-      }
+      if (lane < parts) lm = *reinterpret_cast<const float2*>(p.part_lm + place(q0 + lane) * 2);
       const float mn = fmaxf(mx, warp_max(lm.y)), old = ex2(mx - mn);
       mx = mn;
       const float f = ex2(lm.y - mx);
@@ -104,8 +103,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
       for (int i = 0; i < kCols; ++i) z[i] *= old;
 #pragma unroll 4
       for (int c = 0; c < parts; ++c) {
-        const int64_t slot = 2 * (c0 + c) + (c0 + c == first ? 1 : 0);
-        const float* src = p.part_z + (slot * geo.tile + row) * D + lane * kCols;
+        const float* src = p.part_z + place(q0 + c) * D + lane * kCols;
         const float w = __shfl_sync(0xFFFFFFFFu, f, c);
         if constexpr (kCols == 4) {
           const float4 x = *reinterpret_cast<const float4*>(src);
@@ -141,7 +139,8 @@ cudaError_t launch_join(AttendParams<Geo>& p, cudaStream_t s) {
 
 }  // namespace kv8
 
-// Attention of many rows on the tcgen05 tensor cores (kv8_tc_*.cu), in tiles of 256 rows.
+// Attention of many rows on the tcgen05 tensor cores (kv8_tc_*.cu), in tiles of 256 rows, or of 128
+// where a head has no more.
 constexpr int kTcTileRows = 256;
 template <bool kBf16, int D>
 cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s);

@@ -1,47 +1,56 @@
 // Attention of many query rows over the 8-bit cache, on the tcgen05 tensor cores.
 //
 // The mathematics is that of kv8_attend.cu: in base 2, x_rj = log2(e) s_rj + log2(vs_j),
-// P_rj = 2^{x_rj - m_r} rounded to fp16, z = P V on the codes, l = sum P / vs.  Codes are widened
-// to fp16 on the way into shared memory (exact), queries enter as fp16 times a power of two of
-// their row, so both products are kind::f16 with float32 accumulation.
+// P_rj = 2^{x_rj - m_r} rounded to fp16, z = P V on the codes, l = sum P / vs.
+//   * S = Q K^T is kind::f8f6f4 on the codes as they lie in memory.  A query row over a power of
+//     two (its largest value 224 .. 448) is a sum of E4M3 terms, q = q1 + q2 (+ q3): each term
+//     takes four significant bits and leaves a remainder of at most half a step, so two terms
+//     hold the 8 bits of a bf16 value and three the 11 of an fp16 one, exactly for values down
+//     to 2^-10 (fp16: 2^-7) of the row's largest; below, what is lost is under 2^-18 of the
+//     largest.  The terms' products add up in one float32 accumulator, and two of them cost what
+//     one product on 16-bit operands would.
+//   * P V is kind::f16: V's codes are widened to fp16 on the way into shared memory (exact).
 //
-// One CTA holds a tile of 256 rows of a key/value head as two of 128 (rows ordered by head, so they
-// lie in a row in memory) and walks its run's blocks of 128 keys.  Warpgroups:
-//   0  warps 0, 1: MMA issuers of the two row tiles
-//   1, 2  softmax of row tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant)
-//   3  converters: read codes from global memory a block ahead into registers (and ask L2 for
-//      the blocks after that), widen them and write the swizzled K and V tiles, two stages each
-// Per block j each issuer does P V_{j-1}, then S_j = Q K_j^T, so the tensor core works on one row
-// tile while the other's softmax runs (the arrangement of fwd_tc.cuh).  S and P share TMEM
-// columns; O stays in TMEM for the length of a tile.
+// One CTA walks its run's blocks of 128 keys with two row tiles of 128 (rows ordered by head, so
+// they lie in a row in memory): rows r0 .. and r0 + 128 .. of the same head, or, for heads of at
+// most 128 rows, the same rows twice, one tile taking the even blocks and the other the odd ones;
+// tile 1 then hands its state to tile 0 (through L2) at the end.  Either way the tensor core works on one
+// tile while the other's softmax runs.  Warpgroups:
+//   0  warps 0, 1: MMA issuers of the two tiles (per block j: P V of the block before, then
+//      S_j); warp 2: TMA producer of K tiles (swizzled) and of raw V blocks
+//   1, 2  softmax of tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant)
+//   3  converters: queries into their terms, raw V blocks into fp16 tiles
+// S and P share TMEM columns; O stays in TMEM for the length of a tile.
 //
-// The registers of 512 threads are dealt again: softmax holds a row's 128 scores, the issuers
+// The registers of 512 threads are dealt again: softmax holds a row's 128 scores, the others
 // need few (kRegs*: their sum over the warpgroups is what the block was launched with).
 #pragma once
 #include "kv8_attend.cuh"
 #include "tile.cuh"
+#include "tmap.h"
 
 namespace ea {
 namespace kv8 {
 namespace tc {
 
 constexpr int kRows = 128;   // of a row tile
-constexpr int kTileRows = kTcTileRows;
 constexpr int kThreads = 512;
-constexpr int kStages = 2;   // of the K and the V tiles
 constexpr int kGroups = kBlockKeys / 16;  // scale groups of a block
-constexpr int kPrefetch = 4;
-constexpr int kRegsIssue = 56, kRegsSoftmax = 176, kRegsConvert = 104;
+constexpr int kRegsIssue = 56, kRegsSoftmax = 192, kRegsConvert = 72;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128, "more registers than launched");
 
-template <int D>
+template <bool kBf16, int D>
 struct Config {
-  using TQ = Tile<kRows, D>;
-  using TK = Tile<kBlockKeys, D>;
-  static constexpr int kOffK = 2 * TQ::kBytes;
-  static constexpr int kOffV = kOffK + kStages * TK::kBytes;
-  static constexpr int kBytes = kOffV + kStages * TK::kBytes;
-  static constexpr size_t kSmem = kBytes + 1024;
+  using T8 = Tile<kRows, D / 2>;        // 128 rows of D bytes, as D / 2 16-bit columns
+  using TV = Tile<kBlockKeys, D>;       // fp16
+  static constexpr int kTerms = kBf16 ? 2 : 3;
+  static constexpr int kSK = 2, kSV = 2;  // stages of K tiles and of V tiles
+  static constexpr int kSR = kBf16 ? 3 : 2;  // of raw V blocks
+  static constexpr int kRaw = kBlockKeys * D;
+  static constexpr int kOffK = 2 * kTerms * T8::kBytes;  // Q: [tile][term]
+  static constexpr int kOffV = kOffK + kSK * T8::kBytes;
+  static constexpr int kOffR = kOffV + kSV * TV::kBytes;
+  static constexpr int kOffShared = kOffR + kSR * kRaw;
 };
 
 struct Scales {  // of one block, per 16 keys
@@ -49,13 +58,13 @@ struct Scales {  // of one block, per 16 keys
 };
 
 struct Shared {
-  uint64_t q_full, q_free;
+  uint64_t q_full, q_free, h_full, h_free;
   uint64_t s_full[2], p_full[2], o_done[2], o_read[2];
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], r_full[3], r_empty[3], sc_full[4];
   uint32_t tmem_base;
   uint32_t nan_seen[4];             // by tile number mod 4: a masked block's V held NaN codes
                                     // (cleared two tiles ahead, where its last reader is done)
-  float row_mul[2][kTileRows];      // by tile number mod 2: |c| log2(e) over the row's power of two
+  float row_mul[2][2 * kRows];      // by tile number mod 2: |c| log2(e) times the row's power of two
   Scales scales[4];                 // by block number mod 4
 };
 
@@ -63,10 +72,6 @@ template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 
 // One tile of the run, as every role sees it.
 struct Seg {
@@ -84,7 +89,7 @@ __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t
   s.b = pl.b, s.hk = pl.hk;
   s.len = seq_len(g.lengths, pl.b, g.cap);
   s.cnt = seq_count(g.counts, pl.b, g.n);
-  s.r0 = pl.rt * kTileRows;
+  s.r0 = pl.rt * g.tile;
   const int blocks = chunks_of(g, pl.keys);
   s.j0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
   const int j1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(blocks)));
@@ -93,7 +98,7 @@ __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t
   s.slot = 2 * cta + (s.j0 == 0 ? 1 : 0);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int a = s.r0 + t * kRows, z = min(a + kRows, g.R);
+    const int a = s.r0 + (g.tile > kRows ? t * kRows : 0), z = min(a + kRows, g.R);
     int lo, hi;
     const bool any = a < g.R && g.span(a, z, s.cnt, lo, hi);
     s.reach[t] = any ? chunks_of(g, query_keys(g, s.len, s.cnt, hi)) : 0;
@@ -108,18 +113,18 @@ __device__ __forceinline__ void widen16(uint4 u, uint4& a, uint4& b) {
   b = make_uint4(lo_codes(u.z), hi_codes(u.z), lo_codes(u.w), hi_codes(u.w));
 }
 
-// A thread's pieces of one block of codes: rows (it 128 + tid) / (D / 16), zeros from key `len` on.
+// A converter thread's pieces of one raw block: 16 codes of row (it 128 + tid) / (D / 16).
 template <int D>
 struct Pieces {
   static constexpr int kN = D / 16;
   uint4 u[kN];
-  __device__ __forceinline__ void load(const uint8_t* head, int key0, int len, int tid) {
+  // Rows from `rows` on, which the copy did not bring, are zeros.
+  __device__ __forceinline__ void load(const uint8_t* raw, int rows, int tid) {
 #pragma unroll
     for (int it = 0; it < kN; ++it) {
-      const int idx = it * 128 + tid, key = key0 + idx / kN;
-      u[it] = make_uint4(0, 0, 0, 0);
-      if (key < len)
-        u[it] = __ldg(reinterpret_cast<const uint4*>(head + static_cast<int64_t>(key) * D + idx % kN * 16));
+      const int idx = it * 128 + tid;
+      u[it] = *reinterpret_cast<const uint4*>(raw + idx * 16);
+      if (idx / kN >= rows) u[it] = make_uint4(0, 0, 0, 0);
     }
   }
   // Widened into a swizzled tile.  The two 16-byte halves of a piece are written in an order that
@@ -154,39 +159,54 @@ struct Pieces {
 };
 
 template <bool kBf16, int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams<ByHead> p) {
-  using C = Config<D>;
-  using TQ = typename C::TQ;
-  using TK = typename C::TK;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const AttendParams<ByHead> p) {
+  using C = Config<kBf16, D>;
+  using T8 = typename C::T8;
+  using TV = typename C::TV;
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sV = smem + C::kOffV;
-  __shared__ Shared sh;
+  uint8_t* sR = smem + C::kOffR;
+  Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffShared);
   const int warp = warp_id(), lane = lane_id(), group = warp >> 2;
   const ByHead& geo = p.geo;
+  const bool split = geo.tile == kRows;  // the two tiles are the same rows, of alternate blocks
   grid_launch_dependents();
   int64_t u0, u1;
   Place pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
   if (u0 >= u1) return;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it
+    if (threadIdx.x == 0) raise_timeout(p.status, 0x20);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.q_full, 4);
     mbar_init(&sh.q_free, 2);
+    mbar_init(&sh.h_full, 4);
+    mbar_init(&sh.h_free, 4);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
       mbar_init(&sh.p_full[t], 4);
       mbar_init(&sh.o_done[t], 1);
       mbar_init(&sh.o_read[t], 4);
     }
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh.k_full[s], 4);
-      mbar_init(&sh.v_full[s], 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.k_full[s], 1);
       mbar_init(&sh.k_empty[s], 2);
+      mbar_init(&sh.v_full[s], 4);
       mbar_init(&sh.v_empty[s], 2);
     }
-    for (int i = 0; i < 4; ++i) sh.nan_seen[i] = 0;
+    for (int s = 0; s < C::kSR; ++s) {
+      mbar_init(&sh.r_full[s], 1);
+      mbar_init(&sh.r_empty[s], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.sc_full[i], 1);
+      sh.nan_seen[i] = 0;
+    }
     fence_barrier_init();
   }
   constexpr uint32_t kTmem = 512;
@@ -201,12 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     if (warp < 2) {
       // ------------------------------------------------------------ MMA issuer of row tile t
       const int t = warp;
-      constexpr uint32_t id_s = idesc_f16(128, kBlockKeys, 0, 0, 0);
+      constexpr uint32_t id_s = idesc_e4m3(128, kBlockKeys);
       constexpr uint32_t id_o = idesc_f16(128, D, 0, 0, 1);
-      constexpr uint64_t kStage = TK::kBytes >> 4;
-      const uint64_t dq = TQ::desc_k(smem_u32(sQ + t * TQ::kBytes), 0);
-      const uint64_t dk0 = TK::desc_k(smem_u32(sK), 0);
-      const uint64_t dv0 = TK::desc_mn(smem_u32(sV), 0);
+      const uint64_t dq = T8::desc_k(smem_u32(sQ + (split ? 0 : t) * C::kTerms * T8::kBytes), 0);
+      const uint64_t dk0 = T8::desc_k(smem_u32(sK), 0);
+      const uint64_t dv0 = TV::desc_mn(smem_u32(sV), 0);
       const uint32_t tS = tmem + t * kBlockKeys, tO = tmem + 2 * kBlockKeys + t * D;
       uint32_t gi = 0, pph = 0;  // blocks before this tile; parity of the next p_full phase
       // Tiles in which this row tile takes no block have no o_done and o_read phases.
@@ -220,12 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         for (int i = 0; i <= sg.steps && ok; ++i) {
           const uint32_t cur_i = gi + i, prev_i = cur_i - 1;
           if (i > 0) {
-            ok = mbar_wait_warp(&sh.v_full[prev_i % kStages], (prev_i / kStages) & 1, p.status, 0x22);
+            ok = mbar_wait_warp(&sh.v_full[prev_i & 1], (prev_i >> 1) & 1, p.status, 0x22);
             if (!ok) break;
           }
-          const bool cur = i < sg.steps && sg.j0 + i < reach;
+          const bool cur = i < sg.steps && (split ? ((sg.j0 + i) & 1) == t : sg.j0 + i < reach);
           if (i < sg.steps) {
-            ok = mbar_wait_warp(&sh.k_full[cur_i % kStages], (cur_i / kStages) & 1, p.status, 0x23);
+            ok = mbar_wait_warp(&sh.k_full[cur_i & 1], (cur_i >> 1) & 1, p.status, 0x23);
             if (!ok) break;
           }
           tc_fence_after();
@@ -234,21 +253,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             if (!ok) break;
             pph ^= 1u;
             tc_fence_after();
-            const uint64_t dv = dv0 + (prev_i % kStages) * kStage;
+            const uint64_t dv = dv0 + (prev_i & 1) * static_cast<uint64_t>(TV::kBytes >> 4);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kBlockKeys / 16; ++kk)
-                mma_ts(tO, tS + kk * 8, dv + TK::mn_step(kk), id_o, (started || kk > 0) ? 1u : 0u);
+                mma_ts(tO, tS + kk * 8, dv + TV::mn_step(kk), id_o, (started || kk > 0) ? 1u : 0u);
             }
             __syncwarp();
             started = true;
           }
           if (cur) {
-            const uint64_t dk = dk0 + (cur_i % kStages) * kStage;
+            const uint64_t dk = dk0 + (cur_i & 1) * static_cast<uint64_t>(T8::kBytes >> 4);
             if (elect_one()) {
+              // a step is 32 codes: 32 bytes, as 16 of the tile's 16-bit columns
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                mma_ss(tS, dq + TQ::k_step(kk), dk + TK::k_step(kk), id_s, kk > 0 ? 1u : 0u);
+              for (int term = 0; term < C::kTerms; ++term)
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                  mma_ss_f8(tS, dq + term * static_cast<uint64_t>(T8::kBytes >> 4) + T8::k_step(kk),
+                            dk + T8::k_step(kk), id_s, (term > 0 || kk > 0) ? 1u : 0u);
               mma_commit(&sh.s_full[t]);
             }
             __syncwarp();
@@ -262,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             owed = false;
           }
           if (elect_one()) {
-            if (i < sg.steps) mma_commit(&sh.k_empty[cur_i % kStages]);
+            if (i < sg.steps) mma_commit(&sh.k_empty[cur_i & 1]);
             if (i + 1 == sg.steps) mma_commit(&sh.q_free);
-            if (i > 0) mma_commit(&sh.v_empty[prev_i % kStages]);
+            if (i > 0) mma_commit(&sh.v_empty[prev_i & 1]);
           }
           __syncwarp();
           pend = cur;
@@ -279,6 +302,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (pl.start + chunks_of(geo, pl.keys) >= u1) break;
         next_place(geo, pl);
       }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ TMA producer
+      uint32_t gi = 0;
+      bool ok = true;
+      for (;;) {
+        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+        const int bh = sg.b * geo.Hk + sg.hk;
+        for (int i = 0; i < sg.steps && ok; ++i) {
+          const uint32_t c = gi + i, rs = c % C::kSR;
+          const int key0 = (sg.j0 + i) * kBlockKeys;
+          ok = mbar_wait_warp(&sh.k_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x27);
+          if (!ok) break;
+          if (lane == 0) {  // rows past the cache read as zeros, those past the length are masked
+            mbar_arrive_expect_tx(&sh.k_full[c & 1], T8::kBytes);
+            tma_load_3d(sK + (c & 1) * T8::kBytes, &tm_k, &sh.k_full[c & 1], 0, key0, bh);
+          }
+          ok = mbar_wait_warp(&sh.r_empty[rs], ((c / C::kSR) & 1) ^ 1, p.status, 0x28);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bytes = min(kBlockKeys, sg.len - key0) * D;
+            mbar_arrive_expect_tx(&sh.r_full[rs], bytes);
+            bulk_load(sR + rs * C::kRaw, p.v8 + (static_cast<int64_t>(bh) * geo.cap + key0) * D, bytes,
+                      &sh.r_full[rs]);
+          }
+          __syncwarp();
+        }
+        gi += sg.steps;
+        if (!ok || pl.start + chunks_of(geo, pl.keys) >= u1) break;
+        next_place(geo, pl);
+      }
     }
   } else if (group == 3) {
     // ---------------------------------------------------------------- converters
@@ -291,23 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     for (int seg = 0;; ++seg) {
       const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
       const int64_t bh = static_cast<int64_t>(sg.b) * geo.Hk + sg.hk;
-      const uint8_t* kp = p.k8 + bh * geo.cap * D;
-      const uint8_t* vp = p.v8 + bh * geo.cap * D;
       const float* ksp = p.k_scales + bh * nblk;
       const float* vsp = p.v_scales + bh * nblk;
       const int least = min(sg.least[0], sg.least[1]);
-      Pieces<D> kx, vx;
-      kx.load(kp, sg.j0 * kBlockKeys, sg.len, tid);
       bool ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
       if (!ok) break;
       if (tid == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
-      // Queries: D / 8 lanes a row.  Real rows of the tile only; the others are zeros.
+      // Queries: D / 8 lanes a row; rows past the head's last are zeros.
       {
-        constexpr int kLanes = D / 8, kIt = kTileRows * kLanes / 128;
+        constexpr int kLanes = D / 8;
         const uint16_t* qp = p.q + (bh * geo.R + sg.r0) * D;
-        const int rows = min(kTileRows, geo.R - sg.r0);
+        const int rows = min(geo.tile, geo.R - sg.r0), its = geo.tile * kLanes / 128;
 #pragma unroll 4
-        for (int it = 0; it < kIt; ++it) {
+        for (int it = 0; it < its; ++it) {
           const int idx = it * 128 + tid, row = idx / kLanes, col = idx % kLanes * 8;
           uint4 u = make_uint4(0, 0, 0, 0);
           if (row < rows) u = __ldg(reinterpret_cast<const uint4*>(qp + static_cast<int64_t>(row) * D + col));
@@ -321,64 +370,71 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           }
 #pragma unroll
           for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-          // The row's largest value becomes 2^14 .. 2^15, as in the kernel for few rows.
-          const int e = min(max(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), -100), 100);
-          const float mul = negative ? -pow2(e) : pow2(e);
-          uint4 h = make_uint4(pack2<false>(x[0] * mul, x[1] * mul), pack2<false>(x[2] * mul, x[3] * mul),
-                               pack2<false>(x[4] * mul, x[5] * mul), pack2<false>(x[6] * mul, x[7] * mul));
-          *reinterpret_cast<uint4*>(sQ + row / kRows * TQ::kBytes + TQ::offset(row % kRows, col)) = h;
-          if (idx % kLanes == 0) sh.row_mul[seg & 1][row] = c2 * pow2(-e);
+          const int e = scale_exp(amax);
+          const float mul = negative ? -pow2(-e) : pow2(-e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = nan_unless_finite(x[i]) * mul;
+          uint8_t* dst = sQ + row / kRows * C::kTerms * T8::kBytes + T8::offset(row % kRows, col / 2);
+#pragma unroll
+          for (int term = 0; term < C::kTerms; ++term) {
+            const uint2 c = make_uint2(pack4_e4m3(x[0], x[1], x[2], x[3]), pack4_e4m3(x[4], x[5], x[6], x[7]));
+            *reinterpret_cast<uint2*>(dst + term * T8::kBytes) = c;
+            float y[4], z[4];
+            codes_to_float4(c.x, y);
+            codes_to_float4(c.y, z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] -= y[i], x[4 + i] -= z[i];  // exact
+          }
+          if (idx % kLanes == 0) sh.row_mul[seg & 1][row] = c2 * pow2(e);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
       }
-      // K_0, K_1, V_0, K_2, V_1, ...: each block's codes are loaded while the item before waits for
-      // its stage.
-      auto put_k = [&](int i) -> bool {
-        const uint32_t c = gi + i;
-        if (!mbar_wait_warp(&sh.k_empty[c % kStages], ((c / kStages) & 1) ^ 1, p.status, 0x27)) return false;
-        if (tid == 0 && i + kPrefetch < sg.steps) {
-          const int key0 = (sg.j0 + i + kPrefetch) * kBlockKeys;
-          const uint32_t bytes = min(kBlockKeys, sg.len - key0) * D;
-          prefetch_l2(kp + static_cast<int64_t>(key0) * D, bytes);
-          prefetch_l2(vp + static_cast<int64_t>(key0) * D, bytes);
+      // Scales of block i by the first warp, written a block ahead of V.  The place's last readers
+      // were softmax four blocks ago, which P V of two blocks ago (v_empty) came after.
+      float ks = 1.0f, vs = 1.0f;
+      auto fetch_scales = [&](int i) {
+        const int key = (sg.j0 + i) * kBlockKeys + tid * 16;
+        ks = vs = 1.0f;
+        if (tid < kGroups && key < sg.len) {
+          ks = __ldg(ksp + key / p.block);
+          vs = __ldg(vsp + key / p.block);
         }
+      };
+      auto put_scales = [&](int i) {
+        const uint32_t c = gi + i;
         if (tid < kGroups) {
-          const int key = (sg.j0 + i) * kBlockKeys + tid * 16;
-          const bool in = key < sg.len;
-          const float vs = in ? __ldg(vsp + key / p.block) : 1.0f;
           Scales& sc = sh.scales[c & 3];
-          sc.k[tid] = in ? __ldg(ksp + key / p.block) : 1.0f;
+          sc.k[tid] = ks;
           sc.log2_v[tid] = log2f(vs);
           sc.inv_v[tid] = 1.0f / vs;
         }
-        kx.store(sK + (c % kStages) * TK::kBytes, tid);
+        __syncwarp();
+        if (tid == 0) mbar_arrive(&sh.sc_full[c & 3]);
+      };
+      if (warp == 12) {
+        fetch_scales(0);
+        put_scales(0);
+      }
+      for (int i = 0; i < sg.steps; ++i) {
+        const uint32_t c = gi + i, rs = c % C::kSR;
+        const int key0 = (sg.j0 + i) * kBlockKeys;
+        if (warp == 12 && i + 1 < sg.steps) fetch_scales(i + 1);
+        Pieces<D> x;
+        ok = mbar_wait_warp(&sh.r_full[rs], (c / C::kSR) & 1, p.status, 0x2B);
+        if (!ok) break;
+        x.load(sR + rs * C::kRaw, sg.len - key0, tid);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.r_empty[rs]);
+        if (key0 + kBlockKeys > least && x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
+        ok = mbar_wait_warp(&sh.v_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x2C);
+        if (!ok) break;
+        if (warp == 12 && i + 1 < sg.steps) put_scales(i + 1);
+        x.store(sV + (c & 1) * TV::kBytes, tid);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full[c % kStages]);
-        return true;
-      };
-      auto put_v = [&](int i) -> bool {
-        const uint32_t c = gi + i;
-        if (!mbar_wait_warp(&sh.v_empty[c % kStages], ((c / kStages) & 1) ^ 1, p.status, 0x28)) return false;
-        if ((sg.j0 + i + 1) * kBlockKeys > least && vx.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
-        vx.store(sV + (c % kStages) * TK::kBytes, tid);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[c % kStages]);
-        return true;
-      };
-      vx.load(vp, sg.j0 * kBlockKeys, sg.len, tid);
-      ok = put_k(0);
-      for (int i = 0; i < sg.steps && ok; ++i) {
-        if (i + 1 < sg.steps) {
-          kx.load(kp, (sg.j0 + i + 1) * kBlockKeys, sg.len, tid);
-          ok = put_k(i + 1);
-          if (!ok) break;
-        }
-        ok = put_v(i);
-        if (i + 1 < sg.steps) vx.load(vp, (sg.j0 + i + 1) * kBlockKeys, sg.len, tid);
+        if (lane == 0) mbar_arrive(&sh.v_full[c & 1]);
       }
       gi += sg.steps;
       if (!ok || pl.start + chunks_of(geo, pl.keys) >= u1) break;
@@ -390,25 +446,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     const int t = group - 1, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + t * kBlockKeys + lane_off, tO = tmem + 2 * kBlockKeys + t * D + lane_off;
-    uint32_t gi = 0, s_phase = 0, o_phase = 0;
+    uint32_t gi = 0, s_phase = 0, o_phase = 0, h_phase = 0;
     bool ok = true;
     for (int seg = 0;; ++seg) {
       const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
-      const int row = sg.r0 + t * kRows + r;
+      const int row = sg.r0 + (split ? 0 : t * kRows) + r;
       const int query = geo.query(row < geo.R ? row : 0);
       const bool real = row < geo.R && query < sg.cnt;
       const int lim = real ? query_keys(geo, sg.len, sg.cnt, query) : sg.len;
       const int reach = t ? sg.reach[1] : sg.reach[0], least = t ? sg.least[1] : sg.least[0];
-      const int steps = min(sg.steps, reach - sg.j0);  // the row tile's share, maybe none
+      // The tile's blocks: all up to its reach, or every other one.
+      const int steps = min(sg.steps, reach - sg.j0);
+      const int i0 = split ? (sg.j0 + t) & 1 : 0, stride = split ? 2 : 1;
+      const bool have = i0 < steps;
       float m = kNoMax, l = 0.0f, mul = 0.0f;
       bool first = true;
-      for (int i = 0; i < steps; ++i) {
-        ok = mbar_wait_warp(&sh.s_full[t], s_phase, p.status, 0x29);
+      for (int i = i0; i < steps; i += stride) {
+        const uint32_t c = gi + i;
+        ok = mbar_wait_warp(&sh.sc_full[c & 3], (c >> 2) & 1, p.status, 0x2D) &&
+             mbar_wait_warp(&sh.s_full[t], s_phase, p.status, 0x29);
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after();
-        if (first) mul = sh.row_mul[seg & 1][t * kRows + r];
-        const Scales& sc = sh.scales[(gi + i) & 3];
+        if (first) mul = sh.row_mul[seg & 1][row - sg.r0];
+        const Scales& sc = sh.scales[c & 3];
         const int key0 = (sg.j0 + i) * kBlockKeys;
         float sv[kBlockKeys];
         {
@@ -485,68 +546,123 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
-      const bool have = steps > 0;
       if (have) {
         ok = mbar_wait_warp(&sh.o_done[t], o_phase, p.status, 0x2A);
         if (!ok) break;
         o_phase ^= 1u;
         tc_fence_after();
       }
-      // A masked block's V held NaN codes, which were kept out of the product: the columns of the
-      // keys this row sees are NaN.
-      uint32_t bad[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) bad[i] = 0;
-      if (__builtin_expect(have && sh.nan_seen[seg & 3] != 0, 0)) {
-        const int all = min(sg.least[0], sg.least[1]);
-        const int k0 = max(all / kBlockKeys, sg.j0) * kBlockKeys;
-        const int k1 = min(lim, (sg.j0 + sg.steps) * kBlockKeys);
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(
-            p.v8 + ((static_cast<int64_t>(sg.b) * geo.Hk + sg.hk) * geo.cap) * D);
-        for (int key = k0; key < k1; ++key)
-          for (int w = 0; w < D / 4; ++w) {
-            const uint32_t x = __ldg(vw + static_cast<int64_t>(key) * (D / 4) + w);
-            const uint32_t eq = __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & 0x08040201u;
-            bad[w / 8] |= ((eq | eq >> 8 | eq >> 16 | eq >> 24) & 0xFu) << (4 * (w % 8));
-          }
-      }
-      const bool write = row < geo.R;
-      const int64_t orow = geo.row_offset(sg.b, sg.hk, row);
-      const int64_t prow = static_cast<int64_t>(sg.slot) * kTileRows + t * kRows + r;
-#pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t rr[32];
-        __syncwarp();
+      const bool handed = split && ((sg.j0 + 1) & 1) < sg.steps;  // tile 1 has a state to hand over
+      float4* hand_z = reinterpret_cast<float4*>(
+          p.part_z + (static_cast<int64_t>(2 * p.ctas + blockIdx.x) * kRows) * D) + r;
+      float2* hand_lm = reinterpret_cast<float2*>(p.part_lm) + static_cast<int64_t>(2 * p.ctas + blockIdx.x) * kRows + r;
+      if (split && t == 1) {
         if (have) {
-          tmem_ld32(tO + c0, rr);
-          tmem_wait_ld();
-        } else {
+          ok = mbar_wait_warp(&sh.h_free, h_phase ^ 1u, p.status, 0x2E);
+          if (!ok) break;
+          h_phase ^= 1u;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) rr[k] = 0u;
-        }
-        if (bad[c0 / 32]) {
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t rr[32];
+            tmem_ld32(tO + c0, rr);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (bad[c0 / 32] >> k & 1u) rr[k] = 0x7FC00000u;
-        }
-        if (write) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 z = make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]),
-                                         __uint_as_float(rr[k + 2]), __uint_as_float(rr[k + 3]));
-            if (sg.whole)
-              write_out<kBf16, D, ByHead>(p, orow, c0 + k, z, l, m, real);
-            else
-              *reinterpret_cast<float4*>(p.part_z + prow * D + c0 + k) = z;
+            for (int k = 0; k < 32; k += 4)
+              hand_z[(c0 + k) / 4 * kRows] = make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]),
+                                                         __uint_as_float(rr[k + 2]), __uint_as_float(rr[k + 3]));
+          }
+          *hand_lm = make_float2(l, m);
+          tc_fence_before();
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.h_full);
+            mbar_arrive(&sh.o_read[t]);
           }
         }
-      }
-      if (have) {
+      } else {
+        float f0 = 1.0f, f1 = 0.0f;  // factors of this tile's z and of the one handed over
+        if (handed) {
+          ok = mbar_wait_warp(&sh.h_full, h_phase, p.status, 0x2F);
+          if (!ok) break;
+          h_phase ^= 1u;
+          const float2 lm = __ldcg(hand_lm);
+          const float mx = fmaxf(m, lm.y);
+          f0 = ex2(m - mx);
+          f1 = ex2(lm.y - mx);
+          l = l * f0 + lm.x * f1;
+          m = mx;
+        }
+        // A masked block's V held NaN codes, which were kept out of the product: the columns of
+        // the keys this row sees are NaN.
+        uint32_t bad[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) bad[i] = 0;
+        if (__builtin_expect((have || handed) && sh.nan_seen[seg & 3] != 0, 0)) {
+          const int all = min(sg.least[0], sg.least[1]);
+          const int k0 = max(all / kBlockKeys, sg.j0) * kBlockKeys;
+          const int k1 = min(lim, (sg.j0 + sg.steps) * kBlockKeys);
+          const uint32_t* vw = reinterpret_cast<const uint32_t*>(
+              p.v8 + ((static_cast<int64_t>(sg.b) * geo.Hk + sg.hk) * geo.cap) * D);
+          for (int key = k0; key < k1; ++key)
+            for (int w = 0; w < D / 4; ++w) {
+              const uint32_t x = __ldg(vw + static_cast<int64_t>(key) * (D / 4) + w);
+              const uint32_t eq = __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & 0x08040201u;
+              const uint32_t bits = ((eq | eq >> 8 | eq >> 16 | eq >> 24) & 0xFu) << (4 * (w % 8));
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                if (i == w / 8) bad[i] |= bits;
+            }
+        }
+        const bool write = row < geo.R;
+        const int64_t orow = geo.row_offset(sg.b, sg.hk, row);
+        const int64_t prow = static_cast<int64_t>(sg.slot) * geo.tile + (row - sg.r0);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t rr[32];
+          __syncwarp();
+          if (have) {
+            tmem_ld32(tO + c0, rr);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) rr[k] = 0u;
+          }
+          if (handed) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 h = __ldcg(hand_z + (c0 + k) / 4 * kRows);
+              rr[k] = __float_as_uint(fmaf(__uint_as_float(rr[k]), f0, h.x * f1));
+              rr[k + 1] = __float_as_uint(fmaf(__uint_as_float(rr[k + 1]), f0, h.y * f1));
+              rr[k + 2] = __float_as_uint(fmaf(__uint_as_float(rr[k + 2]), f0, h.z * f1));
+              rr[k + 3] = __float_as_uint(fmaf(__uint_as_float(rr[k + 3]), f0, h.w * f1));
+            }
+          }
+          if (bad[c0 / 32]) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (bad[c0 / 32] >> k & 1u) rr[k] = 0x7FC00000u;
+          }
+          if (write) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 z = make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]),
+                                           __uint_as_float(rr[k + 2]), __uint_as_float(rr[k + 3]));
+              if (sg.whole)
+                write_out<kBf16, D, ByHead>(p, orow, c0 + k, z, l, m, real);
+              else
+                *reinterpret_cast<float4*>(p.part_z + prow * D + c0 + k) = z;
+            }
+          }
+        }
+        if (write && !sg.whole) *reinterpret_cast<float2*>(p.part_lm + prow * 2) = make_float2(l, m);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.o_read[t]);
+        if (lane == 0) {
+          if (have) mbar_arrive(&sh.o_read[t]);
+          if (handed) mbar_arrive(&sh.h_free);
+        }
       }
-      if (write && !sg.whole) *reinterpret_cast<float2*>(p.part_lm + prow * 2) = make_float2(l, m);
       gi += sg.steps;
       if (pl.start + chunks_of(geo, pl.keys) >= u1) break;
       next_place(geo, pl);
@@ -566,8 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 
 template <bool kBf16, int D>
 cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
+  using C = kv8::tc::Config<kBf16, D>;
   auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D>;
-  constexpr size_t smem = kv8::tc::Config<D>::kSmem;
+  constexpr size_t smem = C::kOffShared + sizeof(kv8::tc::Shared);
+  static_assert(smem <= 227 * 1024, "shared memory overflow");
+  CUtensorMap tm_k;
+  if (!encode_byte_map(&tm_k, p.k8, static_cast<uint64_t>(p.geo.B) * p.geo.Hk, p.geo.cap, D,
+                       kv8::kBlockKeys, D))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -578,7 +700,7 @@ cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (4 * attr.numRegs < kv8::tc::kRegsIssue + 2 * kv8::tc::kRegsSoftmax + kv8::tc::kRegsConvert)
     return cudaErrorInvalidConfiguration;
-  void* args[] = {&p};
+  void* args[] = {&tm_k, &p};
   e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas), dim3(kv8::tc::kThreads), args,
                        smem, s);
   if (e != cudaSuccess) return e;
