@@ -17,9 +17,10 @@
 // tile 1 then hands its state to tile 0 (through L2) at the end.  Either way the tensor core works on one
 // tile while the other's softmax runs.  Warpgroups:
 //   0  warps 0, 1: MMA issuers of the two tiles (per block j: P V of the block before, then
-//      S_j); warp 2: TMA producer of K tiles (swizzled) and of raw V blocks
-//   1, 2  softmax of tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant)
-//   3  converters: queries into their terms, raw V blocks into fp16 tiles
+//      S_j); warp 2: TMA producer of the code tiles of K and of V
+//   1, 2  softmax of tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant); at a
+//      tile's start each also cuts its query row into terms
+//   3  converters: one thread a key, its V codes into an fp16 tile
 // S and P share TMEM columns; O stays in TMEM for the length of a tile.
 //
 // The registers of 512 threads are dealt again: softmax holds a row's 128 scores, the others
@@ -36,7 +37,7 @@ namespace tc {
 constexpr int kRows = 128;   // of a row tile
 constexpr int kThreads = 512;
 constexpr int kGroups = kBlockKeys / 16;  // scale groups of a block
-constexpr int kRegsIssue = 56, kRegsSoftmax = 192, kRegsConvert = 72;
+constexpr int kRegsIssue = 64, kRegsSoftmax = 184, kRegsConvert = 80;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128, "more registers than launched");
 
 template <bool kBf16, int D>
@@ -64,7 +65,6 @@ struct Shared {
   uint32_t tmem_base;
   uint32_t nan_seen[4];             // by tile number mod 4: a masked block's V held NaN codes
                                     // (cleared two tiles ahead, where its last reader is done)
-  float row_mul[2][2 * kRows];      // by tile number mod 2: |c| log2(e) times the row's power of two
   Scales scales[4];                 // by block number mod 4
 };
 
@@ -107,60 +107,107 @@ __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t
   return s;
 }
 
-// Sixteen codes to sixteen fp16 values.
-__device__ __forceinline__ void widen16(uint4 u, uint4& a, uint4& b) {
-  a = make_uint4(lo_codes(u.x), hi_codes(u.x), lo_codes(u.y), hi_codes(u.y));
-  b = make_uint4(lo_codes(u.z), hi_codes(u.z), lo_codes(u.w), hi_codes(u.w));
-}
-
-// A converter thread's pieces of one raw block: 16 codes of row (it 128 + tid) / (D / 16).
+// A key's V row in a converter thread.  Thread = key, and a swizzled row's 16-byte pieces lie at
+// piece XOR key (within a 128-byte line), so eight lanes never meet in a bank, reading codes or
+// writing fp16.
 template <int D>
-struct Pieces {
+struct ValueRow {
   static constexpr int kN = D / 16;
   uint4 u[kN];
-  // Rows from `rows` on, which the copy did not bring, are zeros.
-  __device__ __forceinline__ void load(const uint8_t* raw, int rows, int tid) {
+  __device__ __forceinline__ void load(const uint8_t* tile, int key) {
 #pragma unroll
-    for (int it = 0; it < kN; ++it) {
-      const int idx = it * 128 + tid;
-      u[it] = *reinterpret_cast<const uint4*>(raw + idx * 16);
-      if (idx / kN >= rows) u[it] = make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < kN; ++i)
+      u[i] = *reinterpret_cast<const uint4*>(tile + Tile<kBlockKeys, D / 2>::offset(key, 8 * i));
   }
-  // Widened into a swizzled tile.  The two 16-byte halves of a piece are written in an order that
-  // alternates between the halves of a row, which keeps eight lanes' stores on different banks.
-  __device__ __forceinline__ void store(uint8_t* tile, int tid) const {
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, int key) const {
     using T = Tile<kBlockKeys, D>;
 #pragma unroll
-    for (int it = 0; it < kN; ++it) {
-      const int idx = it * 128 + tid, row = idx / kN, col = idx % kN * 16;
-      uint4 a, b;
-      widen16(u[it], a, b);
-      const bool swap = (idx & 4) != 0;
-      *reinterpret_cast<uint4*>(tile + T::offset(row, col + (swap ? 8 : 0))) = swap ? b : a;
-      *reinterpret_cast<uint4*>(tile + T::offset(row, col + (swap ? 0 : 8))) = swap ? a : b;
+    for (int i = 0; i < kN; ++i) {
+      *reinterpret_cast<uint4*>(tile + T::offset(key, 16 * i)) =
+          make_uint4(lo_codes(u[i].x), hi_codes(u[i].x), lo_codes(u[i].y), hi_codes(u[i].y));
+      *reinterpret_cast<uint4*>(tile + T::offset(key, 16 * i + 8)) =
+          make_uint4(lo_codes(u[i].z), hi_codes(u[i].z), lo_codes(u[i].w), hi_codes(u[i].w));
     }
   }
   // Takes NaN codes out (to 0); true if there were any.
   __device__ __forceinline__ bool drop_nan() {
     bool any = false;
 #pragma unroll
-    for (int it = 0; it < kN; ++it) {
-      uint32_t* w[4] = {&u[it].x, &u[it].y, &u[it].z, &u[it].w};
+    for (int i = 0; i < kN; ++i) {
+      uint32_t* w[4] = {&u[i].x, &u[i].y, &u[i].z, &u[i].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t bad = __vcmpeq4(*w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bad = __vcmpeq4(*w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         any |= bad != 0;
-        *w[i] &= ~bad;
+        *w[e] &= ~bad;
       }
     }
     return any;
   }
 };
 
+// Largest finite magnitude of a query row.
+template <bool kBf16, int D>
+__device__ __forceinline__ float row_amax(const uint16_t* q) {
+  float amax = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack16<kBf16>(w[e]);
+      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+    }
+  }
+  return amax;
+}
+
+// Row r of a tile's terms: q times mul, cut into E4M3 values (q null: zeros).
+template <bool kBf16, int D>
+__device__ __forceinline__ void put_query_row(uint8_t* terms, int r, const uint16_t* q, float mul) {
+  using C = Config<kBf16, D>;
+  using T8 = typename C::T8;
+#pragma unroll 2
+  for (int i = 0; i < D / 16; ++i) {
+    uint4 u = make_uint4(0, 0, 0, 0), v = u;
+    if (q) {
+      u = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i);
+      v = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i + 1);
+    }
+    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 f = unpack16<kBf16>(w[e]);
+      x[2 * e] = nan_unless_finite(f.x) * mul;
+      x[2 * e + 1] = nan_unless_finite(f.y) * mul;
+    }
+#pragma unroll
+    for (int term = 0; term < C::kTerms; ++term) {
+      uint32_t c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = pack4_e4m3(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        float y[4];
+        codes_to_float4(c[e], y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[4 * e + k] -= y[k];  // exact
+      }
+      *reinterpret_cast<uint4*>(terms + term * T8::kBytes + T8::offset(r, 8 * i)) =
+          make_uint4(c[0], c[1], c[2], c[3]);
+    }
+  }
+}
+
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const AttendParams<ByHead> p) {
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const AttendParams<ByHead> p) {
   using C = Config<kBf16, D>;
   using T8 = typename C::T8;
   using TV = typename C::TV;
@@ -183,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.q_full, split ? 4 : 8);
     mbar_init(&sh.q_free, 2);
     mbar_init(&sh.h_full, 4);
     mbar_init(&sh.h_free, 4);
@@ -314,17 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key0 = (sg.j0 + i) * kBlockKeys;
           ok = mbar_wait_warp(&sh.k_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x27);
           if (!ok) break;
-          if (lane == 0) {  // rows past the cache read as zeros, those past the length are masked
+          if (lane == 0) {  // rows past the cache read as zeros
             mbar_arrive_expect_tx(&sh.k_full[c & 1], T8::kBytes);
             tma_load_3d(sK + (c & 1) * T8::kBytes, &tm_k, &sh.k_full[c & 1], 0, key0, bh);
           }
           ok = mbar_wait_warp(&sh.r_empty[rs], ((c / C::kSR) & 1) ^ 1, p.status, 0x28);
           if (!ok) break;
           if (lane == 0) {
-            const uint32_t bytes = min(kBlockKeys, sg.len - key0) * D;
-            mbar_arrive_expect_tx(&sh.r_full[rs], bytes);
-            bulk_load(sR + rs * C::kRaw, p.v8 + (static_cast<int64_t>(bh) * geo.cap + key0) * D, bytes,
-                      &sh.r_full[rs]);
+            mbar_arrive_expect_tx(&sh.r_full[rs], C::kRaw);
+            tma_load_3d(sR + rs * C::kRaw, &tm_v, &sh.r_full[rs], 0, key0, bh);
           }
           __syncwarp();
         }
@@ -338,8 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegsConvert>();
     const int tid = threadIdx.x - 3 * 128;
     const int nblk = geo.cap / p.block;
-    const bool negative = p.c2 < 0.0f;
-    const float c2 = fabsf(p.c2);
     uint32_t gi = 0;
     for (int seg = 0;; ++seg) {
       const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
@@ -347,50 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* ksp = p.k_scales + bh * nblk;
       const float* vsp = p.v_scales + bh * nblk;
       const int least = min(sg.least[0], sg.least[1]);
-      bool ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
-      if (!ok) break;
-      if (tid == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
-      // Queries: D / 8 lanes a row; rows past the head's last are zeros.
-      {
-        constexpr int kLanes = D / 8;
-        const uint16_t* qp = p.q + (bh * geo.R + sg.r0) * D;
-        const int rows = min(geo.tile, geo.R - sg.r0), its = geo.tile * kLanes / 128;
-#pragma unroll 4
-        for (int it = 0; it < its; ++it) {
-          const int idx = it * 128 + tid, row = idx / kLanes, col = idx % kLanes * 8;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (row < rows) u = __ldg(reinterpret_cast<const uint4*>(qp + static_cast<int64_t>(row) * D + col));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          float x[8], amax = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack16<kBf16>(w[i]);
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
-            amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
-          }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-          const int e = scale_exp(amax);
-          const float mul = negative ? -pow2(-e) : pow2(-e);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = nan_unless_finite(x[i]) * mul;
-          uint8_t* dst = sQ + row / kRows * C::kTerms * T8::kBytes + T8::offset(row % kRows, col / 2);
-#pragma unroll
-          for (int term = 0; term < C::kTerms; ++term) {
-            const uint2 c = make_uint2(pack4_e4m3(x[0], x[1], x[2], x[3]), pack4_e4m3(x[4], x[5], x[6], x[7]));
-            *reinterpret_cast<uint2*>(dst + term * T8::kBytes) = c;
-            float y[4], z[4];
-            codes_to_float4(c.x, y);
-            codes_to_float4(c.y, z);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] -= y[i], x[4 + i] -= z[i];  // exact
-          }
-          if (idx % kLanes == 0) sh.row_mul[seg & 1][row] = c2 * pow2(e);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full);
-      }
+      bool ok = true;
       // Scales of block i by the first warp, written a block ahead of V.  The place's last readers
       // were softmax four blocks ago, which P V of two blocks ago (v_empty) came after.
       float ks = 1.0f, vs = 1.0f;
@@ -421,15 +421,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t c = gi + i, rs = c % C::kSR;
         const int key0 = (sg.j0 + i) * kBlockKeys;
         if (warp == 12 && i + 1 < sg.steps) fetch_scales(i + 1);
-        Pieces<D> x;
+        ValueRow<D> x;
         ok = mbar_wait_warp(&sh.r_full[rs], (c / C::kSR) & 1, p.status, 0x2B);
         if (!ok) break;
-        x.load(sR + rs * C::kRaw, sg.len - key0, tid);
+        x.load(sR + rs * C::kRaw, tid);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.r_empty[rs]);
-        if (key0 + kBlockKeys > least && x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
+        if (key0 + tid >= sg.len) x.clear();
         ok = mbar_wait_warp(&sh.v_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x2C);
         if (!ok) break;
+        if (key0 + kBlockKeys > least && x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
         if (warp == 12 && i + 1 < sg.steps) put_scales(i + 1);
         x.store(sV + (c & 1) * TV::kBytes, tid);
         fence_proxy_async_smem();
@@ -459,7 +460,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = min(sg.steps, reach - sg.j0);
       const int i0 = split ? (sg.j0 + t) & 1 : 0, stride = split ? 2 : 1;
       const bool have = i0 < steps;
-      float m = kNoMax, l = 0.0f, mul = 0.0f;
+      float m = kNoMax, l = 0.0f, mul;  // mul: |c| log2(e) times the row's power of two
+      {
+        const uint16_t* qrow = row < geo.R ? p.q + geo.row_offset(sg.b, sg.hk, row) * D : nullptr;
+        const int e = scale_exp(qrow ? row_amax<kBf16, D>(qrow) : 0.0f);
+        mul = fabsf(p.c2) * pow2(e);
+        if (!split || t == 0) {
+          ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
+          if (!ok) break;
+          if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
+          put_query_row<kBf16, D>(sQ + t * C::kTerms * T8::kBytes, r, qrow, p.c2 < 0.0f ? -pow2(-e) : pow2(-e));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full);
+        }
+      }
       bool first = true;
       for (int i = i0; i < steps; i += stride) {
         const uint32_t c = gi + i;
@@ -468,7 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after();
-        if (first) mul = sh.row_mul[seg & 1][row - sg.r0];
         const Scales& sc = sh.scales[c & 3];
         const int key0 = (sg.j0 + i) * kBlockKeys;
         float sv[kBlockKeys];
@@ -686,9 +700,10 @@ cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
   auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D>;
   constexpr size_t smem = C::kOffShared + sizeof(kv8::tc::Shared);
   static_assert(smem <= 227 * 1024, "shared memory overflow");
-  CUtensorMap tm_k;
-  if (!encode_byte_map(&tm_k, p.k8, static_cast<uint64_t>(p.geo.B) * p.geo.Hk, p.geo.cap, D,
-                       kv8::kBlockKeys, D))
+  CUtensorMap tm_k, tm_v;
+  const uint64_t heads = static_cast<uint64_t>(p.geo.B) * p.geo.Hk;
+  if (!encode_byte_map(&tm_k, p.k8, heads, p.geo.cap, D, kv8::kBlockKeys, D) ||
+      !encode_byte_map(&tm_v, p.v8, heads, p.geo.cap, D, kv8::kBlockKeys, D))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
@@ -700,7 +715,7 @@ cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (4 * attr.numRegs < kv8::tc::kRegsIssue + 2 * kv8::tc::kRegsSoftmax + kv8::tc::kRegsConvert)
     return cudaErrorInvalidConfiguration;
-  void* args[] = {&tm_k, &p};
+  void* args[] = {&tm_k, &tm_v, &p};
   e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas), dim3(kv8::tc::kThreads), args,
                        smem, s);
   if (e != cudaSuccess) return e;
