@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
     const int tile_chunks = chunks_of(geo, pl.keys);
     const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
     const int c1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(tile_chunks)));
+    if (p.ctas > 0 && c0 == 0 && pl.start >= u0 && threadIdx.x == 0) note_run(p, pl, u0, u1);
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
     const int64_t bh = static_cast<int64_t>(pl.b) * geo.Hk + pl.hk;
     const uint8_t* kp = p.k8 + bh * geo.cap * D;
@@ -398,22 +399,32 @@ cudaError_t launch_attend_nt(const AttendParams<ByQuery>& p, int sms, cudaStream
 // Rows per key/value head up to which the mma.sync kernel is used (see the measurements above).
 constexpr int kFewRows = 32;
 
-size_t kv8_attend_workspace_bytes(int, int, int G, int n, int d, int cap, int sms) {
+int rows_per_tile(int64_t R) {
+  if (R > kFewRows) return R > kTcTileRows / 2 ? kTcTileRows : kTcTileRows / 2;
+  return kv8::rows_per_tile(static_cast<int>(R));
+}
+
+// Rows of the parts: two places a CTA (for tiles of 128 rows, two and one for what its second row
+// tile hands over).
+size_t part_rows(int64_t R, int sms) {
+  if (R > kFewRows) return static_cast<size_t>(2) * sms * kTcTileRows;
+  return static_cast<size_t>(2) * sms * kv8::kMostCtas * rows_per_tile(R);
+}
+
+size_t kv8_attend_workspace_bytes(int B, int Hk, int G, int n, int d, int cap, int sms) {
   const int64_t R = static_cast<int64_t>(G) * n;
-  size_t rows = 0;  // of the parts: two places a CTA
-  if (R > kFewRows)
-    rows = static_cast<size_t>(2) * sms * kTcTileRows;
-  else if (cap > kv8::kAlignedCap)
-    rows = static_cast<size_t>(2) * sms * kv8::kMostCtas * kv8::rows_per_tile(static_cast<int>(R));
-  return rows * (d + 2) * sizeof(float);
+  if (R <= kFewRows && cap <= kv8::kAlignedCap) return 0;  // nothing to join
+  const size_t tiles = static_cast<size_t>(B) * Hk * ((R + rows_per_tile(R) - 1) / rows_per_tile(R));
+  return part_rows(R, sms) * (d + 2) * sizeof(float) + tiles * sizeof(int2);
 }
 
 namespace {
 
 template <class Geo>
-kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int tile, int ctas) {
+kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int ctas, int min_chunks) {
   kv8::AttendParams<Geo> p{};
-  const int R = a.G * a.n;
+  const int R = a.G * a.n, tile = rows_per_tile(R);
+  const size_t rows = part_rows(R, a.sms);
   p.geo = {{a.B, a.Hk, a.G, a.n, a.cap, R, tile, (R + tile - 1) / tile, a.causal, a.lengths, a.counts, false}};
   p.block = a.block;
   p.c2 = a.c * kv8::kLog2e;
@@ -425,8 +436,10 @@ kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int tile, int ctas) {
   p.o = static_cast<uint16_t*>(a.o);
   p.lse = a.lse;
   p.part_z = static_cast<float*>(a.workspace);
-  p.part_lm = p.part_z + static_cast<size_t>(2) * ctas * tile * a.d;
+  p.part_lm = p.part_z + rows * a.d;
+  p.runs = reinterpret_cast<int2*>(p.part_lm + rows * 2);
   p.ctas = ctas;
+  p.min_chunks = min_chunks;
   p.status = a.status;
   return p;
 }
@@ -437,17 +450,13 @@ int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   const int64_t R = static_cast<int64_t>(a.G) * a.n;
   cudaError_t e;
   if (R > kFewRows) {
-    // Two places a CTA for tiles of 256 rows; for 128, two and one for what tile 1 hands over.
-    auto p = attend_params<kv8::ByHead>(a, R > kTcTileRows / 2 ? kTcTileRows : kTcTileRows / 2, a.sms);
-    p.part_lm = p.part_z + static_cast<size_t>(2) * a.sms * kTcTileRows * a.d;
-    p.min_chunks = 2;
+    auto p = attend_params<kv8::ByHead>(a, a.sms, 2);
     if (a.bf16)
       e = a.d == 128 ? launch_kv8_tc<true, 128>(p, s) : launch_kv8_tc<true, 64>(p, s);
     else
       e = a.d == 128 ? launch_kv8_tc<false, 128>(p, s) : launch_kv8_tc<false, 64>(p, s);
   } else {
-    auto p = attend_params<kv8::ByQuery>(a, kv8::rows_per_tile(static_cast<int>(R)), kv8::kMostCtas * a.sms);
-    p.min_chunks = 2 * kv8::kAttendWarps;
+    auto p = attend_params<kv8::ByQuery>(a, kv8::kMostCtas * a.sms, 2 * kv8::kAttendWarps);
     if (a.bf16)
       e = a.d == 128 ? kv8::launch_attend_nt<true, 128>(p, a.sms, s) : kv8::launch_attend_nt<true, 64>(p, a.sms, s);
     else

@@ -24,6 +24,7 @@ struct AttendParams {
   float* lse;
   float* part_z;   // [2 ctas][tile][D]: parts of shared tiles, two places a CTA
   float* part_lm;  // [2 ctas][tile][2]: their l and m
+  int2* runs;      // [tiles of all heads] first and last CTA of a tile that some row of sees a key
   int ctas;        // runs the work is cut into; 0: one CTA a tile, and no parts
   int min_chunks;  // a run has at least this many
   uint32_t* status;
@@ -51,6 +52,16 @@ __device__ __forceinline__ void write_out(const AttendParams<Geo>& p, int64_t ro
   }
 }
 
+// The CTA that holds a tile's first chunk notes which CTAs share it (u0, u1: its run).
+template <class Geo>
+__device__ __forceinline__ void note_run(const AttendParams<Geo>& p, const Place& pl, int64_t u0, int64_t u1) {
+  const int64_t per = u1 - u0;  // a run that ends before its length is the last
+  const int64_t end = pl.start + chunks_of(p.geo, pl.keys);
+  const int more = end > u1 ? static_cast<int>((end - u1 + per - 1) / per) : 0;
+  const int64_t id = (static_cast<int64_t>(pl.b) * p.geo.Hk + pl.hk) * p.geo.tiles + pl.rt;
+  p.runs[id] = make_int2(blockIdx.x, blockIdx.x + more);
+}
+
 // Joins the parts of tiles that several CTAs shared, and writes tiles that see no key at all.
 // One warp a row, eight rows a CTA.
 constexpr int kJoinWarps = 8;
@@ -70,15 +81,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   if (pl.rt == 0 && pl.hk == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
   pl.keys = tile_keys(geo, len, cnt, pl.rt);
-  int64_t first = 0, last = 0;
-  if (pl.keys > 0) {
-    int64_t total;
-    locate(geo, pl, total);
-    const int64_t per = run_length(total, p.ctas, p.min_chunks);
-    first = pl.start / per;
-    last = (pl.start + chunks_of(geo, pl.keys) - 1) / per;
-  }
   grid_dependency_wait();  // by every warp: what follows on the stream may rely on this kernel
+  int first = 0, last = 0;
+  if (pl.keys > 0) {
+    const int2 run = p.runs[blockIdx.x];
+    first = run.x, last = run.y;
+  }
   if (r >= geo.R || (pl.keys > 0 && first == last)) return;  // or one CTA held the tile whole
   float mx = kNoMax, l = 0.0f;
   float z[kCols];
@@ -86,10 +94,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
   if (pl.keys > 0) {
     // Place 1 of the first CTA (the tile starts there), place 0 of the others.
-    const int64_t all = last - first + 1;
-    auto place = [&](int64_t q) { return (2 * (first + q) + (q == 0 ? 1 : 0)) * geo.tile + row; };
-    for (int64_t q0 = 0; q0 < all; q0 += 32) {
-      const int parts = static_cast<int>(min(all - q0, static_cast<int64_t>(32)));
+    const int all = last - first + 1;
+    auto place = [&](int q) {
+      return static_cast<int64_t>(2 * (first + q) + (q == 0 ? 1 : 0)) * geo.tile + row;
+    };
+    for (int q0 = 0; q0 < all; q0 += 32) {
+      const int parts = min(all - q0, 32);
       float2 lm = make_float2(0.0f, kNoMax);
       if (lane < parts) lm = *reinterpret_cast<const float2*>(p.part_lm + place(q0 + lane) * 2);
       const float mn = fmaxf(mx, warp_max(lm.y)), old = ex2(mx - mn);

@@ -145,21 +145,6 @@ __device__ __forceinline__ Place plan_run(const Geo& g, int cta, int ctas, int m
   return p;
 }
 
-// Work-list index of the first chunk of tile p, and the list's length.  Executed by whole warps.
-template <class Geo>
-__device__ __forceinline__ void locate(const Geo& g, Place& p, int64_t& total) {
-  int64_t before = 0, all = 0;
-  for (int b = lane_id(); b < g.B; b += 32) {
-    const int64_t u = head_chunks(g, b);
-    all += u;
-    if (b < p.b) before += u;
-  }
-  total = g.Hk * warp_sum(all);
-  p.start = g.Hk * warp_sum(before) + p.hk * head_chunks(g, p.b);
-  const int len = seq_len(g.lengths, p.b, g.cap), cnt = seq_count(g.counts, p.b, g.n);
-  for (int rt = 0; rt < p.rt; ++rt) p.start += chunks_of(g, tile_keys(g, len, cnt, rt));
-}
-
 // The next tile of the list with at least one chunk (the caller knows that there is one).
 template <class Geo>
 __device__ __forceinline__ void next_place(const Geo& g, Place& p) {

@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;;) {
         const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
         const int bh = sg.b * geo.Hk + sg.hk;
+        if (sg.j0 == 0 && lane == 0) note_run(p, pl, u0, u1);
         for (int i = 0; i < sg.steps && ok; ++i) {
           const uint32_t c = gi + i, rs = c % C::kSR;
           const int key0 = (sg.j0 + i) * kBlockKeys;
