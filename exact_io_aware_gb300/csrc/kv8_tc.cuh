@@ -17,7 +17,8 @@
 // tile 1 then hands its state to tile 0 (through L2) at the end.  Either way the tensor core works on one
 // tile while the other's softmax runs.  Warpgroups:
 //   0  warps 0, 1: MMA issuers of the two tiles (per block j: P V of the block before, then
-//      S_j); warp 2: TMA producer of the code tiles of K and of V
+//      S_j); warp 2: TMA producer of the code tiles of K and of V; warp 3: the run's tiles one
+//      after another, as the other warps need to know them (Seg)
 //   1, 2  softmax of tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant); at a
 //      tile's start each also cuts its query row into terms
 //   3  converters: one thread a key, its V codes into an fp16 tile
@@ -38,6 +39,7 @@ constexpr int kRows = 128;   // of a row tile
 constexpr int kThreads = 512;
 constexpr int kGroups = kBlockKeys / 16;  // scale groups of a block
 constexpr int kRegsIssue = 64, kRegsSoftmax = 184, kRegsConvert = 80;
+constexpr int kSegReaders = 15;  // warps that are told of each tile
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128, "more registers than launched");
 
 template <bool kBf16, int D>
@@ -54,25 +56,6 @@ struct Config {
   static constexpr int kOffShared = kOffR + kSR * kRaw;
 };
 
-struct Scales {  // of one block, per 16 keys
-  float k[kGroups], log2_v[kGroups], inv_v[kGroups];
-};
-
-struct Shared {
-  uint64_t q_full, q_free, h_full, h_free;
-  uint64_t s_full[2], p_full[2], o_done[2], o_read[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], r_full[3], r_empty[3], sc_full[4];
-  uint32_t tmem_base;
-  uint32_t nan_seen[4];             // by tile number mod 4: a masked block's V held NaN codes
-                                    // (cleared two tiles ahead, where its last reader is done)
-  Scales scales[4];                 // by block number mod 4
-};
-
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // One tile of the run, as every role sees it.
 struct Seg {
   int b, hk, len, cnt;
@@ -82,7 +65,30 @@ struct Seg {
   int slot;          // else where its part goes
   int reach[2];      // blocks row tile t takes, counted from block 0
   int least[2];      // keys every real row of row tile t sees (blocks past them are masked)
+  bool last;         // of the run
 };
+
+struct Scales {  // of one block, per 16 keys
+  float k[kGroups], log2_v[kGroups], inv_v[kGroups];
+};
+
+struct Shared {
+  uint64_t q_full, q_free, h_full, h_free;
+  uint64_t s_full[2], p_full[2], o_done[2], o_read[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], r_full[3], r_empty[3], sc_full[4];
+  uint64_t seg_full[4], seg_empty[4];
+  Seg seg[4];                       // by tile number mod 4
+  uint32_t tmem_base;
+  bool idle;                        // nothing to do for this CTA
+  uint32_t nan_seen[4];             // by tile number mod 4: a masked block's V held NaN codes
+                                    // (cleared two tiles ahead, where its last reader is done)
+  Scales scales[4];                 // by block number mod 4
+};
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t u0, int64_t u1, int cta) {
   Seg s;
@@ -95,6 +101,7 @@ __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t
   const int j1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(blocks)));
   s.steps = j1 - s.j0;
   s.whole = s.j0 == 0 && j1 == blocks;
+  s.last = pl.start + blocks >= u1;
   s.slot = 2 * cta + (s.j0 == 0 ? 1 : 0);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -150,18 +157,26 @@ struct ValueRow {
   }
 };
 
-// Largest finite magnitude of a query row.
+// Largest finite magnitude of a query row (null: 0).  This and put_query_row run once a tile, and
+// their loops stay rolled: unrolled, fetching their instructions took longer than running them.
 template <bool kBf16, int D>
 __device__ __forceinline__ float row_amax(const uint16_t* q) {
   float amax = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < D / 8; ++i) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (q) {
+#pragma unroll 1
+    for (int i = 0; i < D / 8; i += 8) {
+      uint4 u[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack16<kBf16>(w[e]);
-      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+      for (int k = 0; k < 8; ++k) u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i + k);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack16<kBf16>(w[e]);
+          amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+        }
+      }
     }
   }
   return amax;
@@ -172,14 +187,14 @@ template <bool kBf16, int D>
 __device__ __forceinline__ void put_query_row(uint8_t* terms, int r, const uint16_t* q, float mul) {
   using C = Config<kBf16, D>;
   using T8 = typename C::T8;
-#pragma unroll 2
+#pragma unroll 1
   for (int i = 0; i < D / 16; ++i) {
-    uint4 u = make_uint4(0, 0, 0, 0), v = u;
+    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (q) {
-      u = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i);
-      v = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i + 1);
+      u[0] = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i);
+      u[1] = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i + 1);
     }
-    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
     float x[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -187,7 +202,7 @@ __device__ __forceinline__ void put_query_row(uint8_t* terms, int r, const uint1
       x[2 * e] = nan_unless_finite(f.x) * mul;
       x[2 * e + 1] = nan_unless_finite(f.y) * mul;
     }
-#pragma unroll
+#pragma unroll 1
     for (int term = 0; term < C::kTerms; ++term) {
       uint32_t c[4];
 #pragma unroll
@@ -221,12 +236,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const ByHead& geo = p.geo;
   const bool split = geo.tile == kRows;  // the two tiles are the same rows, of alternate blocks
   grid_launch_dependents();
-  int64_t u0, u1;
-  Place pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
-  if (u0 >= u1) return;
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it
     if (threadIdx.x == 0) raise_timeout(p.status, 0x20);
     return;
+  }
+  int64_t u0 = 0, u1 = 0;
+  Place pl{};
+  if (warp == 3) {
+    pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    if (lane == 0) sh.idle = u0 >= u1;
   }
 
   if (threadIdx.x == 0) {
@@ -251,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.r_empty[s], 4);
     }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.seg_full[i], 1);
+      mbar_init(&sh.seg_empty[i], kSegReaders);
       mbar_init(&sh.sc_full[i], 1);
       sh.nan_seen[i] = 0;
     }
@@ -263,7 +283,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;  // S_t (and P_t) at 128 t, O_t at 256 + D t
 
-  if (group == 0) {
+  // Tile number n of the run: waits until it is told, and gives its place back when done with.
+  auto next_seg = [&](int n) { return mbar_wait_warp(&sh.seg_full[n & 3], (n >> 2) & 1, p.status, 0x30); };
+  auto done_seg = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.seg_empty[n & 3]);
+  };
+
+  if (sh.idle) {
+  } else if (group == 0) {
     regs_dec<kRegsIssue>();
     if (warp < 2) {
       // ------------------------------------------------------------ MMA issuer of row tile t
@@ -278,19 +306,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Tiles in which this row tile takes no block have no o_done and o_read phases.
       uint32_t rph = 0;
       bool owed = false, ok = true;  // the tile before's O is still to be read
-      for (int seg = 0; ok; ++seg) {
-        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
-        const int reach = t ? sg.reach[1] : sg.reach[0];
+      for (int seg = 0;; ++seg) {
+        ok = next_seg(seg);
+        if (!ok) break;
+        const Seg& sg = sh.seg[seg & 3];
+        const int reach = sg.reach[t], steps = sg.steps, j0 = sg.j0;
         ok = mbar_wait_warp(&sh.q_full, seg & 1, p.status, 0x21);
         bool pend = false, started = false;
-        for (int i = 0; i <= sg.steps && ok; ++i) {
+        for (int i = 0; i <= steps && ok; ++i) {
           const uint32_t cur_i = gi + i, prev_i = cur_i - 1;
           if (i > 0) {
             ok = mbar_wait_warp(&sh.v_full[prev_i & 1], (prev_i >> 1) & 1, p.status, 0x22);
             if (!ok) break;
           }
-          const bool cur = i < sg.steps && (split ? ((sg.j0 + i) & 1) == t : sg.j0 + i < reach);
-          if (i < sg.steps) {
+          const bool cur = i < steps && (split ? ((j0 + i) & 1) == t : j0 + i < reach);
+          if (i < steps) {
             ok = mbar_wait_warp(&sh.k_full[cur_i & 1], (cur_i >> 1) & 1, p.status, 0x23);
             if (!ok) break;
           }
@@ -323,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          if (i + 1 == sg.steps && owed) {
+          if (i + 1 == steps && owed) {
             // Q is released for the next tile only when this row tile's last O has been read, so
             // what softmax holds by tile number stays at most two tiles behind the converters.
             ok = mbar_wait_warp(&sh.o_read[t], rph, p.status, 0x25);
@@ -332,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             owed = false;
           }
           if (elect_one()) {
-            if (i < sg.steps) mma_commit(&sh.k_empty[cur_i & 1]);
-            if (i + 1 == sg.steps) mma_commit(&sh.q_free);
+            if (i < steps) mma_commit(&sh.k_empty[cur_i & 1]);
+            if (i + 1 == steps) mma_commit(&sh.q_free);
             if (i > 0) mma_commit(&sh.v_empty[prev_i & 1]);
           }
           __syncwarp();
@@ -345,21 +375,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           owed = true;
         }
-        gi += sg.steps;
-        if (pl.start + chunks_of(geo, pl.keys) >= u1) break;
-        next_place(geo, pl);
+        gi += steps;
+        const bool last = sg.last;
+        done_seg(seg);
+        if (last) break;
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------ TMA producer
       uint32_t gi = 0;
       bool ok = true;
-      for (;;) {
-        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
-        const int bh = sg.b * geo.Hk + sg.hk;
-        if (sg.j0 == 0 && lane == 0) note_run(p, pl, u0, u1);
-        for (int i = 0; i < sg.steps && ok; ++i) {
+      for (int seg = 0;; ++seg) {
+        ok = next_seg(seg);
+        if (!ok) break;
+        const Seg& sg = sh.seg[seg & 3];
+        const int bh = sg.b * geo.Hk + sg.hk, steps = sg.steps, j0 = sg.j0;
+        for (int i = 0; i < steps && ok; ++i) {
           const uint32_t c = gi + i, rs = c % C::kSR;
-          const int key0 = (sg.j0 + i) * kBlockKeys;
+          const int key0 = (j0 + i) * kBlockKeys;
           ok = mbar_wait_warp(&sh.k_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x27);
           if (!ok) break;
           if (lane == 0) {  // rows past the cache read as zeros
@@ -374,8 +406,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        gi += sg.steps;
-        if (!ok || pl.start + chunks_of(geo, pl.keys) >= u1) break;
+        if (!ok) break;
+        gi += steps;
+        const bool last = sg.last;
+        done_seg(seg);
+        if (last) break;
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ the run's tiles
+      for (int seg = 0;; ++seg) {
+        if (!mbar_wait_warp(&sh.seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, p.status, 0x31)) break;
+        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+        if (lane == 0) {
+          sh.seg[seg & 3] = sg;
+          if (sg.j0 == 0) note_run(p, pl, u0, u1);
+          mbar_arrive(&sh.seg_full[seg & 3]);
+        }
+        __syncwarp();
+        if (sg.last) break;
         next_place(geo, pl);
       }
     }
@@ -386,19 +434,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nblk = geo.cap / p.block;
     uint32_t gi = 0;
     for (int seg = 0;; ++seg) {
-      const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+      bool ok = next_seg(seg);
+      if (!ok) break;
+      const Seg& sg = sh.seg[seg & 3];
       const int64_t bh = static_cast<int64_t>(sg.b) * geo.Hk + sg.hk;
       const float* ksp = p.k_scales + bh * nblk;
       const float* vsp = p.v_scales + bh * nblk;
-      const int least = min(sg.least[0], sg.least[1]);
-      bool ok = true;
+      const int steps = sg.steps, j0 = sg.j0, len = sg.len, least = min(sg.least[0], sg.least[1]);
       // Scales of block i by the first warp, written a block ahead of V.  The place's last readers
       // were softmax four blocks ago, which P V of two blocks ago (v_empty) came after.
       float ks = 1.0f, vs = 1.0f;
       auto fetch_scales = [&](int i) {
-        const int key = (sg.j0 + i) * kBlockKeys + tid * 16;
+        const int key = (j0 + i) * kBlockKeys + tid * 16;
         ks = vs = 1.0f;
-        if (tid < kGroups && key < sg.len) {
+        if (tid < kGroups && key < len) {
           ks = __ldg(ksp + key / p.block);
           vs = __ldg(vsp + key / p.block);
         }
@@ -418,29 +467,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch_scales(0);
         put_scales(0);
       }
-      for (int i = 0; i < sg.steps; ++i) {
+      for (int i = 0; i < steps; ++i) {
         const uint32_t c = gi + i, rs = c % C::kSR;
-        const int key0 = (sg.j0 + i) * kBlockKeys;
-        if (warp == 12 && i + 1 < sg.steps) fetch_scales(i + 1);
+        const int key0 = (j0 + i) * kBlockKeys;
+        if (warp == 12 && i + 1 < steps) fetch_scales(i + 1);
         ValueRow<D> x;
         ok = mbar_wait_warp(&sh.r_full[rs], (c / C::kSR) & 1, p.status, 0x2B);
         if (!ok) break;
         x.load(sR + rs * C::kRaw, tid);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.r_empty[rs]);
-        if (key0 + tid >= sg.len) x.clear();
+        if (key0 + tid >= len) x.clear();
         ok = mbar_wait_warp(&sh.v_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x2C);
         if (!ok) break;
         if (key0 + kBlockKeys > least && x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
-        if (warp == 12 && i + 1 < sg.steps) put_scales(i + 1);
+        if (warp == 12 && i + 1 < steps) put_scales(i + 1);
         x.store(sV + (c & 1) * TV::kBytes, tid);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full[c & 1]);
       }
-      gi += sg.steps;
-      if (!ok || pl.start + chunks_of(geo, pl.keys) >= u1) break;
-      next_place(geo, pl);
+      if (!ok) break;
+      gi += steps;
+      const bool last = sg.last;
+      done_seg(seg);
+      if (last) break;
     }
   } else {
     // ---------------------------------------------------------------- softmax of row tile t
@@ -451,20 +502,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gi = 0, s_phase = 0, o_phase = 0, h_phase = 0;
     bool ok = true;
     for (int seg = 0;; ++seg) {
-      const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+      ok = next_seg(seg);
+      if (!ok) break;
+      const Seg& sg = sh.seg[seg & 3];
       const int row = sg.r0 + (split ? 0 : t * kRows) + r;
       const int query = geo.query(row < geo.R ? row : 0);
       const bool real = row < geo.R && query < sg.cnt;
       const int lim = real ? query_keys(geo, sg.len, sg.cnt, query) : sg.len;
-      const int reach = t ? sg.reach[1] : sg.reach[0], least = t ? sg.least[1] : sg.least[0];
+      const int reach = sg.reach[t], least = sg.least[t], j0 = sg.j0;
       // The tile's blocks: all up to its reach, or every other one.
-      const int steps = min(sg.steps, reach - sg.j0);
-      const int i0 = split ? (sg.j0 + t) & 1 : 0, stride = split ? 2 : 1;
+      const int steps = min(sg.steps, reach - j0);
+      const int i0 = split ? (j0 + t) & 1 : 0, stride = split ? 2 : 1;
       const bool have = i0 < steps;
       float m = kNoMax, l = 0.0f, mul;  // mul: |c| log2(e) times the row's power of two
       {
         const uint16_t* qrow = row < geo.R ? p.q + geo.row_offset(sg.b, sg.hk, row) * D : nullptr;
-        const int e = scale_exp(qrow ? row_amax<kBf16, D>(qrow) : 0.0f);
+        const int e = scale_exp(row_amax<kBf16, D>(qrow));
         mul = fabsf(p.c2) * pow2(e);
         if (!split || t == 0) {
           ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
@@ -485,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1u;
         tc_fence_after();
         const Scales& sc = sh.scales[c & 3];
-        const int key0 = (sg.j0 + i) * kBlockKeys;
+        const int key0 = (j0 + i) * kBlockKeys;
         float sv[kBlockKeys];
         {
           uint32_t rr[kBlockKeys];
@@ -576,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_warp(&sh.h_free, h_phase ^ 1u, p.status, 0x2E);
           if (!ok) break;
           h_phase ^= 1u;
-#pragma unroll
+#pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t rr[32];
             tmem_ld32(tO + c0, rr);
@@ -630,9 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const bool write = row < geo.R;
+        const bool none = l == 0.0f || !real;  // a padding row, or one that sees no key
+        const float inv = 1.0f / l;
         const int64_t orow = geo.row_offset(sg.b, sg.hk, row);
         const int64_t prow = static_cast<int64_t>(sg.slot) * geo.tile + (row - sg.r0);
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t rr[32];
           __syncwarp();
@@ -653,22 +708,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               rr[k + 3] = __float_as_uint(fmaf(__uint_as_float(rr[k + 3]), f0, h.w * f1));
             }
           }
-          if (bad[c0 / 32]) {
+          uint32_t nan = 0;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            if (i == c0 / 32) nan = bad[i];
+          if (nan) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (bad[c0 / 32] >> k & 1u) rr[k] = 0x7FC00000u;
+              if (nan >> k & 1u) rr[k] = 0x7FC00000u;
           }
-          if (write) {
+          if (write && sg.whole) {
+            uint4 w[4];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 z = make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]),
-                                           __uint_as_float(rr[k + 2]), __uint_as_float(rr[k + 3]));
-              if (sg.whole)
-                write_out<kBf16, D, ByHead>(p, orow, c0 + k, z, l, m, real);
-              else
-                *reinterpret_cast<float4*>(p.part_z + prow * D + c0 + k) = z;
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                h[i] = none ? 0u : pack2<kBf16>(__uint_as_float(rr[8 * k + 2 * i]) * inv,
+                                                __uint_as_float(rr[8 * k + 2 * i + 1]) * inv);
+              w[k] = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(p.o + orow * D + c0 + 8 * k) = w[k];
             }
+          } else if (write) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(p.part_z + prow * D + c0 + k) =
+                  make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]), __uint_as_float(rr[k + 2]),
+                              __uint_as_float(rr[k + 3]));
           }
+        }
+        if (write && sg.whole) {
+          p.lse[orow] = none ? -INFINITY : kLn2 * (m + log2f(l));
+          if (none && real) raise_empty_row(p.status);
         }
         if (write && !sg.whole) *reinterpret_cast<float2*>(p.part_lm + prow * 2) = make_float2(l, m);
         tc_fence_before();
@@ -679,8 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       gi += sg.steps;
-      if (pl.start + chunks_of(geo, pl.keys) >= u1) break;
-      next_place(geo, pl);
+      const bool last = sg.last;
+      done_seg(seg);
+      if (last) break;
     }
   }
 
