@@ -85,6 +85,9 @@ struct Shared {
   Scales scales[4];                 // by block number mod 4
 };
 
+// Least factor of a score: 0 (c = 0) would turn masked scores, -inf, to NaN.
+constexpr float kLeastFactor = 1.17549435e-38f;
+
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -156,6 +159,72 @@ struct ValueRow {
     return any;
   }
 };
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+
+// A row's largest x of a block, from its raw scores: their factor is uniform and not negative in a
+// scale group.  kG: groups of a block that differ (1 where the cache's blocks are of 128 tokens).
+template <int kG>
+__device__ __forceinline__ float block_max(const float (&sv)[kBlockKeys], const Scales& sc, float mul) {
+  constexpr int kW = kBlockKeys / kG;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 0; k < kW; k += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = fmax3(a[e], sv[kW * g + k + 2 * e], sv[kW * g + k + 2 * e + 1]);
+    const float t = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+    mx = fmaxf(mx, fmaf(t, fmaxf(sc.k[g] * mul, kLeastFactor), sc.log2_v[g]));
+  }
+  return mx;
+}
+
+// P of the row under m into TMEM at tS (over the scores), two 16-bit values a word; returns the
+// row's sum of P / vs.
+template <int kG>
+__device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], const Scales& sc, float mul, float m,
+                                             uint32_t tS) {
+  constexpr int kW = kBlockKeys / kG;
+  float l = 0.0f;
+  float2 sum[2];
+#pragma unroll
+  for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const int key = c0 + k, g = key / kW;
+      const float f = fmaxf(sc.k[g] * mul, kLeastFactor), shift = sc.log2_v[g] - m;
+      if (key % kW == 0) sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+      const float2 x = fma2(make_float2(sv[key], sv[key + 1]), make_float2(f, f), make_float2(shift, shift));
+      const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+      sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pr);
+      pk[k / 2] = pack2<false>(pr.x, pr.y);
+      if ((key + 2) % kW == 0) {
+        const float2 s = add2(sum[0], sum[1]);
+        l = fmaf(s.x + s.y, sc.inv_v[g], l);
+      }
+    }
+    tmem_st16(tS + c0 / 2, pk);
+  }
+  return l;
+}
 
 // Largest finite magnitude of a query row (null: 0).  This and put_query_row run once a tile, and
 // their loops stay rolled: unrolled, fetching their instructions took longer than running them.
@@ -499,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = group - 1, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + t * kBlockKeys + lane_off, tO = tmem + 2 * kBlockKeys + t * D + lane_off;
+    const bool uniform = p.block >= kBlockKeys;  // one scale a block of keys
     uint32_t gi = 0, s_phase = 0, o_phase = 0, h_phase = 0;
     bool ok = true;
     for (int seg = 0;; ++seg) {
@@ -555,20 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kBlockKeys; ++k)
             if (k >= seen) sv[k] = -INFINITY;
         }
-        // Largest x of the row: the scores' factor is uniform and positive in a scale group.
-        float mx = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float a = fmax3(sv[16 * g], sv[16 * g + 1], sv[16 * g + 2]);
-          float b = fmax3(sv[16 * g + 3], sv[16 * g + 4], sv[16 * g + 5]);
-          a = fmax3(a, sv[16 * g + 6], sv[16 * g + 7]);
-          b = fmax3(b, sv[16 * g + 8], sv[16 * g + 9]);
-          a = fmax3(a, sv[16 * g + 10], sv[16 * g + 11]);
-          b = fmax3(b, sv[16 * g + 12], sv[16 * g + 13]);
-          a = fmax3(a, sv[16 * g + 14], sv[16 * g + 15]);
-          // a factor of 0 (c = 0) would turn masked scores to NaN
-          mx = fmaxf(mx, fmaf(fmaxf(a, b), fmaxf(sc.k[g] * mul, 1.17549435e-38f), sc.log2_v[g]));
-        }
+        const float mx = uniform ? block_max<1>(sv, sc, mul) : block_max<kGroups>(sv, sc, mul);
         float alpha = 1.0f;
         if (mx - m > kRaise) {
           const float mn = mx - kTop;
@@ -588,26 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         first = false;
-#pragma unroll
-        for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int g = c0 / 16 + h;
-            const float f = fmaxf(sc.k[g] * mul, 1.17549435e-38f), shift = sc.log2_v[g] - m;
-            float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float p0 = ex2(fmaf(sv[c0 + 16 * h + 2 * k], f, shift));
-              const float p1 = ex2(fmaf(sv[c0 + 16 * h + 2 * k + 1], f, shift));
-              a0 += p0;
-              a1 += p1;
-              pk[8 * h + k] = pack2<false>(p0, p1);
-            }
-            l = fmaf(a0 + a1, sc.inv_v[g], l);
-          }
-          tmem_st16(tS + c0 / 2, pk);
-        }
+        l += uniform ? block_probs<1>(sv, sc, mul, m, tS) : block_probs<kGroups>(sv, sc, mul, m, tS);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
