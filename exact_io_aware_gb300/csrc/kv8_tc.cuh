@@ -17,7 +17,7 @@
 // tile 1 then hands its state to tile 0 (through L2) at the end.  Either way the tensor core works on one
 // tile while the other's softmax runs.  Warpgroups:
 //   0  warps 0, 1: MMA issuers of the two tiles (per block j: P V of the block before, then
-//      S_j); warp 2: TMA producer of the code tiles of K and of V; warp 3: the run's tiles one
+//      S_j); warp 2: TMA producer of the code tiles of K and of V, and their scales; warp 3: the run's tiles one
 //      after another, as the other warps need to know them (Seg)
 //   1, 2  softmax of tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant); at a
 //      tile's start each also cuts its query row into terms
@@ -451,13 +451,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------ TMA producer
+      const int nblk = geo.cap / p.block;
       uint32_t gi = 0;
       bool ok = true;
       for (int seg = 0;; ++seg) {
         ok = next_seg(seg);
         if (!ok) break;
         const Seg& sg = sh.seg[seg & 3];
-        const int bh = sg.b * geo.Hk + sg.hk, steps = sg.steps, j0 = sg.j0;
+        const int bh = sg.b * geo.Hk + sg.hk, steps = sg.steps, j0 = sg.j0, len = sg.len;
+        const float* ksp = p.k_scales + static_cast<int64_t>(bh) * nblk;
+        const float* vsp = p.v_scales + static_cast<int64_t>(bh) * nblk;
+        // A block's scales, one lane to 16 keys, fetched a block ahead.  Their place's last readers
+        // were softmax four blocks ago; the scores of two blocks ago (k_empty) came after P V of
+        // those.
+        float ks, vs;
+        auto fetch = [&](int i) {
+          const int key = (j0 + i) * kBlockKeys + lane * 16;
+          const bool in = lane < kGroups && key < len;
+          ks = in ? __ldg(ksp + key / p.block) : 1.0f;
+          vs = in ? __ldg(vsp + key / p.block) : 1.0f;
+        };
+        fetch(0);
         for (int i = 0; i < steps && ok; ++i) {
           const uint32_t c = gi + i, rs = c % C::kSR;
           const int key0 = (j0 + i) * kBlockKeys;
@@ -467,6 +481,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&sh.k_full[c & 1], T8::kBytes);
             tma_load_3d(sK + (c & 1) * T8::kBytes, &tm_k, &sh.k_full[c & 1], 0, key0, bh);
           }
+          if (lane < kGroups) {
+            Scales& sc = sh.scales[c & 3];
+            sc.k[lane] = ks;
+            sc.log2_v[lane] = log2f(vs);
+            sc.inv_v[lane] = 1.0f / vs;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.sc_full[c & 3]);
           ok = mbar_wait_warp(&sh.r_empty[rs], ((c / C::kSR) & 1) ^ 1, p.status, 0x28);
           if (!ok) break;
           if (lane == 0) {
@@ -474,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(sR + rs * C::kRaw, &tm_v, &sh.r_full[rs], 0, key0, bh);
           }
           __syncwarp();
+          if (i + 1 < steps) fetch(i + 1);
         }
         if (!ok) break;
         gi += steps;
@@ -500,61 +523,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- converters
     regs_dec<kRegsConvert>();
     const int tid = threadIdx.x - 3 * 128;
-    const int nblk = geo.cap / p.block;
     uint32_t gi = 0;
     for (int seg = 0;; ++seg) {
       bool ok = next_seg(seg);
       if (!ok) break;
       const Seg& sg = sh.seg[seg & 3];
-      const int64_t bh = static_cast<int64_t>(sg.b) * geo.Hk + sg.hk;
-      const float* ksp = p.k_scales + bh * nblk;
-      const float* vsp = p.v_scales + bh * nblk;
       const int steps = sg.steps, j0 = sg.j0, len = sg.len, least = min(sg.least[0], sg.least[1]);
-      // Scales of block i by the first warp, written a block ahead of V.  The place's last readers
-      // were softmax four blocks ago, which P V of two blocks ago (v_empty) came after.
-      float ks = 1.0f, vs = 1.0f;
-      auto fetch_scales = [&](int i) {
-        const int key = (j0 + i) * kBlockKeys + tid * 16;
-        ks = vs = 1.0f;
-        if (tid < kGroups && key < len) {
-          ks = __ldg(ksp + key / p.block);
-          vs = __ldg(vsp + key / p.block);
-        }
-      };
-      auto put_scales = [&](int i) {
-        const uint32_t c = gi + i;
-        if (tid < kGroups) {
-          Scales& sc = sh.scales[c & 3];
-          sc.k[tid] = ks;
-          sc.log2_v[tid] = log2f(vs);
-          sc.inv_v[tid] = 1.0f / vs;
-        }
-        __syncwarp();
-        if (tid == 0) mbar_arrive(&sh.sc_full[c & 3]);
-      };
-      if (warp == 12) {
-        fetch_scales(0);
-        put_scales(0);
-      }
-      for (int i = 0; i < steps; ++i) {
+      // Block i + 1's codes are read from their stage while block i's tile is being written.
+      ValueRow<D> x;
+      auto take = [&](int i) -> bool {
         const uint32_t c = gi + i, rs = c % C::kSR;
-        const int key0 = (j0 + i) * kBlockKeys;
-        if (warp == 12 && i + 1 < steps) fetch_scales(i + 1);
-        ValueRow<D> x;
-        ok = mbar_wait_warp(&sh.r_full[rs], (c / C::kSR) & 1, p.status, 0x2B);
-        if (!ok) break;
+        if (!mbar_wait_warp(&sh.r_full[rs], (c / C::kSR) & 1, p.status, 0x2B)) return false;
         x.load(sR + rs * C::kRaw, tid);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.r_empty[rs]);
-        if (key0 + tid >= len) x.clear();
+        return true;
+      };
+      ok = take(0);
+      for (int i = 0; i < steps && ok; ++i) {
+        const uint32_t c = gi + i;
+        const int key0 = (j0 + i) * kBlockKeys;
         ok = mbar_wait_warp(&sh.v_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x2C);
         if (!ok) break;
-        if (key0 + kBlockKeys > least && x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
-        if (warp == 12 && i + 1 < steps) put_scales(i + 1);
+        if (key0 + kBlockKeys > least) {
+          if (key0 + tid >= len) x.clear();
+          if (x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
+        }
         x.store(sV + (c & 1) * TV::kBytes, tid);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full[c & 1]);
+        if (i + 1 < steps) ok = take(i + 1);
       }
       if (!ok) break;
       gi += steps;
