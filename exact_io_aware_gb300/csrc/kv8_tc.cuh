@@ -20,7 +20,7 @@
 //      S_j); warp 2: TMA producer of the code tiles of K and of V, and their scales; warp 3: the run's tiles one
 //      after another, as the other warps need to know them (Seg)
 //   1, 2  softmax of tile 0 and 1: one thread a row (TMEM lane of the warp's quadrant); at a
-//      tile's start each also cuts its query row into terms
+//      tile's start all of them cut the queries into terms
 //   3  converters: one thread a key, its V codes into an fp16 tile
 // S and P share TMEM columns; O stays in TMEM for the length of a tile.
 //
@@ -82,6 +82,7 @@ struct Shared {
   bool idle;                        // nothing to do for this CTA
   uint32_t nan_seen[4];             // by tile number mod 4: a masked block's V held NaN codes
                                     // (cleared two tiles ahead, where its last reader is done)
+  float row_mul[2][2 * kRows];      // by tile number mod 2: what put_queries leaves
   Scales scales[4];                 // by block number mod 4
 };
 
@@ -226,65 +227,54 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
   return l;
 }
 
-// Largest finite magnitude of a query row (null: 0).  This and put_query_row run once a tile, and
-// their loops stay rolled: unrolled, fetching their instructions took longer than running them.
+// The queries of a tile (rows of q from `q` on, `rows` of them; the tile's others are zeros) as
+// E4M3 terms, by 256 threads: D / 16 lanes a row.  Row r's terms go to the tiles of row tile
+// r / 128 and its factor, c2 times the power of two taken out, to row_mul[r].  The loop stays
+// rolled: unrolled, fetching its instructions once a tile took longer than running them.
 template <bool kBf16, int D>
-__device__ __forceinline__ float row_amax(const uint16_t* q) {
-  float amax = 0.0f;
-  if (q) {
-#pragma unroll 1
-    for (int i = 0; i < D / 8; i += 8) {
-      uint4 u[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i + k);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack16<kBf16>(w[e]);
-          amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
-        }
-      }
-    }
-  }
-  return amax;
-}
-
-// Row r of a tile's terms: q times mul, cut into E4M3 values (q null: zeros).
-template <bool kBf16, int D>
-__device__ __forceinline__ void put_query_row(uint8_t* terms, int r, const uint16_t* q, float mul) {
+__device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, const uint16_t* q, int rows,
+                                            int tile, float c2, int tid) {
   using C = Config<kBf16, D>;
   using T8 = typename C::T8;
+  constexpr int kLanes = D / 16;
 #pragma unroll 1
-  for (int i = 0; i < D / 16; ++i) {
+  for (int idx = tid; idx < tile * kLanes; idx += 2 * kRows) {
+    const int row = idx / kLanes, piece = idx % kLanes;
     uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (q) {
-      u[0] = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i);
-      u[1] = __ldg(reinterpret_cast<const uint4*>(q) + 2 * i + 1);
+    if (row < rows) {
+      const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(row) * D + piece * 16);
+      u[0] = __ldg(src);
+      u[1] = __ldg(src + 1);
     }
     const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-    float x[16];
+    float x[16], amax = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float2 f = unpack16<kBf16>(w[e]);
-      x[2 * e] = nan_unless_finite(f.x) * mul;
-      x[2 * e + 1] = nan_unless_finite(f.y) * mul;
+      x[2 * e] = f.x, x[2 * e + 1] = f.y;
+      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
     }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const int e = scale_exp(amax);
+    const float mul = c2 < 0.0f ? -pow2(-e) : pow2(-e);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = nan_unless_finite(x[i]) * mul;
+    uint8_t* dst = terms + row / kRows * C::kTerms * T8::kBytes + T8::offset(row % kRows, 8 * piece);
 #pragma unroll 1
     for (int term = 0; term < C::kTerms; ++term) {
       uint32_t c[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        c[e] = pack4_e4m3(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+      for (int i = 0; i < 4; ++i) {
+        c[i] = pack4_e4m3(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         float y[4];
-        codes_to_float4(c[e], y);
+        codes_to_float4(c[i], y);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[4 * e + k] -= y[k];  // exact
+        for (int k = 0; k < 4; ++k) x[4 * i + k] -= y[k];  // exact
       }
-      *reinterpret_cast<uint4*>(terms + term * T8::kBytes + T8::offset(r, 8 * i)) =
-          make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint4*>(dst + term * T8::kBytes) = make_uint4(c[0], c[1], c[2], c[3]);
     }
+    if (piece == 0) row_mul[row] = fabsf(c2) * pow2(e);
   }
 }
 
@@ -317,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    mbar_init(&sh.q_full, split ? 4 : 8);
+    mbar_init(&sh.q_full, 8);
     mbar_init(&sh.q_free, 2);
     mbar_init(&sh.h_full, 4);
     mbar_init(&sh.h_free, 4);
@@ -583,21 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = min(sg.steps, reach - j0);
       const int i0 = split ? (j0 + t) & 1 : 0, stride = split ? 2 : 1;
       const bool have = i0 < steps;
-      float m = kNoMax, l = 0.0f, mul;  // mul: |c| log2(e) times the row's power of two
-      {
-        const uint16_t* qrow = row < geo.R ? p.q + geo.row_offset(sg.b, sg.hk, row) * D : nullptr;
-        const int e = scale_exp(row_amax<kBf16, D>(qrow));
-        mul = fabsf(p.c2) * pow2(e);
-        if (!split || t == 0) {
-          ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
-          if (!ok) break;
-          if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
-          put_query_row<kBf16, D>(sQ + t * C::kTerms * T8::kBytes, r, qrow, p.c2 < 0.0f ? -pow2(-e) : pow2(-e));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full);
-        }
-      }
+      float m = kNoMax, l = 0.0f, mul = 0.0f;  // mul: |c| log2(e) times the row's power of two
+      ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
+      if (!ok) break;
+      if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
+      put_queries<kBf16, D>(sQ, sh.row_mul[seg & 1], p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D,
+                            geo.R - sg.r0, geo.tile, p.c2, t * kRows + r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
       bool first = true;
       for (int i = i0; i < steps; i += stride) {
         const uint32_t c = gi + i;
@@ -606,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after();
+        if (first) mul = sh.row_mul[seg & 1][row - sg.r0];
         const Scales& sc = sh.scales[c & 3];
         const int key0 = (j0 + i) * kBlockKeys;
         float sv[kBlockKeys];
