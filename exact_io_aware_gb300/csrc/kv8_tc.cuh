@@ -54,6 +54,7 @@ struct Config {
   static constexpr int kOffV = kOffK + kSK * T8::kBytes;
   static constexpr int kOffR = kOffV + kSV * TV::kBytes;
   static constexpr int kOffShared = kOffR + kSR * kRaw;
+  static_assert(kOffShared % 16 == 0, "the shared block is misaligned");
 };
 
 // One tile of the run, as every role sees it.

@@ -283,7 +283,7 @@ def test_attend_offsets_past_32_bits():
 # ------------------------------------------------------------------ weights
 
 @pytest.mark.parametrize("dtype,d,block", [("bf16", 128, 64), ("f16", 64, 16), ("bf16", 64, 32)])
-@pytest.mark.parametrize("G,n", [(1, 1), (4, 1), (3, 5), (4, 32), (5, 60)])
+@pytest.mark.parametrize("G,n", [(1, 1), (4, 1), (3, 5), (4, 6), (33, 1), (4, 32), (5, 33), (5, 60), (8, 70)])
 @pytest.mark.parametrize("mask", ["none", "causal"])
 def test_weights(dtype, d, block, G, n, mask):
     lengths = [0, 1, 16, 33, 127, 129, 255, 384]
