@@ -21,7 +21,7 @@ using tc::kRows;
 constexpr int kThreads = 384;
 constexpr int kStages = 4;      // of K tiles
 constexpr int kMostRows = 256;  // held at once
-constexpr int kCols = 16;       // rows whose scores a thread takes from tensor memory at once
+constexpr int kCols = 16;       // rows that are looked at for masks together
 
 struct Shared {
   uint64_t q_full, q_free;
@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem_base;  // accumulator of key warps w, row tile rt at 128 (2 w + rt)
 
   // Every role walks the same tiles, and in each the same groups of rows and blocks of keys.
+  const int block_shift = 31 - __clz(p.block);
   bool ok = true;
   uint32_t c = 0, part = 0;        // blocks and groups of rows so far
   uint32_t use[2][2] = {{0, 0}, {0, 0}};  // uses of each accumulator so far
@@ -165,12 +166,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sh.q_full);
         ok = mbar_wait_warp(&sh.q_full, part & 1, p.status, 0x38);
         const float* w_in = r0 ? p.w_out : p.w_in;  // later passes add to the first's
-        for (int j = j0 + ((j0 & 1) != w ? 1 : 0); j < j1 && ok; j += 2) {
+        // A key's scale and sum so far are fetched a block ahead.
+        float next_kf = 0.0f, next_before = 0.0f;
+        auto fetch = [&](int j) {
+          const int key = j * kBlockKeys + key_lane;
+          const bool in = j < j1 && key < len;
+          next_kf = in ? __ldg(p.k_scales + bh * (geo.cap >> block_shift) + (key >> block_shift)) : 0.0f;
+          next_before = in && w_in ? w_in[bh * geo.cap + key] : 0.0f;
+        };
+        int j = j0 + ((j0 & 1) != w ? 1 : 0);
+        fetch(j);
+        for (; j < j1 && ok; j += 2) {
           const int key0 = j * kBlockKeys, key = key0 + key_lane;
           const bool held = key < len;
-          const float kf = held ? __ldg(p.k_scales + bh * (geo.cap / p.block) + key / p.block) : 0.0f;
-          const float before = held && w_in ? w_in[bh * geo.cap + key] : 0.0f;
-          float sum[2] = {0.0f, 0.0f};
+          const float kf = next_kf, before = next_before;
+          fetch(j + 2);
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int rt = 0; rt < tiles; ++rt) {
             ok = mbar_wait_warp(&sh.s_full[w][rt], use[w][rt] & 1, p.status, 0x37);
             if (!ok) break;
@@ -178,29 +189,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tS = tmem + 128 * (2 * w + rt) + lane_off;
             const int groups = (min(kRows, rows - rt * kRows) + kCols - 1) / kCols;
-            uint32_t s[2][kCols];
-            tmem_ld16(tS, s[0]);
-#pragma unroll 2
-            for (int gr = 0; gr < groups; ++gr) {
+            // 64 rows' scores at a time: shorter loads from tensor memory left its latency bare.
+            for (int g0 = 0; g0 < groups; g0 += 4) {
+              uint32_t s[64];
+              tmem_ld32(tS + g0 * kCols, *reinterpret_cast<uint32_t(*)[32]>(s));
+              if (g0 + 2 < groups) tmem_ld32(tS + g0 * kCols + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
               tmem_wait_ld();
-              if (gr + 1 < groups) tmem_ld16(tS + (gr + 1) * kCols, s[(gr + 1) & 1]);
-              const int col = rt * kRows + gr * kCols;
-              const uint32_t (&x)[kCols] = s[gr & 1];
-              if (key0 + kBlockKeys <= sh.least[col / kCols]) {
 #pragma unroll
-                for (int k = 0; k < kCols; k += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(&sh.row_mul[col + k]);
-                  const float4 b = *reinterpret_cast<const float4*>(&sh.neg_lse[col + k]);
-                  sum[0] += ex2(fmaf(__uint_as_float(x[k]) * kf, f.x, b.x));
-                  sum[1] += ex2(fmaf(__uint_as_float(x[k + 1]) * kf, f.y, b.y));
-                  sum[0] += ex2(fmaf(__uint_as_float(x[k + 2]) * kf, f.z, b.z));
-                  sum[1] += ex2(fmaf(__uint_as_float(x[k + 3]) * kf, f.w, b.w));
-                }
-              } else {  // some row does not see all of the block, or counts for nothing
+              for (int i = 0; i < 4; ++i) {
+                if (g0 + i >= groups) break;
+                const int col = rt * kRows + (g0 + i) * kCols;
+                const uint32_t* x = s + i * kCols;
+                if (key0 + kBlockKeys <= sh.least[col / kCols]) {
 #pragma unroll
-                for (int k = 0; k < kCols; ++k) {
-                  const float e = ex2(fmaf(__uint_as_float(x[k]) * kf, sh.row_mul[col + k], sh.neg_lse[col + k]));
-                  sum[k & 1] += key < sh.lim[col + k] ? e : 0.0f;
+                  for (int k = 0; k < kCols; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sh.row_mul[col + k]);
+                    const float4 b = *reinterpret_cast<const float4*>(&sh.neg_lse[col + k]);
+                    sum[0] += ex2(fmaf(__uint_as_float(x[k]) * kf, f.x, b.x));
+                    sum[1] += ex2(fmaf(__uint_as_float(x[k + 1]) * kf, f.y, b.y));
+                    sum[2] += ex2(fmaf(__uint_as_float(x[k + 2]) * kf, f.z, b.z));
+                    sum[3] += ex2(fmaf(__uint_as_float(x[k + 3]) * kf, f.w, b.w));
+                  }
+                } else {  // some row does not see all of the block, or counts for nothing
+#pragma unroll
+                  for (int k = 0; k < kCols; ++k) {
+                    const float e = ex2(fmaf(__uint_as_float(x[k]) * kf, sh.row_mul[col + k], sh.neg_lse[col + k]));
+                    sum[k & 3] += key < sh.lim[col + k] ? e : 0.0f;
+                  }
                 }
               }
             }
@@ -208,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.s_empty[w][rt]);
           }
-          if (ok && held) p.w_out[bh * geo.cap + key] = before + (sum[0] + sum[1]);
+          if (ok && held) p.w_out[bh * geo.cap + key] = before + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_free);
