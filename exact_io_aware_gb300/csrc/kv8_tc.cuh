@@ -229,17 +229,17 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
 }
 
 // The queries of a tile (rows of q from `q` on, `rows` of them; the tile's others are zeros) as
-// E4M3 terms, by 256 threads: D / 16 lanes a row.  Row r's terms go to the tiles of row tile
+// E4M3 terms, by kN threads (tid): D / 16 lanes a row.  Row r's terms go to the tiles of row tile
 // r / 128 and its factor, c2 times the power of two taken out, to row_mul[r].  The loop stays
 // rolled: unrolled, fetching its instructions once a tile took longer than running them.
-template <bool kBf16, int D>
+template <bool kBf16, int D, int kN>
 __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, const uint16_t* q, int rows,
                                             int tile, float c2, int tid) {
   using C = Config<kBf16, D>;
   using T8 = typename C::T8;
   constexpr int kLanes = D / 16;
 #pragma unroll 1
-  for (int idx = tid; idx < tile * kLanes; idx += 2 * kRows) {
+  for (int idx = tid; idx < tile * kLanes; idx += kN) {
     const int row = idx / kLanes, piece = idx % kLanes;
     uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (row < rows) {
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
       if (!ok) break;
       if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
-      put_queries<kBf16, D>(sQ, sh.row_mul[seg & 1], p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D,
+      put_queries<kBf16, D, 2 * kRows>(sQ, sh.row_mul[seg & 1], p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D,
                             geo.R - sg.r0, geo.tile, p.c2, t * kRows + r);
       fence_proxy_async_smem();
       __syncwarp();
