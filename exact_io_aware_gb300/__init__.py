@@ -13,6 +13,7 @@ CPU or PyTorch fallback, and every entry point raises if the library is not buil
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -381,11 +382,10 @@ _KV8_INPUTS = (torch.float16, torch.bfloat16)
 
 
 def _kv8_array(t, dtype, shape, name, device):
-    """The address of t, a contiguous tensor of the given type and shape on the call's device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must lie on the call's device, {device}")
+    """The address of t, a contiguous tensor of the given type and shape on CUDA device ``device``."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous tensor {list(shape)} of {dtype} on CUDA "
+                         f"device {device}")
     return t.data_ptr()
 
 
@@ -406,7 +406,7 @@ def _kv8_optional(t, dtype, shape, name, device):
 
 
 def _kv8_shape(k8, k_scales):
-    """(B, H_kv, cap, d, block, device) from the codes [B,H_kv,cap,d] and scales [B,H_kv,cap/block]."""
+    """(B, H_kv, cap, d, block, device index) from the codes [B,H_kv,cap,d] and scales [B,H_kv,cap/block]."""
     if not k8.is_cuda:
         raise ValueError("the 8-bit cache must be CUDA tensors")
     if k8.dim() != 4 or k_scales.dim() != 3:
@@ -415,7 +415,7 @@ def _kv8_shape(k8, k_scales):
     nblk = k_scales.shape[2]
     if nblk < 1 or cap % nblk:
         raise ValueError("scales must be [B,H_kv,cap/block]")
-    return B, Hk, cap, d, cap // nblk, k8.device
+    return B, Hk, cap, d, cap // nblk, k8.get_device()
 
 
 def _kv8_heads(q, B, Hk, mask):
@@ -425,13 +425,13 @@ def _kv8_heads(q, B, Hk, mask):
 
 
 class _On:
-    """The call's device made current for a call, and its stream: what is allocated inside belongs
-    to the stream the kernels run on.  Yields the stream's handle."""
+    """A call's device made current for it, and its stream: what is allocated inside belongs to the
+    stream the kernels run on.  Yields the stream's handle."""
 
     __slots__ = ("index", "stream", "was")
 
-    def __init__(self, device, stream):
-        self.index, self.stream, self.was = device.index, stream, None
+    def __init__(self, index, stream):
+        self.index, self.stream, self.was = index, stream, None
 
     def __enter__(self):
         was = torch.cuda.current_device()
@@ -448,6 +448,13 @@ class _On:
             self.stream.__exit__(*exc)
         if self.was is not None:
             torch.cuda.set_device(self.was)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv8_workspace(code, B, H, Hk, n, d, cap, device):
+    """attn_fwd_kv8_workspace_bytes on the current device, which is ``device`` (a function of these
+    sizes alone)."""
+    return int(load().attn_fwd_kv8_workspace_bytes(code, B, H, Hk, n, d, cap))
 
 
 def attn_kv8_append(k_new, v_new, k8, v8, k_scales, v_scales, lengths, counts=None, weights=None,
@@ -507,10 +514,10 @@ def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="n
         else:
             _kv8_array(lse, f32, (B, H, n), "lse", dev)
         if workspace is None:
-            size = lib.attn_fwd_kv8_workspace_bytes(code, B, H, Hk, n, d, cap)
+            size = _kv8_workspace(code, B, H, Hk, n, d, cap, dev)
             if size > 0:
                 workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the call's device")
         else:
             size = workspace.numel() * workspace.element_size()
@@ -550,9 +557,9 @@ def attn_kv8_evict(k8, v8, k_scales, v_scales, weights, lengths, keep, k8_out, v
     the heaviest of the rest by ``weights``, in order, ``keep`` at most.  Returns the kept
     positions, int32 [B,H_kv,keep], -1 past the new length."""
     B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
-    cap_out, keep, f32, i32 = k8_out.shape[2], int(keep), torch.float32, torch.int32
-    if cap_out % block:
+    if k8_out.dim() != 4 or k8_out.shape[2] % block:
         raise ValueError("the output cache's capacity must be a multiple of the block")
+    cap_out, keep, f32, i32 = k8_out.shape[2], int(keep), torch.float32, torch.int32
 
     def cache(k, v, ks, vs, w, lens, m):
         return ((_kv8_codes(k, (B, Hk, m, d), "k8", dev), _kv8_codes(v, (B, Hk, m, d), "v8", dev),

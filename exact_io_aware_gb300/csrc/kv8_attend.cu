@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
   uint8_t* ring = smem + warp * (kStages * stage_bytes<D>());
   const int nblk = geo.cap / p.block;
 
-  int64_t u0, u1;
+  int u0, u1;
   Place pl;
   if (p.ctas > 0) {
     pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
   }
   for (;;) {
     const int tile_chunks = chunks_of(geo, pl.keys);
-    const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
-    const int c1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(tile_chunks)));
+    const int c0 = max(u0 - pl.start, 0);
+    const int c1 = min(u1 - pl.start, tile_chunks);
     if (p.ctas > 0 && c0 == 0 && pl.start >= u0 && threadIdx.x == 0) note_run(p, pl, u0, u1);
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
     const int64_t bh = static_cast<int64_t>(pl.b) * geo.Hk + pl.hk;
@@ -448,6 +448,11 @@ kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int ctas, int min_chunks)
 
 int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   const int64_t R = static_cast<int64_t>(a.G) * a.n;
+  const int tiles = static_cast<int>((R + rows_per_tile(R) - 1) / rows_per_tile(R));
+  if (kv8::list_too_long(a.B, a.Hk, tiles, a.cap, R > kFewRows ? kv8::kBlockKeys : kv8::kChunk)) {
+    err = "B * H * n_q * cap is too large for one call";
+    return -2;
+  }
   cudaError_t e;
   if (R > kFewRows) {
     auto p = attend_params<kv8::ByHead>(a, a.sms, 2);

@@ -54,10 +54,10 @@ __device__ __forceinline__ void write_out(const AttendParams<Geo>& p, int64_t ro
 
 // The CTA that holds a tile's first chunk notes which CTAs share it (u0, u1: its run).
 template <class Geo>
-__device__ __forceinline__ void note_run(const AttendParams<Geo>& p, const Place& pl, int64_t u0, int64_t u1) {
-  const int64_t per = u1 - u0;  // a run that ends before its length is the last
-  const int64_t end = pl.start + chunks_of(p.geo, pl.keys);
-  const int more = end > u1 ? static_cast<int>((end - u1 + per - 1) / per) : 0;
+__device__ __forceinline__ void note_run(const AttendParams<Geo>& p, const Place& pl, int u0, int u1) {
+  const int per = u1 - u0;  // a run that ends before its length is the last
+  const int end = pl.start + chunks_of(p.geo, pl.keys);
+  const int more = end > u1 ? (end - u1 + per - 1) / per : 0;
   const int64_t id = (static_cast<int64_t>(pl.b) * p.geo.Hk + pl.hk) * p.geo.tiles + pl.rt;
   p.runs[id] = make_int2(blockIdx.x, blockIdx.x + more);
 }

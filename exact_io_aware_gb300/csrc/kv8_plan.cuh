@@ -73,15 +73,15 @@ __device__ __forceinline__ int chunks_of(const Geo&, int keys) {
 
 // Chunks of all row tiles of one head of sequence b.
 template <class Geo>
-__device__ __forceinline__ int64_t head_chunks(const Geo& g, int b) {
+__device__ __forceinline__ int head_chunks(const Geo& g, int b) {
   const int len = seq_len(g.lengths, b, g.cap), cnt = seq_count(g.counts, b, g.n);
   if (g.tiles == 1) return chunks_of(g, tile_keys(g, len, cnt, 0));
-  int64_t u = 0;
+  int u = 0;
   for (int rt = 0; rt < g.tiles; ++rt) u += chunks_of(g, tile_keys(g, len, cnt, rt));
   return u;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+__device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
@@ -89,12 +89,18 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 
 struct Place {
   int b, hk, rt;
-  int keys;       // keys of the tile
-  int64_t start;  // work-list index of the tile's first chunk
+  int keys;   // keys of the tile
+  int start;  // work-list index of the tile's first chunk
 };
 
-__device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int min_chunks) {
-  const int64_t per = (total + ctas - 1) / ctas;
+// Whether a call's work list could outgrow the 32-bit arithmetic on it (its chunks if every
+// sequence were full; far more than a cache in memory has, unless its queries are many).
+inline bool list_too_long(int B, int Hk, int tiles, int cap, int step) {
+  return static_cast<double>(B) * Hk * tiles * ((cap + step - 1) / step) >= static_cast<double>(1 << 30);
+}
+
+__device__ __forceinline__ int run_length(int total, int ctas, int min_chunks) {
+  const int per = (total + ctas - 1) / ctas;
   return per < min_chunks ? min_chunks : per;
 }
 
@@ -102,24 +108,24 @@ __device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int min_c
 // whole warps; lanes take a sequence each.
 template <class Geo>
 __device__ __forceinline__ Place plan_run(const Geo& g, int cta, int ctas, int min_chunks,
-                                          int64_t& u0, int64_t& u1) {
+                                          int& u0, int& u1) {
   const int lane = lane_id();
-  const int64_t v0 = lane < g.B ? head_chunks(g, lane) * g.Hk : 0;
-  int64_t sum = v0;
+  const int v0 = lane < g.B ? head_chunks(g, lane) * g.Hk : 0;
+  int sum = v0;
   for (int b = lane + 32; b < g.B; b += 32) sum += head_chunks(g, b) * g.Hk;
-  const int64_t total = warp_sum(sum);
-  const int64_t per = run_length(total, ctas, min_chunks);
+  const int total = warp_sum(sum);
+  const int per = run_length(total, ctas, min_chunks);
   u0 = cta * per;
   u1 = min(u0 + per, total);
   Place p{0, 0, 0, 0, 0};
   if (u0 >= u1) return p;
-  int64_t base = 0, head = 0;
+  int base = 0, head = 0;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int64_t v = b0 == 0 ? v0 : b0 + lane < g.B ? head_chunks(g, b0 + lane) * g.Hk : 0;
-    int64_t x = v;
+    const int v = b0 == 0 ? v0 : b0 + lane < g.B ? head_chunks(g, b0 + lane) * g.Hk : 0;
+    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
     const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + x > u0);
@@ -133,7 +139,7 @@ __device__ __forceinline__ Place plan_run(const Geo& g, int cta, int ctas, int m
     base += __shfl_sync(0xFFFFFFFFu, x, 31);
   }
   const int len = seq_len(g.lengths, p.b, g.cap), cnt = seq_count(g.counts, p.b, g.n);
-  p.hk = static_cast<int>((u0 - base) / head);
+  p.hk = (u0 - base) / head;
   base += p.hk * head;
   for (;; ++p.rt) {
     p.keys = tile_keys(g, len, cnt, p.rt);

@@ -95,15 +95,15 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-__device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int64_t u0, int64_t u1, int cta) {
+__device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int u0, int u1, int cta) {
   Seg s;
   s.b = pl.b, s.hk = pl.hk;
   s.len = seq_len(g.lengths, pl.b, g.cap);
   s.cnt = seq_count(g.counts, pl.b, g.n);
   s.r0 = pl.rt * g.tile;
   const int blocks = chunks_of(g, pl.keys);
-  s.j0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
-  const int j1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(blocks)));
+  s.j0 = max(u0 - pl.start, 0);
+  const int j1 = min(u1 - pl.start, blocks);
   s.steps = j1 - s.j0;
   s.whole = s.j0 == 0 && j1 == blocks;
   s.last = pl.start + blocks >= u1;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) raise_timeout(p.status, 0x20);
     return;
   }
-  int64_t u0 = 0, u1 = 0;
+  int u0 = 0, u1 = 0;
   Place pl{};
   if (warp == 3) {
     pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kWeightsThreads, weights_ctas_per_sm<NT>())
   constexpr int kStages = weights_stages<D, NT>();
   const int lane = lane_id(), warp = warp_id(), g = lane >> 2, t = lane & 3;
   const ByQuery& geo = p.geo;
-  int64_t u0, u1;
+  int u0, u1;
   Place pl = plan_run(geo, blockIdx.x, gridDim.x, kWeightsWarps, u0, u1);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < geo.B; b += kWeightsThreads)
@@ -44,8 +44,8 @@ __global__ void __launch_bounds__(kWeightsThreads, weights_ctas_per_sm<NT>())
 
   for (;;) {
     const int tile_chunks = chunks_of(geo, pl.keys);
-    const int c0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
-    const int c1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(tile_chunks)));
+    const int c0 = max(u0 - pl.start, 0);
+    const int c1 = min(u1 - pl.start, tile_chunks);
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
     const int64_t bh = static_cast<int64_t>(pl.b) * geo.Hk + pl.hk;
     const uint8_t* kp = p.k8 + bh * geo.cap * D;
@@ -195,6 +195,10 @@ kv8::WeightsParams<Geo> weights_params(const Kv8Args& a) {
 }  // namespace
 
 int launch_kv8_weights(const Kv8Args& a, cudaStream_t s, std::string& err) {
+  if (kv8::list_too_long(a.B, a.Hk, 1, a.cap, kv8::kChunk)) {
+    err = "B * H_kv * cap is too large for one call";
+    return -2;
+  }
   cudaError_t e;
   if (static_cast<int64_t>(a.G) * a.n > kFewRows) {
     const auto p = weights_params<kv8::ByHead>(a);

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) raise_timeout(p.status, 0x20);
     return;
   }
-  int64_t u0, u1;
+  int u0, u1;
   Place pl = plan_run(geo, blockIdx.x, gridDim.x, 2, u0, u1);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < geo.B; b += kThreads)
@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t use[kTeams] = {};       // uses of each accumulator so far
   for (;;) {
     const int blocks = chunks_of(geo, pl.keys);
-    const int j0 = static_cast<int>(max(u0 - pl.start, static_cast<int64_t>(0)));
-    const int j1 = static_cast<int>(min(u1 - pl.start, static_cast<int64_t>(blocks)));
+    const int j0 = max(u0 - pl.start, 0);
+    const int j1 = min(u1 - pl.start, blocks);
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
     const int64_t bh = static_cast<int64_t>(pl.b) * geo.Hk + pl.hk;
     for (int r0 = 0; r0 < geo.R && ok; r0 += kMostRows, ++part) {

@@ -244,7 +244,9 @@ int attn_fwd_fp8_blocks(int B, int H, int n, int d, float c,
  *                        rows) sequence b has; NULL is n for all.  Token i < counts[b] has the
  *                        position lengths[b] - counts[b] + i; rows i >= counts[b] are padding.
  *   weights              float32 [B][H_kv][cap]: accumulated attention weight of each token
- * d: 64 or 128; block: 16, 32, 64 or 128; cap: a multiple of block; B * H_kv at most 65535.
+ * d: 64 or 128; block: 16, 32, 64 or 128; cap: a multiple of block, at most 2^30; B * H_kv at
+ * most 65535; for attention and weights H / H_kv * n_q at most 2^24, and the steps of 32 keys
+ * (128 for more than 32 rows a key/value head) over all heads and tiles of rows below 2^30.
  * Scales must be positive and finite (those of blocks with no held token are not read); the
  * entry points below write powers of two, which E4M3, a floating-point format, loses no
  * precision to, so codes move between blocks exactly down to E4M3's subnormals.  What lies past
