@@ -25,6 +25,7 @@ constexpr int kSelThreads = 512;  // two CTAs and more fit a multiprocessor, so 
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 256;
 constexpr int kPasses = 4;
+constexpr int kMostRanks = 8;  // CTAs of a cluster (the portable size)
 constexpr int kMoveThreads = 256;
 
 struct EvictParams {
@@ -67,6 +68,7 @@ struct SelectSmem {
   uint32_t hist[kPasses][kBins];
   uint32_t red[kPasses][kSelWarps];
   uint32_t digit[kPasses], left[kPasses];
+  bool whole[kPasses];
   uint32_t above[kSelWarps], equal[kSelWarps];
   uint32_t total[2];
 };
@@ -100,7 +102,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictParam
   for (int i = tid; i < kPasses * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
   __syncthreads();
   uint32_t prefix = 0, left = want;
-#pragma unroll
+  int low = 0;  // bits of a key that were not needed
+#pragma unroll 1  // rolled: what a pass costs is the latency of its steps, instruction fetches among them
   for (int pass = 0; pass < kPasses; ++pass) {
     const int shift = 24 - 8 * pass;
     uint32_t* hist = sm.hist[pass];
@@ -114,18 +117,28 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictParam
     constexpr int kPer = kSelThreads / kBins;
     const int bin = kBins - 1 - tid / kPer;
     uint32_t h = 0;
-    for (int r = tid % kPer; r < ranks; r += kPer) h += cluster.map_shared_rank(hist, r)[bin];
+#pragma unroll
+    for (int i = 0; i < kMostRanks / kPer; ++i) {  // loads from other CTAs take long: all at once
+      const int r = i * kPer + tid % kPer;
+      if (r < ranks) h += cluster.map_shared_rank(hist, r)[bin];
+    }
 #pragma unroll
     for (int o = 1; o < kPer; o <<= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
     const uint32_t ex = block_scan(tid % kPer == 0 ? h : 0u, sm.red[pass]);
     if (tid % kPer == 0 && ex < left && left <= ex + h) {
       sm.digit[pass] = bin;
       sm.left[pass] = left - ex;
+      sm.whole[pass] = left == ex + h;
     }
     __syncthreads();
     if (want > 0) {
       prefix |= sm.digit[pass] << shift;
       left = sm.left[pass];
+    }
+    // The whole of the last bin is taken: its keys need no telling apart.
+    if (want > 0 && sm.whole[pass]) {
+      low = shift;
+      break;
     }
   }
   // Keys above `prefix` are kept, and the first `left` of those equal to it.  A warp takes
@@ -138,9 +151,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictParam
     if (i < p.sink || i >= len - p.recent) {
       above = true;
     } else if (want > 0) {
-      const uint32_t k = order_key(__ldg(w + i));
-      above = k > prefix;
-      equal = k == prefix;
+      const uint32_t k = order_key(__ldg(w + i)) >> low;
+      above = k > prefix >> low;
+      equal = k == prefix >> low;
     }
   };
   uint32_t na = 0, ne = 0;
@@ -162,10 +175,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictParam
     if (lane == 0) sm.total[0] = xa, sm.total[1] = xe;
   }
   sync_cluster();
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* t = cluster.map_shared_rank(sm.total, r);
-    ab += t[0];
-    eq += t[1];
+  {
+    uint32_t la = 0, le = 0;
+    if (lane < rank) {
+      const uint32_t* t = cluster.map_shared_rank(sm.total, lane);
+      la = t[0];
+      le = t[1];
+    }
+    ab += __reduce_add_sync(0xFFFFFFFFu, la);
+    eq += __reduce_add_sync(0xFFFFFFFFu, le);
   }
 #pragma unroll 2
   for (int i = w0; i < w1; i += 32) {
@@ -203,7 +221,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, uint32_t ratio2) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, D == 64 ? 6 : 4) evict_move_kernel(EvictParams p) {
   constexpr int kLanes = D / 16;           // lanes of one row (16 codes each)
   constexpr int kRowsIt = 32 / kLanes;
   constexpr int kIters = 16 / kRowsIt;
@@ -325,7 +343,7 @@ int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s, std::string& err) {
   // to look at and the clusters leave multiprocessors idle.
   const int heads = a.B * a.Hk;
   int ranks = 1;
-  while (ranks < 8 && a.cap > 4096 * ranks && heads * ranks * 2 <= 2 * a.sms) ranks *= 2;
+  while (ranks < kv8::kMostRanks && a.cap > 4096 * ranks && heads * ranks * 2 <= 2 * a.sms) ranks *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
