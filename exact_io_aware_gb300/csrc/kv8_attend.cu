@@ -7,8 +7,9 @@
 //     z_r = sum_j P_rj v_j,   l_r = sum_j P_rj / vs_j,   O_r = z_r / l_r,
 //     LSE_r = ln 2 (m_r + log2 l_r),
 // so a value block's scale costs one constant a block: P is what the product takes and z needs
-// no second scaling.  P is rounded to fp16 for that product (half a step is 2^-12, an eighth of
-// the bf16 output's); m_r is set so that the largest P is 2^6 and is raised only when a P would
+// no second scaling.  P enters that product as fp16 (half a step 2^-11, an eighth of the bf16
+// output's; for fp16 outputs, whose own rounding that would equal, as a pair of fp16 values and
+// two products); m_r is set so that the largest P is 2^6 and is raised only when a P would
 // pass 2^14, which keeps P inside fp16 and weights down to 2^-20 of the largest at full precision
 // (the sums z and l are float32).
 //
@@ -51,8 +52,8 @@ constexpr size_t merge_bytes() {
   return static_cast<size_t>(kAttendWarps) * NT * 8 * (merge_stride<D>() + 2) * sizeof(float);
 }
 
-// One chunk of 32 keys against the tile's rows.
-template <int D, int NT>
+// One chunk of 32 keys against the tile's rows.  kPair: P as a pair of fp16 values.
+template <int D, int NT, bool kPair>
 __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool masked, int block,
                                              float kmul, const QFrag<D> (&q)[NT],
                                              const int (&lim)[NT][2], float (&z)[NT][D / 16][4],
@@ -104,7 +105,7 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     uint32_t b0[NT], b1[NT];
-    [[maybe_unused]] uint32_t seen0[NT], seen1[NT];
+    uint32_t lo0[kPair ? NT : 1], lo1[kPair ? NT : 1];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float pr[4];
@@ -113,8 +114,14 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
         pr[e] = ex2(x[mt][j][e] - m[j][e & 1]);
         l[j][e & 1] = fmaf(pr[e], inv_vs[mt], l[j][e & 1]);
       }
-      b0[j] = transpose8x8(pack_f16(pr[0], pr[1]));
-      b1[j] = transpose8x8(pack_f16(pr[2], pr[3]));
+      const uint32_t h0 = pack_f16(pr[0], pr[1]), h1 = pack_f16(pr[2], pr[3]);
+      b0[j] = transpose8x8(h0);
+      b1[j] = transpose8x8(h1);
+      if constexpr (kPair) {
+        const float2 u = unpack16<false>(h0), v = unpack16<false>(h1);
+        lo0[j] = transpose8x8(pack_f16(pr[0] - u.x, pr[1] - u.y));
+        lo1[j] = transpose8x8(pack_f16(pr[2] - v.x, pr[3] - v.y));
+      }
     }
     // V rows of the slots 2t, 2t + 1 (of the lower, then the upper eight keys).
     uint32_t v[4][D / 32];
@@ -180,6 +187,10 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
       for (int j = 0; j < NT; ++j) {
         mma_f16(z[j][2 * w], a0, a1, a2, a3, b0[j], b1[j]);
         mma_f16(z[j][2 * w + 1], c0, c1, c2, c3, b0[j], b1[j]);
+        if constexpr (kPair) {
+          mma_f16(z[j][2 * w], a0, a1, a2, a3, lo0[j], lo1[j]);
+          mma_f16(z[j][2 * w + 1], c0, c1, c2, c3, lo0[j], lo1[j]);
+        }
       }
     }
   }
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       issue(ch + (kStages - 1) * kAttendWarps, ahead);
       const int key0 = ch * kChunk;
       const bool masked = key0 + kChunk > least;
-      attend_chunk<D, NT>(ring + stage * stage_bytes<D>(), key0, masked, p.block, kmul, q, lim, z, l, m);
+      attend_chunk<D, NT, !kBf16>(ring + stage * stage_bytes<D>(), key0, masked, p.block, kmul, q, lim, z, l, m);
       __syncwarp();
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
