@@ -402,31 +402,34 @@ template <bool kBf16, int D>
 cudaError_t launch_attend_nt(const AttendParams<ByQuery>& p, int sms, cudaStream_t s) {
   if (p.geo.tile == 8) return launch_attend<kBf16, D, 1>(p, sms, s);
   if (p.geo.tile == 16) return launch_attend<kBf16, D, 2>(p, sms, s);
-  return launch_attend<kBf16, D, 4>(p, sms, s);
+  if constexpr (D == 64) return launch_attend<kBf16, D, 4>(p, sms, s);
+  return cudaErrorInvalidValue;  // more rows are the tcgen05 kernel's
 }
 
 }  // namespace kv8
 
-// Rows per key/value head up to which the mma.sync kernel is used (see the measurements above).
-constexpr int kFewRows = 32;
+// Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  16
+// sequences x 8 heads of 8187 keys, bf16, us here and there: d = 128, 16 rows 54 and 87, 24 rows
+// 123 and 88 (32-row tiles spill registers); d = 64, 32 rows 52 and 73, 48 rows 83 and 74.
+constexpr int few_rows(int d) { return d == 64 ? 32 : 16; }
 
-int rows_per_tile(int64_t R) {
-  if (R > kFewRows) return R > kTcTileRows / 2 ? kTcTileRows : kTcTileRows / 2;
+int rows_per_tile(int64_t R, int d) {
+  if (R > few_rows(d)) return R > kTcTileRows / 2 ? kTcTileRows : kTcTileRows / 2;
   return kv8::rows_per_tile(static_cast<int>(R));
 }
 
 // Rows of the parts: two places a CTA (for tiles of 128 rows, two and one for what its second row
 // tile hands over).
-size_t part_rows(int64_t R, int sms) {
-  if (R > kFewRows) return static_cast<size_t>(2) * sms * kTcTileRows;
-  return static_cast<size_t>(2) * sms * kv8::kMostCtas * rows_per_tile(R);
+size_t part_rows(int64_t R, int d, int sms) {
+  if (R > few_rows(d)) return static_cast<size_t>(2) * sms * kTcTileRows;
+  return static_cast<size_t>(2) * sms * kv8::kMostCtas * rows_per_tile(R, d);
 }
 
 size_t kv8_attend_workspace_bytes(int B, int Hk, int G, int n, int d, int cap, int sms) {
   const int64_t R = static_cast<int64_t>(G) * n;
-  if (R <= kFewRows && cap <= kv8::kAlignedCap) return 0;  // nothing to join
-  const size_t tiles = static_cast<size_t>(B) * Hk * ((R + rows_per_tile(R) - 1) / rows_per_tile(R));
-  return part_rows(R, sms) * (d + 2) * sizeof(float) + tiles * sizeof(int2);
+  if (R <= few_rows(d) && cap <= kv8::kAlignedCap) return 0;  // nothing to join
+  const size_t tiles = static_cast<size_t>(B) * Hk * ((R + rows_per_tile(R, d) - 1) / rows_per_tile(R, d));
+  return part_rows(R, d, sms) * (d + 2) * sizeof(float) + tiles * sizeof(int2);
 }
 
 namespace {
@@ -434,8 +437,8 @@ namespace {
 template <class Geo>
 kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int ctas, int min_chunks) {
   kv8::AttendParams<Geo> p{};
-  const int R = a.G * a.n, tile = rows_per_tile(R);
-  const size_t rows = part_rows(R, a.sms);
+  const int R = a.G * a.n, tile = rows_per_tile(R, a.d);
+  const size_t rows = part_rows(R, a.d, a.sms);
   p.geo = {{a.B, a.Hk, a.G, a.n, a.cap, R, tile, (R + tile - 1) / tile, a.causal, a.lengths, a.counts, false}};
   p.block = a.block;
   p.c2 = a.c * kv8::kLog2e;
@@ -459,13 +462,13 @@ kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int ctas, int min_chunks)
 
 int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   const int64_t R = static_cast<int64_t>(a.G) * a.n;
-  const int tiles = static_cast<int>((R + rows_per_tile(R) - 1) / rows_per_tile(R));
-  if (kv8::list_too_long(a.B, a.Hk, tiles, a.cap, R > kFewRows ? kv8::kBlockKeys : kv8::kChunk)) {
+  const int tiles = static_cast<int>((R + rows_per_tile(R, a.d) - 1) / rows_per_tile(R, a.d));
+  if (kv8::list_too_long(a.B, a.Hk, tiles, a.cap, R > few_rows(a.d) ? kv8::kBlockKeys : kv8::kChunk)) {
     err = "B * H * n_q * cap is too large for one call";
     return -2;
   }
   cudaError_t e;
-  if (R > kFewRows) {
+  if (R > few_rows(a.d)) {
     auto p = attend_params<kv8::ByHead>(a, a.sms, 2);
     if (a.bf16)
       e = a.d == 128 ? launch_kv8_tc<true, 128>(p, s) : launch_kv8_tc<true, 64>(p, s);

@@ -19,7 +19,7 @@ constexpr int kWeightsThreads = kWeightsWarps * 32;
 template <int D>
 constexpr int weights_stage_bytes() { return Chunk<D>::kBytes + 16 + 4 * kChunk; }  // K, scales, sums
 template <int NT>
-constexpr int weights_ctas_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
+constexpr int weights_ctas_per_sm() { return NT == 1 ? 4 : 3; }
 template <int D, int NT>
 constexpr int weights_stages() {
   const int fit = (225 * 1024 / weights_ctas_per_sm<NT>() - 1024) / (kWeightsWarps * weights_stage_bytes<D>());
@@ -163,15 +163,17 @@ cudaError_t launch_weights(WeightsParams<ByQuery> p, int sms, cudaStream_t s) {
 template <bool kBf16, int D>
 cudaError_t launch_weights_nt(const WeightsParams<ByQuery>& p, int sms, cudaStream_t s) {
   if (p.geo.R <= 8) return launch_weights<kBf16, D, 1>(p, sms, s);
-  if (p.geo.R <= 16) return launch_weights<kBf16, D, 2>(p, sms, s);
-  return launch_weights<kBf16, D, 4>(p, sms, s);
+  return launch_weights<kBf16, D, 2>(p, sms, s);
 }
 
 }  // namespace kv8
 
 namespace {
 
-constexpr int kFewRows = 32;
+// Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  16
+// sequences x 8 heads of 8187 keys, bf16, d = 128, us here and there: 16 rows 33 and 39, 24 rows 47
+// and 41; one sequence, 24 rows, 15 and 10.
+constexpr int kFewRows = 16;
 
 template <class Geo>
 kv8::WeightsParams<Geo> weights_params(const Kv8Args& a) {

@@ -246,7 +246,7 @@ int attn_fwd_fp8_blocks(int B, int H, int n, int d, float c,
  *   weights              float32 [B][H_kv][cap]: accumulated attention weight of each token
  * d: 64 or 128; block: 16, 32, 64 or 128; cap: a multiple of block, at most 2^30; B * H_kv at
  * most 65535; for attention and weights H / H_kv * n_q at most 2^24, and the steps of 32 keys
- * (128 for more than 32 rows a key/value head) over all heads and tiles of rows below 2^30.
+ * (128 for more than 16 rows a key/value head) over all heads and tiles of rows below 2^30.
  * Scales must be positive and finite (those of blocks with no held token are not read); the
  * entry points below write powers of two, which E4M3, a floating-point format, loses no
  * precision to, so codes move between blocks exactly down to E4M3's subnormals.  What lies past
@@ -281,7 +281,7 @@ int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int b
  * key below lengths[b] (ATTN_MASK_BITMAP is refused).  A padding row (i >= counts[b]) gets
  * O = 0, LSE = -inf; so does a row that sees no key, which also raises ATTN_WARN_EMPTY_ROW.
  * The codes are read exactly and the queries keep their bits; probabilities enter the product
- * with V as fp16 values (half a step 2^-11), as pairs of them for ATTN_F16 and at most 32 rows
+ * with V as fp16 values (half a step 2^-11), as pairs of them for ATTN_F16 and at most 16 (d = 64: 32) rows
  * H / H_kv * n_q a key/value head; sums are float32.
  *   workspace  device buffer of at least attn_fwd_kv8_workspace_bytes(...) bytes, 16-byte
  *              aligned; its contents on entry do not matter.  Calls that may overlap on the GPU
