@@ -84,8 +84,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   grid_dependency_wait();  // by every warp: what follows on the stream may rely on this kernel
   int first = 0, last = 0;
   if (pl.keys > 0) {
+    // Kept inside the parts even if the lengths changed since the first kernel read them (which
+    // leaves the result undefined, but not the addresses).
     const int2 run = p.runs[blockIdx.x];
-    first = run.x, last = run.y;
+    first = min(max(run.x, 0), p.ctas - 1);
+    last = min(max(run.y, first), p.ctas - 1);
   }
   if (r >= geo.R || (pl.keys > 0 && first == last)) return;  // or one CTA held the tile whole
   float mx = kNoMax, l = 0.0f;

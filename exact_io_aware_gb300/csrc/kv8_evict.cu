@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kMoveThreads, D == 64 ? 6 : 4) evict_move_kern
   uint4 raw[2][kIters];
   float sc[2][kIters];
   {
-    const int from16 = p0 + (lane & 15) < live ? kept[p0 + (lane & 15)] : -1;
+    // Kept inside the cache even if the lengths changed since the first kernel read them.
+    const int from16 = p0 + (lane & 15) < live ? min(kept[p0 + (lane & 15)], p.cap - 1) : -1;
     if (lane < 16 && from16 >= 0)
       p.weights_out[static_cast<int64_t>(bh) * p.cap_out + p0 + lane] =
           __ldg(p.weights + static_cast<int64_t>(bh) * p.cap + from16);

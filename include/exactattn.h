@@ -253,7 +253,8 @@ int attn_fwd_fp8_blocks(int B, int H, int n, int d, float c,
  * a sequence's length is neither used nor changed.  A length outside [0, cap] or a count
  * outside [0, n] is clamped and raises ATTN_WARN_CLAMPED.  Code arrays and 16-bit arrays are
  * 16-byte aligned, the others 4-byte.  All calls are asynchronous on `stream`, can be
- * captured, and allocate nothing.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
+ * captured, and allocate nothing; what they read, lengths and counts among it, must not change
+ * until they have finished.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
  * ATTN_ERR_ALIGNMENT, ATTN_ERR_WORKSPACE, ATTN_ERR_CUDA, as for attn_fwd_kv.
  */
 
@@ -281,8 +282,8 @@ int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int b
  * key below lengths[b] (ATTN_MASK_BITMAP is refused).  A padding row (i >= counts[b]) gets
  * O = 0, LSE = -inf; so does a row that sees no key, which also raises ATTN_WARN_EMPTY_ROW.
  * The codes are read exactly and the queries keep their bits; probabilities enter the product
- * with V as fp16 values (half a step 2^-11), as pairs of them for ATTN_F16 and at most 16 (d = 64: 32) rows
- * H / H_kv * n_q a key/value head; sums are float32.
+ * with V as fp16 values (half a step 2^-11), as pairs of them for ATTN_F16 and at most 16 rows
+ * H / H_kv * n_q a key/value head (d = 64: 32); sums are float32.
  *   workspace  device buffer of at least attn_fwd_kv8_workspace_bytes(...) bytes, 16-byte
  *              aligned; its contents on entry do not matter.  Calls that may overlap on the GPU
  *              need workspaces of their own.

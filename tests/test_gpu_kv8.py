@@ -217,6 +217,26 @@ def test_attend_scales_far_apart_and_large_scores(n, G):
     status()
 
 
+@pytest.mark.parametrize("c", [-0.3, 0.0])
+@pytest.mark.parametrize("dtype,G,n", [("bf16", 4, 1), ("f16", 3, 7), ("bf16", 5, 40)])
+def test_scale_negative_and_zero(c, dtype, G, n):
+    rng = np.random.default_rng(14)
+    ca = Cache(rng, [200, 50], 2, 256, 128, 32)
+    q = rounded(rng.normal(size=(2, 2 * G, n, 128)), dtype)
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, c, mask="causal")
+    O, L, A, S, F = kv8.attend(ca.c, q.double().numpy(), c, None, True)
+    ds = (128 + 16) * 2.0 ** -23 * (np.abs(S) + 32.0)
+    tol = (2.0 ** -8 * np.abs(O) + 2.0 ** -25 + 1.1 * A * (2.0 ** -11 + 2 * ds[..., None] + 2.0 ** -16)
+           + 2.0 ** -31 * F)
+    assert (np.abs(o.double().cpu().numpy() - O) <= tol).all()
+    # LSE: the scores' error and float32 sums and rounding of values up to 64
+    assert (np.abs(lse.double().cpu().numpy() - L) <= ds + 2.0 ** -15).all()
+    ref = kv8.add_weights(ca.c, q.double().numpy(), c, lse.double().cpu().numpy(), None, True)
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, lse, ca.w, c, mask="causal")
+    held = (np.arange(256) < np.array([200, 50])[:, None])[:, None].repeat(2, 1)
+    assert np.allclose(w.double().cpu().numpy()[held], ref[held], rtol=1e-3 if c else 1e-5, atol=0)
+
+
 def test_attend_query_sizes():
     """Rows of one call whose queries differ by 2^60, and tiny and huge ones."""
     rng = np.random.default_rng(12)
@@ -447,6 +467,43 @@ def test_captured_step_replays_with_new_lengths():
         assert np.allclose(got[held], ref[held], rtol=2e-4, atol=0)
         ca.c["w"] = got
         ca.check(ca.c)
+
+
+def test_captured_eviction_replays_with_new_weights():
+    rng = np.random.default_rng(42)
+    ca = Cache(rng, [300, 64], 2, 320, 64, 32)
+    out = Cache(rng, [0, 0], 2, 128, 64, 32)
+    out.c["k8"][:], out.c["v8"][:], out.c["ks"][:], out.c["vs"][:] = 1.0, 1.0, 1.0, 1.0
+    out.load()
+    kept = torch.empty(2, 2, 100, dtype=torch.int32, device="cuda")
+    call = lambda: ea.attn_kv8_evict(ca.k8, ca.v8, ca.ks, ca.vs, ca.w, ca.lengths, 100, out.k8, out.v8, out.ks,
+                                     out.vs, out.w, out.lengths, sink=3, recent=20, kept=kept)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call_on_side = ea.attn_kv8_evict(ca.k8, ca.v8, ca.ks, ca.vs, ca.w, ca.lengths, 100, out.k8, out.v8, out.ks,
+                                     out.vs, out.w, out.lengths, sink=3, recent=20, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        graph.replay()
+        ref, pos = kv8.evict(ca.c, out.c, 100, 3, 20)
+        assert kept.cpu().numpy().tolist() == pos.tolist()
+        out.check(ref)
+        w = rng.random(ca.c["w"].shape).astype(np.float32)
+        ca.c["w"] = w.astype(np.float64)
+        ca.w.copy_(torch.from_numpy(w))
+    assert call_on_side.shape == kept.shape
+
+
+def test_codes_as_bytes_are_the_same_cache():
+    rng = np.random.default_rng(43)
+    ca = Cache(rng, [90, 17], 2, 96, 128, 32)
+    q = rounded(rng.normal(size=(2, 2, 1, 128)), "bf16").cuda()
+    a = ea.attn_fwd_kv8(q, ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, 0.1)
+    b = ea.attn_fwd_kv8(q, ca.k8.view(torch.uint8), ca.v8.view(torch.uint8), ca.ks, ca.vs, ca.lengths, 0.1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_calls_on_two_streams_at_once():
