@@ -277,6 +277,40 @@ def test_a_nan_value_reaches_only_the_rows_that_see_it(d, G, n):
     assert torch.isfinite(o[:, :, :-1]).all() and torch.isfinite(lse[:, :, :-1]).all()
 
 
+@pytest.mark.parametrize("B,Hk,G,n", [(170, 5, 17, 2), (150, 5, 66, 2)])
+def test_many_short_tiles_a_cta(B, Hk, G, n):
+    """Many tiles in each CTA's run (of 128 rows, and of 256), some ending in a NaN value or seeing
+    no key, so that what the kernel keeps by tile number is used over and over."""
+    rng = np.random.default_rng(15)
+    lengths = [int(x) for x in rng.integers(0, 140, B)]
+    ca = Cache(rng, lengths, Hk, 256, 64, 16)
+    sick = [b for b in range(B) if b % 7 == 3 and lengths[b] > 2]
+    for b in sick:
+        ca.c["v8"][b, :, lengths[b] - 1, 5] = np.nan
+    ca.load()
+    q = rounded(rng.normal(size=(B, Hk * G, n, 64)), "bf16")
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, 0.125, mask="causal")
+    nan = torch.isnan(o).cpu().numpy()
+    want = np.zeros_like(nan)
+    want[sick, :, n - 1, 5] = True
+    assert (nan == want).all(), np.argwhere(nan != want)[:5].tolist()
+    for b in sick:
+        ca.c["v8"][b, :, lengths[b] - 1, 5] = 0.0
+    some = rng.choice(B, 12, replace=False)
+    sub = type("Sub", (), {})()
+    sub.c = {key: val[some] for key, val in ca.c.items()}
+    sub.k8 = ca.k8
+    o2 = o[some].clone()
+    o2[torch.isnan(o2)] = 0.0
+    O, L, tol, ltol = attend_bounds(sub, q[some], 0.125, "bf16", None, True)
+    o2, l2 = o2.double().cpu().numpy(), lse[some].double().cpu().numpy()
+    keep = ~want[some]
+    assert (np.abs(o2 - O) <= tol)[keep].all()
+    empty = np.isneginf(L)
+    assert (np.isneginf(l2) == empty).all() and (np.abs(l2 - L)[~empty] <= ltol[~empty]).all()
+    status()
+
+
 def test_attend_offsets_past_32_bits():
     """One head of 2^24 + 256 tokens: codes past 2^31 bytes.  Zero keys: every weight is 1 / len."""
     cap = (1 << 24) + 256
