@@ -4,6 +4,7 @@ For profilers (ncu) and for timing one shape or one named workload:
 
     python -m exact_io_aware_gb300.run --B 1 --H 64 --n 4096 --d 128 --iters 2
     python -m exact_io_aware_gb300.run --workload longctx_bf16_n65536 --iters 5
+    python -m exact_io_aware_gb300.run --kv8 --B 32 --H 32 --H-kv 8 --n 1 --n-kv 4096 --keep 1024
 
 Inputs are seeded N(0,1) tensors generated on the device (the workload's query scale
 applied); a bitmap workload uses the seeded allowed-key sets of ``synth``.  Prints the mean
@@ -45,6 +46,12 @@ def main(argv=None):
     ap.add_argument("--dropout", type=float, default=0.0, help="drop probability (0 = none)")
     ap.add_argument("--n-kv", type=int, default=0,
                     help="keys of a key/value cache (forward of --n query rows through attn_fwd_kv)")
+    ap.add_argument("--kv8", action="store_true",
+                    help="8-bit key/value cache of --n-kv tokens: append of --n tokens, attention of "
+                         "--n rows, their weights, and eviction down to --keep tokens")
+    ap.add_argument("--H-kv", type=int, default=0, help="with --kv8: key/value heads (default: H)")
+    ap.add_argument("--block", type=int, default=64, help="with --kv8: tokens of a scale block")
+    ap.add_argument("--keep", type=int, default=0, help="with --kv8: tokens kept (default: a quarter)")
     ap.add_argument("--fp8", action="store_true", help="forward through attn_fwd_fp8 (E4M3 inputs)")
     ap.add_argument("--fp8-blocks", action="store_true",
                     help="with --fp8: attn_fp8_quantize (timed apart) + attn_fwd_fp8_blocks")
@@ -74,6 +81,8 @@ def main(argv=None):
             bits = torch.from_numpy(pack_bitmap(allowed).view(np.int32)).cuda()
     dt = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[dtype]
     ea.load()
+    if a.kv8:
+        return _run_kv8(a, B, H, n, a.n_kv or 4096, d, dt, mask, c)
     if a.n_kv:
         return _run_kv(a, B, H, n, a.n_kv, d, dt, mask, c, kvb)
     if a.fp8:
@@ -214,6 +223,59 @@ def _run_kv(a, B, H, nq, nk, d, dt, mask, c, kvb):
            "kv_gbs": kv_bytes / (ms / 1e3) / 1e9, "kv_bytes": kv_bytes, "status": status}
     print(json.dumps(out) if a.json else " ".join(f"{k}={v}" for k, v in out.items()))
     return 0 if status == ea.ATTN_OK else 1
+
+
+def _run_kv8(a, B, H, n, nk, d, dt, mask, c):
+    """One round over an 8-bit cache of nk tokens, the last n of them appended in it: time of each
+    operator, and the cache bytes a second of the attention and weights calls."""
+    import torch
+
+    import exact_io_aware_gb300 as ea
+    Hk, block = a.H_kv or H, a.block
+    cap = (nk + block - 1) // block * block
+    keep = a.keep or max(1, nk // 4)
+    small = (keep + block - 1) // block * block
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g)
+
+    def cache(m):
+        codes = [torch.zeros((B, Hk, m, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.ones((B, Hk, m // block), device="cuda") for _ in range(2)]
+        return [*codes, *scales]
+
+    k8, v8, ks, vs = cache(cap)
+    k8b, v8b, ksb, vsb = cache(small)
+    w, wb = rand(B, Hk, cap).abs(), torch.zeros((B, Hk, small), device="cuda")
+    lens = torch.full((B,), nk, dtype=torch.int32, device="cuda")
+    lens_b = torch.zeros_like(lens)
+    ea.attn_kv8_append(rand(B, Hk, nk, d).to(dt), rand(B, Hk, nk, d).to(dt), k8, v8, ks, vs, lens)
+    q, k, v = (rand(B, x, n, d).to(dt) for x in (H, Hk, Hk))
+    kept = torch.empty((B, Hk, keep), dtype=torch.int32, device="cuda")
+    o, lse = ea.attn_fwd_kv8(q, k8, v8, ks, vs, lens, c, mask=mask)
+    ops = {
+        "append": lambda: ea.attn_kv8_append(k, v, k8, v8, ks, vs, lens, weights=w),
+        "attend": lambda: ea.attn_fwd_kv8(q, k8, v8, ks, vs, lens, c, mask=mask, o=o, lse=lse),
+        "weights": lambda: ea.attn_kv8_weights(q, k8, ks, lens, lse, w, c, mask=mask),
+        "evict": lambda: ea.attn_kv8_evict(k8, v8, ks, vs, w, lens, keep, k8b, v8b, ksb, vsb, wb, lens_b,
+                                           sink=min(4, keep), kept=kept),
+    }
+    out = {"workload": "kv8", "B": B, "H": H, "H_kv": Hk, "n": n, "n_kv": nk, "d": d, "block": block,
+           "keep": keep, "dtype": str(dt).split(".")[-1], "mask": mask}
+    for name, op in ops.items():
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        op()
+        ev[0].record()
+        for _ in range(a.iters):
+            op()
+        ev[1].record()
+        torch.cuda.synchronize()
+        out[f"{name}_us"] = ev[0].elapsed_time(ev[1]) * 1e3 / a.iters
+    out["status"] = ea.attn_device_status()
+    out["attend_gbs"] = 2 * B * Hk * nk * d / out["attend_us"] / 1e3
+    out["weights_gbs"] = B * Hk * nk * d / out["weights_us"] / 1e3
+    print(json.dumps(out) if a.json else " ".join(f"{k}={v}" for k, v in out.items()))
+    return 0 if out["status"] == ea.ATTN_OK else 1
 
 
 if __name__ == "__main__":

@@ -579,3 +579,13 @@ def test_binding_refusals():
         ea.attn_kv8_evict(ca.k8, ca.v8, ca.ks, ca.vs, ca.w, ca.lengths, 8, ca.k8, ca.v8, ca.ks, ca.vs, ca.w,
                           ca.lengths)
     assert e.value.code == ea.ATTN_ERR_INVALID_ARG
+
+
+def test_runner(capsys):
+    import json
+
+    from exact_io_aware_gb300 import run
+
+    rc = run.main("--kv8 --B 2 --H 8 --H-kv 2 --n 3 --n-kv 700 --d 64 --mask causal --iters 2 --json".split())
+    out = json.loads(capsys.readouterr().out)
+    assert rc == 0 and out["keep"] == 175 and all(out[f"{x}_us"] > 0 for x in ("append", "attend", "weights", "evict"))
