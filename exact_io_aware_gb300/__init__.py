@@ -9,6 +9,10 @@ CPU or PyTorch fallback, and every entry point raises if the library is not buil
     o, lse = attn_fwd_split(q, k, v, c, mask="causal")   # key shares + merge (few heads)
     dq, dk, dv = attn_bwd(q, k, v, o, lse, do, c, mask="causal")
     y = attention(q, k, v, c, mask="causal")      # autograd-aware wrapper
+    attn_kv8_append(k, v, k8, v8, ks, vs, lengths)               # 8-bit key/value cache:
+    o, lse = attn_fwd_kv8(q, k8, v8, ks, vs, lengths, c)         # write, attend,
+    attn_kv8_weights(q, k8, ks, lengths, lse, w, c)              # weigh the tokens, and
+    attn_kv8_evict(k8, v8, ks, vs, w, lengths, keep, *smaller)   # keep the heaviest
 """
 from __future__ import annotations
 
