@@ -490,7 +490,8 @@ int attn_selftest_exp2(const float* x, float* y_fma, float* y_mufu, int64_t n, v
  * bf16 inputs, d = v = 128, key block 128 (or 0) and no dropout, and the FP8 forward with
  * d = 128 and per-tensor scales, run (one instantiation of each kernel reads its depths at
  * launch; the others keep them constant and cost nothing); other calls return
- * ATTN_ERR_UNSUPPORTED.  Returns ATTN_ERR_INVALID_ARG unless 0 <= stages <= 4.
+ * ATTN_ERR_UNSUPPORTED, except those of the 8-bit key/value cache, which the cap does not
+ * concern.  Returns ATTN_ERR_INVALID_ARG unless 0 <= stages <= 4.
  */
 int attn_debug_set_ring_stages(int stages);
 
