@@ -385,47 +385,49 @@ _KV8_CODES = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 _KV8_INPUTS = (torch.float16, torch.bfloat16)
 
 
-def _kv8_array(t, dtype, shape, name, device):
-    """The address of t, a contiguous tensor of the given type and shape on CUDA device ``device``."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name} must be a contiguous tensor {list(shape)} of {dtype} on CUDA "
-                         f"device {device}")
-    return t.data_ptr()
+def _kv8_check(device, *specs):
+    """Addresses of the call's tensors: each (tensor, dtype, shape, name) must be contiguous, of that
+    type and shape, on CUDA device ``device``; None for None."""
+    ptrs = []
+    for t, dtype, shape, name in specs:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"{name} must be a contiguous tensor {list(shape)} of {dtype} on CUDA "
+                             f"device {device}")
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
-def _kv8_codes(t, shape, name, device):
-    if t.dtype not in _KV8_CODES:
-        raise ValueError(f"{name} must hold E4M3 values (torch.float8_e4m3fn or uint8)")
-    return _kv8_array(t, t.dtype, shape, name, device)
-
-
-def _kv8_input(t, shape, name, device):
-    if t.dtype not in _KV8_INPUTS:
-        raise ValueError(f"{name} must be float16 or bfloat16")
-    return _kv8_array(t, t.dtype, shape, name, device)
-
-
-def _kv8_optional(t, dtype, shape, name, device):
-    return None if t is None else _kv8_array(t, dtype, shape, name, device)
+def _kv8_types(codes, inputs):
+    for t in codes:
+        if t.dtype not in _KV8_CODES:
+            raise ValueError("codes must be E4M3 values (torch.float8_e4m3fn or uint8)")
+    for t in inputs:
+        if t.dtype not in _KV8_INPUTS:
+            raise ValueError("queries, keys and values must be float16 or bfloat16")
 
 
 def _kv8_shape(k8, k_scales):
     """(B, H_kv, cap, d, block, device index) from the codes [B,H_kv,cap,d] and scales [B,H_kv,cap/block]."""
-    if not k8.is_cuda:
+    shape, device = k8.shape, k8.get_device()
+    if device < 0:
         raise ValueError("the 8-bit cache must be CUDA tensors")
-    if k8.dim() != 4 or k_scales.dim() != 3:
+    if len(shape) != 4 or k_scales.dim() != 3:
         raise ValueError("codes must be [B,H_kv,cap,d] and scales [B,H_kv,cap/block]")
-    B, Hk, cap, d = k8.shape
+    B, Hk, cap, d = shape
     nblk = k_scales.shape[2]
     if nblk < 1 or cap % nblk:
         raise ValueError("scales must be [B,H_kv,cap/block]")
-    return B, Hk, cap, d, cap // nblk, k8.get_device()
+    return B, Hk, cap, d, cap // nblk, device
 
 
 def _kv8_heads(q, B, Hk, mask):
-    if q.dim() != 4 or q.shape[0] != B or q.shape[1] < 1 or q.shape[1] % Hk:
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] < 1 or shape[1] % Hk:
         raise ValueError("q must be [B,H,n_q,d] with H a multiple of H_kv")
-    return q.shape[1], q.shape[2], MASK_CODE[mask]
+    return shape[1], shape[2], MASK_CODE[mask]
 
 
 class _On:
@@ -471,17 +473,14 @@ def attn_kv8_append(k_new, v_new, k8, v8, k_scales, v_scales, lengths, counts=No
     B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
     if k_new.dim() != 4:
         raise ValueError("k_new and v_new must be [B,H_kv,n,d]")
-    if v_new.dtype is not k_new.dtype:
-        raise ValueError("k_new and v_new must share one dtype")
-    n, f32, i32 = k_new.shape[2], torch.float32, torch.int32
+    _kv8_types((k8, v8), (k_new,))
+    n, f32, i32, dt = k_new.shape[2], torch.float32, torch.int32, k_new.dtype
     new, codes, scales = (B, Hk, n, d), (B, Hk, cap, d), (B, Hk, cap // block)
-    ptrs = (_kv8_input(k_new, new, "k_new", dev), _kv8_input(v_new, new, "v_new", dev),
-            _kv8_array(lengths, i32, (B,), "lengths", dev),
-            _kv8_optional(counts, i32, (B,), "counts", dev),
-            _kv8_codes(k8, codes, "k8", dev), _kv8_codes(v8, codes, "v8", dev),
-            _kv8_array(k_scales, f32, scales, "k_scales", dev),
-            _kv8_array(v_scales, f32, scales, "v_scales", dev),
-            _kv8_optional(weights, f32, (B, Hk, cap), "weights", dev))
+    ptrs = _kv8_check(dev, (k_new, dt, new, "k_new"), (v_new, dt, new, "v_new"),
+                      (lengths, i32, (B,), "lengths"), (counts, i32, (B,), "counts"),
+                      (k8, k8.dtype, codes, "k8"), (v8, v8.dtype, codes, "v8"),
+                      (k_scales, f32, scales, "k_scales"), (v_scales, f32, scales, "v_scales"),
+                      (weights, f32, (B, Hk, cap), "weights"))
     with _On(dev, stream) as s:
         _check(load().attn_kv8_append(DTYPE_CODE[k_new.dtype], B, Hk, n, d, cap, block, *ptrs, s))
 
@@ -500,23 +499,23 @@ def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="n
     (o [B,H,n_q,d], lse [B,H,n_q] float32)."""
     B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
     H, n, kind = _kv8_heads(q, B, Hk, mask)
-    f32, i32 = torch.float32, torch.int32
+    _kv8_types((k8, v8), (q,))
+    f32, i32, rows = torch.float32, torch.int32, (B, H, n, d)
     codes, scales = (B, Hk, cap, d), (B, Hk, cap // block)
-    ptrs = (_kv8_input(q, (B, H, n, d), "q", dev), _kv8_codes(k8, codes, "k8", dev),
-            _kv8_codes(v8, codes, "v8", dev), _kv8_array(k_scales, f32, scales, "k_scales", dev),
-            _kv8_array(v_scales, f32, scales, "v_scales", dev),
-            _kv8_array(lengths, i32, (B,), "lengths", dev),
-            _kv8_optional(counts, i32, (B,), "counts", dev))
+    ptrs = _kv8_check(dev, (q, q.dtype, rows, "q"), (k8, k8.dtype, codes, "k8"),
+                      (v8, v8.dtype, codes, "v8"), (k_scales, f32, scales, "k_scales"),
+                      (v_scales, f32, scales, "v_scales"), (lengths, i32, (B,), "lengths"),
+                      (counts, i32, (B,), "counts"))
     lib, code = load(), DTYPE_CODE[q.dtype]
     with _On(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
         else:
-            _kv8_array(o, q.dtype, q.shape, "o", dev)
+            _kv8_check(dev, (o, q.dtype, rows, "o"))
         if lse is None:
             lse = torch.empty((B, H, n), dtype=f32, device=dev)
         else:
-            _kv8_array(lse, f32, (B, H, n), "lse", dev)
+            _kv8_check(dev, (lse, f32, (B, H, n), "lse"))
         if workspace is None:
             size = _kv8_workspace(code, B, H, Hk, n, d, cap, dev)
             if size > 0:
@@ -538,14 +537,13 @@ def attn_kv8_weights(q, k8, k_scales, lengths, lse, weights, c, counts=None, mas
     same arguments.  Writes ``out`` (None: ``weights`` in place) and returns it."""
     B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
     H, n, kind = _kv8_heads(q, B, Hk, mask)
-    f32, i32 = torch.float32, torch.int32
-    ptrs = (_kv8_input(q, (B, H, n, d), "q", dev), _kv8_codes(k8, (B, Hk, cap, d), "k8", dev),
-            _kv8_array(k_scales, f32, (B, Hk, cap // block), "k_scales", dev),
-            _kv8_array(lengths, i32, (B,), "lengths", dev),
-            _kv8_optional(counts, i32, (B,), "counts", dev))
-    p_lse = _kv8_array(lse, f32, (B, H, n), "lse", dev)
-    p_w = _kv8_optional(weights, f32, (B, Hk, cap), "weights", dev)
-    _kv8_optional(out, f32, (B, Hk, cap), "out", dev)
+    _kv8_types((k8,), (q,))
+    f32, i32, tokens = torch.float32, torch.int32, (B, Hk, cap)
+    *ptrs, p_lse, p_w, _ = _kv8_check(
+        dev, (q, q.dtype, (B, H, n, d), "q"), (k8, k8.dtype, (B, Hk, cap, d), "k8"),
+        (k_scales, f32, (B, Hk, cap // block), "k_scales"), (lengths, i32, (B,), "lengths"),
+        (counts, i32, (B,), "counts"), (lse, f32, (B, H, n), "lse"), (weights, f32, tokens, "weights"),
+        (out, f32, tokens, "out"))
     with _On(dev, stream) as s:
         if out is None:
             out = torch.zeros((B, Hk, cap), dtype=f32, device=dev) if weights is None else weights
@@ -565,12 +563,13 @@ def attn_kv8_evict(k8, v8, k_scales, v_scales, weights, lengths, keep, k8_out, v
         raise ValueError("the output cache's capacity must be a multiple of the block")
     cap_out, keep, f32, i32 = k8_out.shape[2], int(keep), torch.float32, torch.int32
 
+    _kv8_types((k8, v8, k8_out, v8_out), ())
+
     def cache(k, v, ks, vs, w, lens, m):
-        return ((_kv8_codes(k, (B, Hk, m, d), "k8", dev), _kv8_codes(v, (B, Hk, m, d), "v8", dev),
-                 _kv8_array(ks, f32, (B, Hk, m // block), "k_scales", dev),
-                 _kv8_array(vs, f32, (B, Hk, m // block), "v_scales", dev),
-                 _kv8_array(w, f32, (B, Hk, m), "weights", dev),
-                 _kv8_array(lens, i32, (B,), "lengths", dev)))
+        codes, scales = (B, Hk, m, d), (B, Hk, m // block)
+        return _kv8_check(dev, (k, k.dtype, codes, "k8"), (v, v.dtype, codes, "v8"),
+                          (ks, f32, scales, "k_scales"), (vs, f32, scales, "v_scales"),
+                          (w, f32, (B, Hk, m), "weights"), (lens, i32, (B,), "lengths"))
 
     src = cache(k8, v8, k_scales, v_scales, weights, lengths, cap)
     dst = cache(k8_out, v8_out, k_scales_out, v_scales_out, weights_out, lengths_out, cap_out)
@@ -578,7 +577,7 @@ def attn_kv8_evict(k8, v8, k_scales, v_scales, weights, lengths, keep, k8_out, v
         if kept is None:
             kept = torch.empty((B, Hk, max(keep, 0)), dtype=i32, device=dev)
         else:
-            _kv8_array(kept, i32, (B, Hk, keep), "kept", dev)
+            _kv8_check(dev, (kept, i32, (B, Hk, keep), "kept"))
         _check(load().attn_kv8_evict(B, Hk, d, cap, block, *src, keep, int(sink), int(recent), cap_out,
                                      *dst, kept.data_ptr(), s))
     return kept

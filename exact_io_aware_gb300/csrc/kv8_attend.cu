@@ -385,8 +385,8 @@ template <bool kBf16, int D, int NT>
 cudaError_t launch_attend(AttendParams<ByQuery> p, int sms, cudaStream_t s) {
   constexpr size_t smem = ring_bytes<D, NT>() > merge_bytes<D, NT>() ? ring_bytes<D, NT>() : merge_bytes<D, NT>();
   auto* kernel = attend_kernel<kBf16, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, allowed);
   if (e != cudaSuccess) return e;
   const unsigned tiles = static_cast<unsigned>(p.geo.B) * p.geo.Hk * p.geo.tiles;
   const bool aligned = p.geo.cap <= kAlignedCap;

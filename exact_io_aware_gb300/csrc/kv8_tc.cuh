@@ -814,16 +814,17 @@ cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
   if (!encode_byte_map(&tm_k, p.k8, heads, p.geo.cap, D, kv8::kBlockKeys, D) ||
       !encode_byte_map(&tm_v, p.v8, heads, p.geo.cap, D, kv8::kBlockKeys, D))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
   // The registers dealt inside the kernel are those it is launched with: were a compiler to give
   // it fewer, the warpgroups that ask for more would wait for ever.
-  cudaFuncAttributes attr;
-  e = cudaFuncGetAttributes(&attr, kernel);
-  if (e != cudaSuccess) return e;
-  if (4 * attr.numRegs < kv8::tc::kRegsIssue + 2 * kv8::tc::kRegsSoftmax + kv8::tc::kRegsConvert)
+  static const int regs = [&] {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
+  }();
+  if (4 * regs < kv8::tc::kRegsIssue + 2 * kv8::tc::kRegsSoftmax + kv8::tc::kRegsConvert)
     return cudaErrorInvalidConfiguration;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = kv8::allow_smem(reinterpret_cast<const void*>(kernel), smem, allowed);
+  if (e != cudaSuccess) return e;
   void* args[] = {&tm_k, &tm_v, &p};
   e = cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas), dim3(kv8::tc::kThreads), args,
                        smem, s);

@@ -153,7 +153,8 @@ template <bool kBf16, int D, int NT>
 cudaError_t launch_weights(WeightsParams<ByQuery> p, int sms, cudaStream_t s) {
   auto* kernel = weights_kernel<kBf16, D, NT>;
   constexpr int smem = kWeightsWarps * weights_stages<D, NT>() * weights_stage_bytes<D>();
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, allowed);
   if (e != cudaSuccess) return e;
   void* args[] = {&p};
   return cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(weights_ctas_per_sm<NT>() * sms),

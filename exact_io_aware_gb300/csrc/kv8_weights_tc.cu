@@ -255,8 +255,8 @@ cudaError_t launch_kv8_weights_tc(kv8::WeightsParams<kv8::ByHead> p, int sms, cu
   CUtensorMap tm_k;
   if (!encode_byte_map(&tm_k, p.k8, static_cast<uint64_t>(p.geo.B) * p.geo.Hk, p.geo.cap, D, kv8::kBlockKeys, D))
     return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = kv8::allow_smem(reinterpret_cast<const void*>(kernel), smem, allowed);
   if (e != cudaSuccess) return e;
   void* args[] = {&tm_k, &p};
   return cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(sms), dim3(kv8::wtc::kThreads), args, smem, s);
