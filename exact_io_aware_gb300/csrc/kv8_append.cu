@@ -8,8 +8,10 @@
 //
 // One CTA takes a span of 128 positions of one head's K or V, each warp 16 of them, so a block
 // is one to eight whole warps of one CTA: the values stay in registers between the block's
-// maximum and the conversion, and the input is read once.  Memory-bound for prompts; for one
-// token a sequence it is the latency of its two dependent loads (length, then token and scale).
+// maximum and the conversion, and the input is read once.  Memory-bound for prompts (4 x 8 heads of
+// up to 8192 tokens, d = 128: 26.7 us, 5.1 TB/s, 77 % of the measured copy rate); for one token a
+// sequence it is the latency of its two dependent loads (length, then token and scale; 4 us for 256
+// heads).
 #include "kv8_common.cuh"
 
 namespace ea {

@@ -6,7 +6,8 @@
 // This file: the kernel for few rows, which is bound by reading the codes, and the choice between
 // it and the tcgen05 kernel for many (kv8_weights_tc.cu).  Scores are formed as in kv8_attend.cu
 // (S^T = K Q^T, a warp to 32 keys), the queries stay in registers, and a key's weight is summed
-// over the rows of a lane and then over the four lanes that share the key.
+// over the rows of a lane and then over the four lanes that share the key.  Measured (d = 128, four
+// rows): 256 heads of 2000 to 8192 keys, 36.5 us, 4.8 TB/s, 72 % of the measured copy rate.
 #include "kv8_mma.cuh"
 #include "kv8_weights.cuh"
 
