@@ -37,6 +37,14 @@ int entry(const char* name, F&& body) noexcept {
   }
 }
 
+// A launcher's outcome as the entry point's.  The runtime keeps a refused launch as its last error;
+// it is taken here, so that no later call reads it as its own.
+int outcome(int rc, const std::string& err) {
+  if (rc == 0) return ATTN_OK;
+  (void)cudaGetLastError();
+  return fail(rc, err);
+}
+
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 // Bytes [p, p + n) and [q, q + m) share a byte.
@@ -131,7 +139,7 @@ int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int b
     if (int rc = ea::device_status_word(&a.status)) return rc;
     std::string err;
     const int rc = ea::launch_kv8_append(a, static_cast<cudaStream_t>(stream), err);
-    return rc ? fail(rc, err) : ATTN_OK;
+    return outcome(rc, err);
   });
 }
 
@@ -174,7 +182,7 @@ int attn_fwd_kv8(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int
     a.workspace = workspace;
     std::string err;
     const int rc = ea::launch_kv8_attend(a, static_cast<cudaStream_t>(stream), err);
-    return rc ? fail(rc, err) : ATTN_OK;
+    return outcome(rc, err);
   });
 }
 
@@ -206,7 +214,7 @@ int attn_kv8_weights(int dtype, int B, int H, int H_kv, int n_q, int d, int cap,
     a.weights_out = weights_out;
     std::string err;
     const int rc = ea::launch_kv8_weights(a, static_cast<cudaStream_t>(stream), err);
-    return rc ? fail(rc, err) : ATTN_OK;
+    return outcome(rc, err);
   });
 }
 
@@ -251,7 +259,7 @@ int attn_kv8_evict(int B, int H_kv, int d, int cap, int block, const void* k8, c
     if (int rc = ea::device_status_word(&a.status)) return rc;
     std::string err;
     const int rc = ea::launch_kv8_evict(a, static_cast<cudaStream_t>(stream), err);
-    return rc ? fail(rc, err) : ATTN_OK;
+    return outcome(rc, err);
   });
 }
 

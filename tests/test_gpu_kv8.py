@@ -311,6 +311,28 @@ def test_many_short_tiles_a_cta(B, Hk, G, n):
     status()
 
 
+@pytest.mark.parametrize("G,n", [(4, 1), (2, 6), (7, 5)])
+def test_many_sequences(G, n):
+    """More sequences than lanes of a warp, some empty: attention and weights over runs that cross
+    many heads."""
+    rng = np.random.default_rng(16)
+    B = 75
+    lengths = [int(x) for x in rng.integers(0, 1024, B)]
+    lengths[5] = lengths[40] = lengths[74] = 0
+    ca = Cache(rng, lengths, 2, 1024, 64, 64)
+    counts = [min(n, m) for m in lengths]
+    q = rounded(rng.normal(size=(B, 2 * G, n, 64)), "f16")
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, 0.125, counts=i32(counts),
+                             mask="causal")
+    check_attend(ca, q, 0.125, "f16", o, lse, counts, True)
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, lse, ca.w, 0.125, counts=i32(counts),
+                            mask="causal")
+    ref = kv8.add_weights(ca.c, q.double().numpy(), 0.125, lse.double().cpu().numpy(), counts, True)
+    held = (np.arange(1024) < np.array(lengths)[:, None])[:, None].repeat(2, 1)
+    assert np.allclose(w.double().cpu().numpy()[held], ref[held], rtol=2e-4, atol=0)
+    status()
+
+
 def test_attend_offsets_past_32_bits():
     """One head of 2^24 + 256 tokens: codes past 2^31 bytes.  Zero keys: every weight is 1 / len."""
     cap = (1 << 24) + 256
@@ -413,6 +435,24 @@ def test_evict_weights_that_are_hard_to_order(kind):
     ca.load()
     for keep, sink, recent in ((50, 0, 0), (cap // 2, 3, 30), (cap - 100, 0, 1)):
         evict_both(ca, keep, sink, recent, -(-keep // 16) * 16, rng, 16)
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "nan"])
+def test_evict_long_sequences(kind):
+    """Sequences whose tokens several CTAs look at together (40960 tokens; one just over keep)."""
+    rng = np.random.default_rng(22)
+    cap, lengths = 40960, [40960, 33333, 9001]
+    ca = Cache(rng, lengths, 1, cap, 64, 128)
+    w = np.exp(2 * rng.normal(size=ca.c["w"].shape))
+    if kind == "ties":
+        w = np.floor(w)
+    elif kind == "nan":
+        w[rng.random(w.shape) < 0.5] = np.nan
+    ca.c["w"] = w.astype(np.float32).astype(np.float64)
+    ca.load()
+    for keep, sink, recent in ((9000, 5, 100), (1, 0, 0), (128, 64, 64)):
+        evict_both(ca, keep, sink, recent, -(-keep // 128) * 128, rng, 128)
+    assert status() == ea.ATTN_OK
 
 
 # ------------------------------------------------------------------ as they are used
