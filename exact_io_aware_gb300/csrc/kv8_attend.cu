@@ -273,8 +273,9 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
         for (int j = 0; j < NT; ++j) {
           const int r = pl.rt * kTile + j * 8 + g;
           float x[D / 4];
-          load_q_row<kBf16, D>(
-              r < geo.R ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
+          // Padding rows may hold anything: they must not enter the size of the real ones.
+          const bool real = r < geo.R && geo.query(r) < cnt;
+          load_q_row<kBf16, D>(real ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
           if (pass) {
             pack_q<D>(x, qmul, q[j]);
           } else {

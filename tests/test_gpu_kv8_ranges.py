@@ -1,0 +1,46 @@
+"""The 8-bit cache's attention and weights over the whole range of values their inputs may have.
+
+Bounds are those of test_gpu_kv8.py (counted from the roundings there), with a term of its own
+where a test says so.
+"""
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_gb300 as ea
+from oracle import kv8
+from test_gpu_kv8 import DT, Cache, attend_bounds, check_attend, i32, rounded, status
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ padding rows
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,G,n", [(128, 1, 5), (128, 3, 5), (64, 4, 8), (128, 8, 6), (64, 5, 60)])
+@pytest.mark.parametrize("cap", [384, 1024])
+def test_what_padding_rows_hold_does_not_matter(dtype, d, G, n, cap):
+    """Real rows come out bit for bit alike whatever the padding rows of q hold."""
+    rng = np.random.default_rng(G * n)
+    lengths = [cap, 17, 200, 0, 129]
+    counts = [1, n - 1, n // 2, 0, n]
+    ca = Cache(rng, lengths, 2, cap, d, 64)
+    q = rounded(rng.normal(size=(5, 2 * G, n, d)), dtype)
+    pad = (np.arange(n) >= np.array(counts)[:, None])[:, None, :, None]
+    pad = torch.from_numpy(np.broadcast_to(pad, q.shape).copy())
+    q[pad] = 0.0
+    kw = dict(counts=i32(counts), mask="causal")
+    args = (ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, d ** -0.5)
+    o, lse = ea.attn_fwd_kv8(q.cuda(), *args, **kw)
+    check_attend(ca, q, d ** -0.5, dtype, o, lse, counts, True)
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, lse, None, d ** -0.5, **kw)
+    for bad in (torch.finfo(DT[dtype]).max, 2.0 ** 15 if dtype == "f16" else 2.0 ** 60, float("inf"),
+                float("-inf"), float("nan")):
+        sick = q.clone()
+        sick[pad] = bad
+        o2, lse2 = ea.attn_fwd_kv8(sick.cuda(), *args, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), bad
+        w2 = ea.attn_kv8_weights(sick.cuda(), ca.k8, ca.ks, ca.lengths, lse, None, d ** -0.5, **kw)
+        assert torch.equal(w, w2), bad
+    # the sequence of 17 has more than 17 queries where n is large: the first see no key
+    assert status() == (ea.ATTN_WARN_EMPTY_ROW if n - 1 > 17 else ea.ATTN_OK)
