@@ -60,7 +60,7 @@ constexpr size_t merge_bytes() {
 // One chunk of 32 keys against the tile's rows.  kPair: P as a pair of fp16 values.
 template <int D, int NT, bool kPair>
 __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool masked, int block,
-                                             float kmul, const QFrag<D> (&q)[NT],
+                                             const float (&kmul)[NT][2], const QFrag<D> (&q)[NT],
                                              const int (&lim)[NT][2], float (&z)[NT][D / 16][4],
                                              float (&l)[NT][2], float (&m)[NT][2]) {
   const int lane = lane_id(), g = lane >> 2, t = lane & 3;
@@ -71,14 +71,15 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     scores16<D, NT>(st, mt, q, x[mt]);
-    const float kf = kmul * sc[mt], vs = sc[2 + mt];
+    const float ks = sc[mt], vs = sc[2 + mt];
     const float lvs = log2f(vs);
     inv_vs[mt] = 1.0f / vs;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      const float kf[2] = {kmul[j][0] * ks, kmul[j][1] * ks};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float y = fmaf(x[mt][j][e], kf, lvs);
+        float y = fmaf(x[mt][j][e], kf[e & 1], lvs);
         if (masked) {
           const int key = key0 + mt * 16 + (e >> 1) * 8 + Chunk<D>::key_of_slot(g);
           if (key >= lim[j][e & 1]) y = -INFINITY;
@@ -86,6 +87,7 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
         x[mt][j][e] = y;
         top = fmaxf(top, y - m[j][e & 1]);
       }
+    }
   }
   if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
 #pragma unroll
@@ -259,43 +261,29 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(c0 + warp + i * kAttendWarps, i);
 
-    // Queries of the tile as fp16 times 2^e.
+    // Queries of the tile as fp16 times a power of two a row.
     QFrag<D> q[NT];
+    float kmul[NT][2];
     int lim[NT][2];
     int least = len;  // keys every real row sees
-    float qmul;
-    {
-      float amax = 0.0f;
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        if (pass) qmul = pow2(q_exp(warp_max(amax)));
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int r = pl.rt * kTile + j * 8 + g;
-          float x[D / 4];
-          // Padding rows may hold anything: they must not enter the size of the real ones.
-          const bool real = r < geo.R && geo.query(r) < cnt;
-          load_q_row<kBf16, D>(real ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
-          if (pass) {
-            pack_q<D>(x, qmul, q[j]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, finite_abs(x[e]));
-          }
-        }
+    for (int j = 0; j < NT; ++j) {
+      {
+        const int r = pl.rt * kTile + j * 8 + g;
+        const bool real = r < geo.R && geo.query(r) < cnt;  // what padding rows hold does not matter
+        float x[D / 4];
+        load_q_row<kBf16, D>(real ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
+        pack_q<D>(x, p.c2, q[j], kmul[j]);
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = pl.rt * kTile + j * 8 + 2 * t + c;
-          const bool real = r < geo.R && geo.query(r) < cnt;
-          lim[j][c] = real ? query_keys(geo, len, cnt, geo.query(r)) : len;
-          least = min(least, lim[j][c]);
-        }
-      least = __reduce_min_sync(0xFFFFFFFFu, least);
+      for (int c = 0; c < 2; ++c) {
+        const int r = pl.rt * kTile + j * 8 + 2 * t + c;
+        const bool real = r < geo.R && geo.query(r) < cnt;
+        lim[j][c] = real ? query_keys(geo, len, cnt, geo.query(r)) : len;
+        least = min(least, lim[j][c]);
+      }
     }
-    const float kmul = p.c2 / qmul;
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
 
     float z[NT][D / 16][4], l[NT][2], m[NT][2];
 #pragma unroll

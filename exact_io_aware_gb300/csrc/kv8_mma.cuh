@@ -116,21 +116,32 @@ __device__ __forceinline__ void load_q_row(const uint16_t* row, float (&x)[D / 4
   }
 }
 
-// Exponent that brings the largest finite |q| of a warp's rows to 2^14 .. 2^15: queries enter
-// the products as fp16 times a power of two, so bf16 rows keep their range, and values down to
-// 2^-31 of the largest keep all of their bits.
+// Exponent that brings a row's largest finite |q| to 2^14 .. 2^15: queries enter the products as
+// fp16 times a power of two of their own, so bf16 rows keep their range whatever the other rows
+// hold, and values down to 2^-31 of the row's largest keep all of their bits.
 __device__ __forceinline__ int q_exp(float amax) {
   const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
   return min(max(14 - e, -100), 100);
 }
 
+// The lane's share `x` of its row (lane / 4 of eight) as a fragment, and in kmul the factors of the
+// scores of rows 2t and 2t + 1 (those of the lane's accumulators): c2 over the rows' powers of two.
 template <int D>
-__device__ __forceinline__ void pack_q(const float (&x)[D / 4], float mul, QFrag<D>& f) {
+__device__ __forceinline__ void pack_q(const float (&x)[D / 4], float c2, QFrag<D>& f, float (&kmul)[2]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+  const float mul = pow2(q_exp(amax)), factor = c2 / mul;
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
     f.b[s][0] = pack_f16(x[4 * s] * mul, x[4 * s + 1] * mul);
     f.b[s][1] = pack_f16(x[4 * s + 2] * mul, x[4 * s + 3] * mul);
   }
+  const int t = lane_id() & 3;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) kmul[c] = __shfl_sync(0xFFFFFFFFu, factor, (2 * t + c) * 4);
 }
 
 // Scores of 16 keys (slots g and g + 8 of half `mt` of the chunk) with NT blocks of 8 rows:

@@ -73,39 +73,26 @@ __global__ void __launch_bounds__(kWeightsThreads, weights_ctas_per_sm<NT>())
     float neg_lse[NT][2];  // -log2(e) LSE
     int lim[NT][2];        // keys the row sees; 0 for a row that counts for nothing
     int least = len;
-    float qmul;
-    {
-      float amax = 0.0f;
+    float kmul[NT][2];
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        if (pass) qmul = pow2(q_exp(warp_max(amax)));
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int r = j * 8 + g;
-          float x[D / 4];
-          load_q_row<kBf16, D>(r < geo.R && geo.query(r) < cnt ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
-          if (pass) {
-            pack_q<D>(x, qmul, q[j]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, finite_abs(x[e]));
-          }
-        }
+    for (int j = 0; j < NT; ++j) {
+      {
+        const int r = j * 8 + g;
+        float x[D / 4];
+        load_q_row<kBf16, D>(r < geo.R && geo.query(r) < cnt ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
+        pack_q<D>(x, p.c2, q[j], kmul[j]);
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = j * 8 + 2 * t + c;
-          const bool real = r < geo.R && geo.query(r) < cnt;
-          const float lse = real ? __ldg(p.lse + geo.row_offset(pl.b, pl.hk, r)) : -INFINITY;
-          neg_lse[j][c] = lse != -INFINITY ? -lse * kLog2e : -INFINITY;
-          lim[j][c] = lse != -INFINITY ? query_keys(geo, len, cnt, geo.query(r)) : 0;
-          least = min(least, lim[j][c]);
-        }
-      least = __reduce_min_sync(0xFFFFFFFFu, least);
+      for (int c = 0; c < 2; ++c) {
+        const int r = j * 8 + 2 * t + c;
+        const bool real = r < geo.R && geo.query(r) < cnt;
+        const float lse = real ? __ldg(p.lse + geo.row_offset(pl.b, pl.hk, r)) : -INFINITY;
+        neg_lse[j][c] = lse != -INFINITY ? -lse * kLog2e : -INFINITY;
+        lim[j][c] = lse != -INFINITY ? query_keys(geo, len, cnt, geo.query(r)) : 0;
+        least = min(least, lim[j][c]);
+      }
     }
-    const float kmul = p.c2 / qmul;
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
 
     int stage = 0;
     for (int ch = c0 + warp; ch < c1; ch += kWeightsWarps) {
@@ -119,19 +106,21 @@ __global__ void __launch_bounds__(kWeightsThreads, weights_ctas_per_sm<NT>())
       for (int mt = 0; mt < 2; ++mt) {
         float acc[NT][4];
         scores16<D, NT>(st, mt, q, acc);
-        const float kf = kmul * sc[mt];
+        const float ks = sc[mt];
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+          const float kf[2] = {kmul[j][0] * ks, kmul[j][1] * ks};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float pr = ex2(fmaf(acc[j][e], kf, neg_lse[j][e & 1]));
+            float pr = ex2(fmaf(acc[j][e], kf[e & 1], neg_lse[j][e & 1]));
             if (key0 + kChunk > least) {
               const int key = key0 + mt * 16 + (e >> 1) * 8 + Chunk<D>::key_of_slot(g);
               if (key >= lim[j][e & 1]) pr = 0.0f;
             }
             sum[e >> 1] += pr;
           }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float s = sum[e];

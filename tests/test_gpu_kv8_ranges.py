@@ -44,3 +44,29 @@ def test_what_padding_rows_hold_does_not_matter(dtype, d, G, n, cap):
         assert torch.equal(w, w2), bad
     # the sequence of 17 has more than 17 queries where n is large: the first see no key
     assert status() == (ea.ATTN_WARN_EMPTY_ROW if n - 1 > 17 else ea.ATTN_OK)
+
+
+# ------------------------------------------------------------------ rows of different sizes
+
+@pytest.mark.parametrize("d,G,n", [(128, 4, 1), (128, 8, 2), (64, 8, 4)])
+def test_each_row_keeps_its_bits_beside_much_larger_rows(d, G, n):
+    """Rows of one head that differ by 2^45, the small ones' scores of size one: an attention of
+    their own, and weights."""
+    rng = np.random.default_rng(d + G)
+    m = 300
+    ca = Cache(rng, [m], 2, 384, d, 32)
+    x = rng.normal(size=(1, 2 * G, n, d))
+    x[:, ::4] *= 2.0 ** 45
+    q = rounded(x, "bf16")
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, d ** -0.5)
+    check_attend(ca, q, d ** -0.5, "bf16", o, lse)
+    # The large rows count for nothing in the sums.
+    _, L, _, S, _ = kv8.attend(ca.c, q.double().numpy(), d ** -0.5)
+    L[:, ::4], S[:, ::4] = -np.inf, 0.0
+    given = torch.from_numpy(L).float()
+    ref = kv8.add_weights(ca.c, q.double().numpy(), d ** -0.5, given.double().numpy()) - ca.c["w"]
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, given.cuda(), None, d ** -0.5)
+    rel = (d + 16) * 2.0 ** -23 * (S.max() + 32.0) + 2.0 ** -21 + G * n * 2.0 ** -24
+    got = w.double().cpu().numpy()
+    assert (np.abs(got - ref)[..., :m] <= rel * ref[..., :m]).all()
+    status()
