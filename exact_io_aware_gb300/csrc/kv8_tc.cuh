@@ -94,6 +94,10 @@ struct Shared {
 // Least factor of a score: 0 (c = 0) would turn masked scores, -inf, to NaN.
 constexpr float kLeastFactor = 1.17549435e-38f;
 
+// block_probs takes x - m in one rounding, so the largest P is off 2^kTop by the rounding of m.
+// Up to this |m| that is at most 2^(1/4); far above, P would leave fp16 or all of a row's be 0.
+constexpr float kExactShift = 4194304.0f;  // 2^22, where float32 steps by 1/2
+
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -226,6 +230,26 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
         const float2 s = add2(sum[0], sum[1]);
         l = fmaf(s.x + s.y, sc.inv_v[g], l);
       }
+    }
+    tmem_st16(tS + c0 / 2, pk);
+  }
+  return l;
+}
+
+// The same, with x rounded before m is taken from it, as the maximum was: for rows past kExactShift.
+__device__ __forceinline__ float block_probs_rounded(const float (&sv)[kBlockKeys], const Scales& sc, float mul,
+                                                     float m, uint32_t tS) {
+  float l = 0.0f;
+#pragma unroll
+  for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const int key = c0 + k, g = key / 16;
+      const float f = fmaxf(sc.k[g] * mul, kLeastFactor);
+      const float p0 = ex2(fmaf(sv[key], f, sc.log2_v[g]) - m), p1 = ex2(fmaf(sv[key + 1], f, sc.log2_v[g]) - m);
+      l = fmaf(p0 + p1, sc.inv_v[g], l);
+      pk[k / 2] = pack2<false>(p0, p1);
     }
     tmem_st16(tS + c0 / 2, pk);
   }
@@ -593,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
-      bool first = true;
+      bool first = true, far = false;  // far: a real row of the warp has |m| past kExactShift
       for (int i = i0; i < steps; i += stride) {
         const uint32_t c = gi + i;
         ok = mbar_wait_warp(&sh.sc_full[c & 3], (c >> 2) & 1, p.status, 0x2D) &&
@@ -628,9 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mn;
           l *= alpha;
         }
-        if (__builtin_expect(!first && __any_sync(0xFFFFFFFFu, alpha != 1.0f), 0)) {
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, alpha != 1.0f), 0)) {
+          far = __any_sync(0xFFFFFFFFu, real && fabsf(m) > kExactShift && m != kNoMax);
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
+          for (int c0 = first ? D : 0; c0 < D; c0 += 16) {
             uint32_t rr[16];
             tmem_ld16(tO + c0, rr);
             tmem_wait_ld();
@@ -645,7 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           turn_phase ^= 1u;
         }
-        l += uniform ? block_probs<1>(sv, sc, mul, m, tS) : block_probs<kGroups>(sv, sc, mul, m, tS);
+        if (__builtin_expect(far, 0))
+          l += block_probs_rounded(sv, sc, mul, m, tS);
+        else
+          l += uniform ? block_probs<1>(sv, sc, mul, m, tS) : block_probs<kGroups>(sv, sc, mul, m, tS);
         __syncwarp();
         if (lane == 0 && i + t < both) mbar_arrive(&sh.turn[t ^ 1]);
         tmem_wait_st();

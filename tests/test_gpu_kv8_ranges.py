@@ -70,3 +70,35 @@ def test_each_row_keeps_its_bits_beside_much_larger_rows(d, G, n):
     got = w.double().cpu().numpy()
     assert (np.abs(got - ref)[..., :m] <= rel * ref[..., :m]).all()
     status()
+
+
+# ------------------------------------------------------------------ large scores
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,G,n", [(128, 4, 1), (64, 8, 4), (128, 8, 6), (64, 4, 70)])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 27, 2.0 ** 45])
+def test_scores_far_past_the_step_of_float32(dtype, d, G, n, size):
+    """Scores so large that the step of float32 passes 2^14 in the exponent: the row's largest score
+    is alone (the inputs are drawn until its lead is 2^-12 of the sums that make it, whose float32 error
+    is below (d + 16) 2^-23), so O is that key's V, off by half a step of P in fp16 (2^-11; its sum l takes P
+    unrounded) and half a step of the output, and LSE its score."""
+    rng = np.random.default_rng(int(np.log2(size)) + d)
+    m, c = 300, 0.1 * size
+    ca = Cache(rng, [m], 1, 384, d, 32)
+    x = rng.normal(size=(1, G, n, d))
+    for g in range(G):
+        for i in range(n):
+            k = ca.c["k8"][0, 0, :m] * np.repeat(ca.c["ks"][0, 0], 32)[:m, None]
+            while True:
+                row = rounded(x[0, g, i], dtype).double().numpy()
+                s = np.sort(k @ row)
+                if s[-1] - s[-2] > 2.0 ** -12 * (np.abs(k) @ np.abs(row)).max():
+                    break
+                x[0, g, i] = rng.normal(size=d)
+    q = rounded(x, dtype)
+    O, L, A, S, _ = kv8.attend(ca.c, q.double().numpy(), c)
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, c)
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(o - O) <= (1.01 * torch.finfo(DT[dtype]).eps / 2 + 2.0 ** -11) * np.abs(O) + 2.0 ** -25).all()
+    assert (np.abs(lse - L) <= (d + 16) * 2.0 ** -23 * S + 2.0 ** -15).all()
+    assert status() == ea.ATTN_OK
