@@ -7,7 +7,7 @@
 //     z_r = sum_j P_rj v_j,   l_r = sum_j P_rj / vs_j,   O_r = z_r / l_r,
 //     LSE_r = ln 2 (m_r + log2 l_r),
 // so a value block's scale costs one constant a block: P is what the product takes and z needs
-// no second scaling.  P enters that product as fp16 (half a step 2^-11, an eighth of the bf16
+// no second scaling (scales at the ends of their range: kv8_attend.cuh).  P enters that product as fp16 (half a step 2^-11, an eighth of the bf16
 // output's; for fp16 outputs, whose own rounding that would equal, as a pair of fp16 values and
 // two products); m_r is set so that the largest P is 2^6 and is raised only when a P would
 // pass 2^14, which keeps P inside fp16 and weights down to 2^-20 of the largest at full precision
@@ -62,24 +62,35 @@ template <int D, int NT, bool kPair>
 __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool masked, int block,
                                              const float (&kmul)[NT][2], const QFrag<D> (&q)[NT],
                                              const int (&lim)[NT][2], float (&z)[NT][D / 16][4],
-                                             float (&l)[NT][2], float (&m)[NT][2]) {
+                                             float (&l)[NT][2], float (&m)[NT][2], float& hi) {
   const int lane = lane_id(), g = lane >> 2, t = lane & 3;
   const float* sc = reinterpret_cast<const float*>(st + 2 * Chunk<D>::kBytes);
   float x[2][NT][4];
-  float inv_vs[2];
+  float lvs[2] = {log2f(sc[2]), log2f(sc[3])}, inv_vs[2] = {kLiftFactor / sc[2], kLiftFactor / sc[3]};
+  float rest[2] = {1.0f, 1.0f};  // factor of what the V product takes
+  hi = fmaxf(hi, fmaxf(lvs[0], lvs[1]));
+  const float floor = fmaxf(kLeastScale, hi - kScaleSpan);
+  const bool small = fminf(lvs[0], lvs[1]) < floor;  // the same in every lane
+  if (__builtin_expect(small, 0)) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      if (lvs[mt] >= floor) continue;
+      rest[mt] = ex2(lvs[mt] - floor);
+      inv_vs[mt] = ex2(kLift - floor);
+      lvs[mt] = floor;
+    }
+  }
   float top = -INFINITY;  // largest excess of x over the allowed shift
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     scores16<D, NT>(st, mt, q, x[mt]);
-    const float ks = sc[mt], vs = sc[2 + mt];
-    const float lvs = log2f(vs);
-    inv_vs[mt] = 1.0f / vs;
+    const float ks = sc[mt];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const float kf[2] = {kmul[j][0] * ks, kmul[j][1] * ks};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float y = fmaf(x[mt][j][e], kf[e & 1], lvs);
+        float y = fmaf(x[mt][j][e], kf[e & 1], lvs[mt]);
         if (masked) {
           const int key = key0 + mt * 16 + (e >> 1) * 8 + Chunk<D>::key_of_slot(g);
           if (key >= lim[j][e & 1]) y = -INFINITY;
@@ -98,9 +109,9 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
         const float mn = fmaxf(m[j][c], mx - kTop);
-        const float r = ex2(m[j][c] - mn);
+        const float half = ex2(0.5f * (m[j][c] - mn)), r = half * half;
         m[j][c] = mn;
-        l[j][c] *= r;
+        l[j][c] = l[j][c] * half * half;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           z[j][i][c] *= r;
@@ -120,6 +131,7 @@ __device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool m
       for (int e = 0; e < 4; ++e) {
         pr[e] = ex2(x[mt][j][e] - m[j][e & 1]);
         l[j][e & 1] = fmaf(pr[e], inv_vs[mt], l[j][e & 1]);
+        if (small) pr[e] *= rest[mt];
       }
       const uint32_t h0 = pack_f16(pr[0], pr[1]), h1 = pack_f16(pr[2], pr[3]);
       b0[j] = transpose8x8(h0);
@@ -295,6 +307,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       l[j][0] = l[j][1] = 0.0f;
       m[j][0] = m[j][1] = kNoMax;
     }
+    float hi = -INFINITY;  // log2 of the largest V scale so far
 
     int stage = 0;
     for (int ch = c0 + warp; ch < c1; ch += kAttendWarps) {
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       issue(ch + (kStages - 1) * kAttendWarps, ahead);
       const int key0 = ch * kChunk;
       const bool masked = key0 + kChunk > least;
-      attend_chunk<D, NT, !kBf16>(ring + stage * stage_bytes<D>(), key0, masked, p.block, kmul, q, lim, z, l, m);
+      attend_chunk<D, NT, !kBf16>(ring + stage * stage_bytes<D>(), key0, masked, p.block, kmul, q, lim, z, l, m, hi);
       __syncwarp();
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -349,13 +362,13 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       float ls = 0.0f;
 #pragma unroll
       for (int w = 0; w < kAttendWarps; ++w) {
-        const float f = ex2(mlm[(w * kTile + at) * 2 + 1] - mx);
+        const float half = ex2(0.5f * (mlm[(w * kTile + at) * 2 + 1] - mx)), f = half * half;
         const float4 x = *reinterpret_cast<const float4*>(mz + (w * kTile + at) * kStride + col);
         zs.x = fmaf(f, x.x, zs.x);
         zs.y = fmaf(f, x.y, zs.y);
         zs.z = fmaf(f, x.z, zs.z);
         zs.w = fmaf(f, x.w, zs.w);
-        ls = fmaf(f, mlm[(w * kTile + at) * 2], ls);
+        ls = fmaf(mlm[(w * kTile + at) * 2] * half, half, ls);
       }
       const int r = pl.rt * kTile + row;
       if (whole) {

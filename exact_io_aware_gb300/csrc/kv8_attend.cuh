@@ -10,6 +10,24 @@ constexpr float kTop = 6.0f;     // log2 of the largest P when m is set
 constexpr float kRaise = 14.0f;  // a larger log2 P raises m
 constexpr float kNoMax = -3.0e38f;
 
+// The sum l.  P follows x, the score and log2 of its V block's scale, while l adds 2^(s - m) of the
+// bare score s as P / vs, and scales lie anywhere in 2^-100 .. 2^120 (a block of zeros has 2^-100).
+// So that l neither overflows nor loses keys:
+//   * scales below 2^kLeastScale, or more than 2^kScaleSpan below the tile's largest so far, enter x
+//     and l as that bound, and what the V product takes of the block is multiplied by the rest (in
+//     fp16: 2^-95 of a row's O, or 2^-101 of a code a key, can be lost).  P of a key that counts
+//     (2^-24 of the largest 2^s) is then above 2^-126, where ex2 flushes, and s below m + 84;
+//   * l is kept 2^kLift times as large: up to 2^30 keys sum to less than 2^127, and under scales of
+//     2^120 keys of 2^-24 of the largest still count;
+//   * factors of l that a new m brings are applied as two halves: one could be flushed where its
+//     product with l is not.
+constexpr float kLift = 12.0f;
+constexpr float kLiftFactor = 4096.0f;
+constexpr float kLeastScale = -70.0f;
+constexpr float kScaleSpan = 96.0f;
+// A row's LSE from its l and m.
+__device__ __forceinline__ float row_lse(float l, float m) { return kLn2 * (m + log2f(l * (1.0f / kLiftFactor))); }
+
 template <class Geo>
 struct AttendParams {
   Geo geo;
@@ -36,7 +54,7 @@ template <bool kBf16, int D, class Geo>
 __device__ __forceinline__ void write_out(const AttendParams<Geo>& p, int64_t row, int col, float4 z,
                                           float l, float m, bool real) {
   const bool none = l == 0.0f || !real;
-  const float inv = none ? 0.0f : 1.0f / l;
+  const float inv = none ? 0.0f : kLiftFactor / l;
   uint2 w;
   if constexpr (kBf16) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(z.x * inv, z.y * inv), b = __floats2bfloat162_rn(z.z * inv, z.w * inv);
@@ -47,7 +65,7 @@ __device__ __forceinline__ void write_out(const AttendParams<Geo>& p, int64_t ro
   if (none) w = make_uint2(0u, 0u);
   *reinterpret_cast<uint2*>(p.o + row * D + col) = w;
   if (col == 0) {
-    p.lse[row] = none ? -INFINITY : kLn2 * (m + log2f(l));
+    p.lse[row] = none ? -INFINITY : row_lse(l, m);
     if (none && real) raise_empty_row(p.status);
   }
 }
@@ -105,13 +123,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
       const int parts = min(all - q0, 32);
       float2 lm = make_float2(0.0f, kNoMax);
       if (lane < parts) lm = *reinterpret_cast<const float2*>(p.part_lm + place(q0 + lane) * 2);
-      const float mn = fmaxf(mx, warp_max(lm.y)), old = ex2(mx - mn);
+      const float mn = fmaxf(mx, warp_max(lm.y)), old_half = ex2(0.5f * (mx - mn)), old = old_half * old_half;
       mx = mn;
-      const float f = ex2(lm.y - mx);
-      float ls = f * lm.x;
+      const float half = ex2(0.5f * (lm.y - mx)), f = half * half;
+      float ls = lm.x * half * half;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
-      l = fmaf(l, old, ls);
+      l = fmaf(l * old_half, old_half, ls);
 #pragma unroll
       for (int i = 0; i < kCols; ++i) z[i] *= old;
 #pragma unroll 4

@@ -66,15 +66,17 @@ struct Seg {
   int b, hk, len, cnt;
   int r0;            // first row
   int j0, steps;     // first block and number of blocks
+  bool last;         // of the run
   bool whole;        // the tile is this CTA's alone
   int slot;          // else where its part goes
   int reach[2];      // blocks row tile t takes, counted from block 0
   int least[2];      // keys every real row of row tile t sees (blocks past them are masked)
-  bool last;         // of the run
 };
 
 struct Scales {  // of one block, per 16 keys
-  float k[kGroups], log2_v[kGroups], inv_v[kGroups];
+  float k[kGroups], log2_v[kGroups], inv_v[kGroups];  // inv_v: 2^kLift / vs
+  int8_t rest[kGroups];  // log2 of what a raised scale (kv8_attend.cuh) leaves to the V values, else 0
+  bool raised;           // some group's scale was
 };
 
 struct Shared {
@@ -153,6 +155,15 @@ struct ValueRow {
           make_uint4(lo_codes(u[i].z), hi_codes(u[i].z), lo_codes(u[i].w), hi_codes(u[i].w));
     }
   }
+  // Multiplies a stored row by f (a block whose scale was raised).
+  __device__ __forceinline__ static void scale(uint8_t* tile, int key, float f) {
+#pragma unroll 1
+    for (int col = 0; col < D; col += 2) {
+      uint32_t& w = *reinterpret_cast<uint32_t*>(tile + Tile<kBlockKeys, D>::offset(key, col));
+      const float2 x = unpack16<false>(w);
+      w = pack2<false>(x.x * f, x.y * f);
+    }
+  }
   // Takes NaN codes out (to 0); true if there were any.
   __device__ __forceinline__ bool drop_nan() {
     bool any = false;
@@ -207,7 +218,7 @@ __device__ __forceinline__ float block_max(const float (&sv)[kBlockKeys], const 
 }
 
 // P of the row under m into TMEM at tS (over the scores), two 16-bit values a word; returns the
-// row's sum of P / vs.
+// row's sum of 2^kLift P / vs.
 template <int kG>
 __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], const Scales& sc, float mul, float m,
                                              uint32_t tS) {
@@ -236,20 +247,28 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
   return l;
 }
 
-// The same, with x rounded before m is taken from it, as the maximum was: for rows past kExactShift.
-__device__ __forceinline__ float block_probs_rounded(const float (&sv)[kBlockKeys], const Scales& sc, float mul,
-                                                     float m, uint32_t tS) {
+// The same for rows past kExactShift: x is rounded before m is taken from it, as the maximum was.
+// The scores are read from tensor memory again, in a rolled loop, so that the common path pays for
+// this neither registers nor instruction fetches.  `seen`: keys of the block that the row sees.
+__device__ __forceinline__ float far_probs(const Scales& sc, float mul, float m, int seen, uint32_t tS) {
   float l = 0.0f;
-#pragma unroll
+#pragma unroll 1
   for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
-    uint32_t pk[16];
+    uint32_t s[32], pk[16];
+    tmem_ld32(tS + c0, s);
+    tmem_wait_ld();
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      const int key = c0 + k, g = key / 16;
+      const int g = (c0 + k) / 16;
       const float f = fmaxf(sc.k[g] * mul, kLeastFactor);
-      const float p0 = ex2(fmaf(sv[key], f, sc.log2_v[g]) - m), p1 = ex2(fmaf(sv[key + 1], f, sc.log2_v[g]) - m);
-      l = fmaf(p0 + p1, sc.inv_v[g], l);
-      pk[k / 2] = pack2<false>(p0, p1);
+      float pr[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = fmaf(__uint_as_float(s[k + e]), f, sc.log2_v[g]);
+        pr[e] = c0 + k + e < seen ? ex2(x - m) : 0.0f;
+        l = fmaf(pr[e], sc.inv_v[g], l);
+      }
+      pk[k / 2] = pack2<false>(pr[0], pr[1]);
     }
     tmem_st16(tS + c0 / 2, pk);
   }
@@ -482,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* ksp = p.k_scales + static_cast<int64_t>(bh) * nblk;
         const float* vsp = p.v_scales + static_cast<int64_t>(bh) * nblk;
         // A block's scales, one lane to 16 keys, fetched a block ahead.  Their place's last readers
-        // were softmax four blocks ago; the scores of two blocks ago (k_empty) came after P V of
-        // those.
+        // were softmax and the converters four blocks ago; the scores of two blocks ago (k_empty) came
+        // after P V of those.
         float ks, vs;
         auto fetch = [&](int i) {
           const int key = (j0 + i) * kBlockKeys + lane * 16;
@@ -492,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           vs = in ? __ldg(vsp + key / p.block) : 1.0f;
         };
         fetch(0);
+        int hi = -200;  // exponent of the tile's largest V scale so far
         for (int i = 0; i < steps && ok; ++i) {
           const uint32_t c = gi + i, rs = c % C::kSR;
           const int key0 = (j0 + i) * kBlockKeys;
@@ -501,14 +521,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&sh.k_full[c & 1], T8::kBytes);
             tma_load_3d(sK + (c & 1) * T8::kBytes, &tm_k, &sh.k_full[c & 1], 0, key0, bh);
           }
+          const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 127;
+          const bool in = lane < kGroups && key0 + lane * 16 < len;
+          hi = max(hi, __reduce_max_sync(0xFFFFFFFFu, in ? e : -200));
+          const int floor = max(static_cast<int>(kLeastScale), hi - static_cast<int>(kScaleSpan));
+          const bool raised = __any_sync(0xFFFFFFFFu, in && e < floor);
+          int rest = 0;  // whole powers of two, so the values stay exact down to fp16's subnormals
+          if (in && e < floor) {
+            rest = max(e - floor, -126);
+            vs *= pow2(-rest);
+          }
           if (lane < kGroups) {
             Scales& sc = sh.scales[c & 3];
             sc.k[lane] = ks;
             sc.log2_v[lane] = log2f(vs);
-            sc.inv_v[lane] = 1.0f / vs;
+            sc.inv_v[lane] = kLiftFactor / vs;
+            sc.rest[lane] = static_cast<int8_t>(rest);
+            if (lane == 0) sc.raised = raised;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.sc_full[c & 3]);
+          if (lane == 0) mbar_arrive(&sh.sc_full[c & 3]);  // (the converters are told by r_full)
           ok = mbar_wait_warp(&sh.r_empty[rs], ((c / C::kSR) & 1) ^ 1, p.status, 0x28);
           if (!ok) break;
           if (lane == 0) {
@@ -563,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < steps && ok; ++i) {
         const uint32_t c = gi + i;
         const int key0 = (j0 + i) * kBlockKeys;
+        const bool raised = sh.scales[c & 3].raised;  // there since r_full
         ok = mbar_wait_warp(&sh.v_empty[c & 1], ((c >> 1) & 1) ^ 1, p.status, 0x2C);
         if (!ok) break;
         if (key0 + kBlockKeys > least) {
@@ -570,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (x.drop_nan()) atomicOr(&sh.nan_seen[seg & 3], 1u);
         }
         x.store(sV + (c & 1) * TV::kBytes, tid);
+        if (__builtin_expect(raised, 0)) x.scale(sV + (c & 1) * TV::kBytes, tid, pow2(sh.scales[c & 3].rest[tid / 16]));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full[c & 1]);
@@ -647,10 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mx = uniform ? block_max<1>(sv, sc, mul) : block_max<kGroups>(sv, sc, mul);
         float alpha = 1.0f;
         if (mx - m > kRaise) {
-          const float mn = mx - kTop;
-          alpha = ex2(m - mn);
+          const float mn = mx - kTop, half = ex2(0.5f * (m - mn));
+          alpha = half * half;
           m = mn;
-          l *= alpha;
+          l = l * half * half;
         }
         if (__builtin_expect(__any_sync(0xFFFFFFFFu, alpha != 1.0f), 0)) {
           far = __any_sync(0xFFFFFFFFu, real && fabsf(m) > kExactShift && m != kNoMax);
@@ -671,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           turn_phase ^= 1u;
         }
         if (__builtin_expect(far, 0))
-          l += block_probs_rounded(sv, sc, mul, m, tS);
+          l += far_probs(sc, mul, m, lim - key0, tS);
         else
           l += uniform ? block_probs<1>(sv, sc, mul, m, tS) : block_probs<kGroups>(sv, sc, mul, m, tS);
         __syncwarp();
@@ -724,9 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           h_phase ^= 1u;
           const float2 lm = __ldcg(hand_lm);
           const float mx = fmaxf(m, lm.y);
-          f0 = ex2(m - mx);
-          f1 = ex2(lm.y - mx);
-          l = l * f0 + lm.x * f1;
+          const float h0 = ex2(0.5f * (m - mx)), h1 = ex2(0.5f * (lm.y - mx));
+          f0 = h0 * h0;
+          f1 = h1 * h1;
+          l = l * h0 * h0 + lm.x * h1 * h1;
           m = mx;
         }
         // A masked block's V held NaN codes, which were kept out of the product: the columns of
@@ -752,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool write = row < geo.R;
         const bool none = l == 0.0f || !real;  // a padding row, or one that sees no key
-        const float inv = 1.0f / l;
+        const float inv = kLiftFactor / l;
         const int64_t orow = geo.row_offset(sg.b, sg.hk, row);
         const int64_t prow = static_cast<int64_t>(sg.slot) * geo.tile + (row - sg.r0);
 #pragma unroll 1
@@ -806,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (write && sg.whole) {
-          p.lse[orow] = none ? -INFINITY : kLn2 * (m + log2f(l));
+          p.lse[orow] = none ? -INFINITY : row_lse(l, m);
           if (none && real) raise_empty_row(p.status);
         }
         if (write && !sg.whole) *reinterpret_cast<float2*>(p.part_lm + prow * 2) = make_float2(l, m);

@@ -247,8 +247,9 @@ int attn_fwd_fp8_blocks(int B, int H, int n, int d, float c,
  * d: 64 or 128; block: 16, 32, 64 or 128; cap: a multiple of block, at most 2^30; B * H_kv at
  * most 65535; for attention and weights H / H_kv * n_q at most 2^24, and the steps of 32 keys
  * (128 for more than 16 rows a key/value head) over all heads and tiles of rows below 2^30.
- * Scales must be positive and finite (those of blocks with no held token are not read); the
- * entry points below write powers of two, which E4M3, a floating-point format, loses no
+ * Scales must be positive, finite and, of V, at most 2^120 (those of blocks with no held token are
+ * not read); attention may lose what is below 2^-90 of its output.  The entry points below write
+ * powers of two, which E4M3, a floating-point format, loses no
  * precision to, so codes move between blocks exactly down to E4M3's subnormals.  What lies past
  * a sequence's length is neither used nor changed.  A length outside [0, cap] or a count
  * outside [0, n] is clamped and raises ATTN_WARN_CLAMPED.  Code arrays and 16-bit arrays are

@@ -102,3 +102,92 @@ def test_scores_far_past_the_step_of_float32(dtype, d, G, n, size):
     assert (np.abs(o - O) <= (1.01 * torch.finfo(DT[dtype]).eps / 2 + 2.0 ** -11) * np.abs(O) + 2.0 ** -25).all()
     assert (np.abs(lse - L) <= (d + 16) * 2.0 ** -23 * S + 2.0 ** -15).all()
     assert status() == ea.ATTN_OK
+
+
+# ------------------------------------------------------------------ value scales
+
+FEW_AND_MANY = [(4, 1), (4, 4), (8, 6), (4, 70)]
+
+
+@pytest.mark.parametrize("G,n", FEW_AND_MANY)
+@pytest.mark.parametrize("block", [16, 128])
+@pytest.mark.parametrize("exps", [(-100, 40), (40, -100), (-100, 40, -100), (-100, 119), (119, -100, -20, 119),
+                                  (0, -100), (-100, 0), (-100, -100), (60, -60), (-60, 60)])
+def test_value_scales_at_both_ends(G, n, block, exps):
+    """Blocks whose scales lie far apart, as those that hold only zeros (2^-100) and large values
+    give; all scores are equal, so every key has the same weight."""
+    m = block * len(exps) - 3
+    cap = 128 * -(-m // 128)
+    ca = Cache(np.random.default_rng(5), [m], 2, cap, 64, block)
+    ca.c["k8"][0, :, :m] = 0.0
+    for i, e in enumerate(exps):
+        ca.c["vs"][0, :, i] = 2.0 ** e
+        if e == -100:
+            ca.c["v8"][0, :, i * block:min(m, (i + 1) * block)] = 0.0
+    ca.load()
+    q = rounded(np.random.default_rng(6).normal(size=(1, 2 * G, n, 64)), "bf16")
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, 0.125)
+    check_attend(ca, q, 0.125, "bf16", o, lse)
+    assert np.abs(lse.double().cpu().numpy() - np.log(m)).max() <= 2.0 ** -14
+    status()
+
+
+@pytest.mark.parametrize("G,n", FEW_AND_MANY)
+@pytest.mark.parametrize("lo,hi", [(-100, 100), (-100, -90), (90, 110), (-70, -50), (-20, 90)])
+@pytest.mark.parametrize("pow2", [True, False])
+def test_value_scales_over_the_whole_range(G, n, lo, hi, pow2):
+    """Every block's scale drawn over a wide range, the scores random too.  A scale below 2^-70 counts as
+    2^-70 and the values take the rest, in fp16: a value may lose 2^-25 (half a step below its normal
+    values) of 2^-70, or a probability 2^-25 of a code over sums of at least 2^76."""
+    rng = np.random.default_rng(abs(lo) + hi)
+    lengths = [1000, 90]
+    ca = Cache(rng, lengths, 2, 1024, 128, 16, pow2=pow2)
+    for b, m in enumerate(lengths):
+        e = rng.integers(lo, hi + 1, size=(2, -(-m // 16))) + (0.0 if pow2 else rng.random((2, -(-m // 16))))
+        ca.c["vs"][b, :, :-(-m // 16)] = np.float32(2.0 ** e)
+    ca.load()
+    q = rounded(rng.normal(size=(2, 2 * G, n, 128)), "bf16")
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, 0.3, mask="causal")
+    O, L, tol, ltol = attend_bounds(ca, q, 0.3, "bf16", None, True)
+    codes = np.where(np.isnan(ca.c["v8"]), 0.0, np.abs(ca.c["v8"])).sum(2).repeat(G, 1)[:, :, None]
+    # log2 of the scale stands beside the score: float32 values up to 128 + |score|, rounded twice
+    ds = 2.0 ** -16
+    A = kv8.attend(ca.c, q.double().numpy(), 0.3, None, True)[2]
+    assert (np.abs(o.double().cpu().numpy() - O) <= tol + 2 * ds * A + 2.0 ** -95 + 2.0 ** -101 * codes).all()
+    assert (np.abs(lse.double().cpu().numpy() - L) <= ltol + ds).all()
+    status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("G,n", FEW_AND_MANY)
+@pytest.mark.parametrize("first", [True, False])
+def test_value_scales_far_apart_in_parts_of_a_long_sequence(dtype, G, n, first):
+    """Half of the sequence holds zeros, the other large values: CTAs of each half join their parts."""
+    rng = np.random.default_rng(8)
+    cap, m = 8192, 8000
+    ca = Cache(rng, [m], 1, cap, 64, 128)
+    half = slice(0, 4096) if first else slice(4096, m)
+    ca.c["v8"][0, :, half] = 0.0
+    ca.c["vs"][0, :, :63] = 2.0 ** 40 if dtype == "bf16" else 0.125
+    ca.c["vs"][0, :, 0 if first else 32:32 if first else 63] = 2.0 ** -100
+    ca.load()
+    q = rounded(rng.normal(size=(1, G, n, 64)), dtype)
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, 0.125, mask="causal")
+    check_attend(ca, q, 0.125, dtype, o, lse, None, True)
+    status()
+
+
+@pytest.mark.parametrize("G,n", [(1, 1), (8, 5)])
+def test_a_long_sequence_of_zero_values(G, n):
+    """2^22 tokens whose values are all zero (scale 2^-100), in every CTA's part and their join."""
+    cap = 1 << 22
+    codes = torch.zeros(1, 1, cap, 64, dtype=torch.uint8, device="cuda")
+    ks, vs = torch.ones(1, 1, cap // 128, device="cuda"), torch.full((1, 1, cap // 128), 2.0 ** -100, device="cuda")
+    q = torch.ones(1, G, n, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = ea.attn_fwd_kv8(q, codes, codes, ks, vs, i32([cap]), 1.0)
+    assert (o == 0).all()
+    # sums of 2^22 equal terms in float32 over the warps of every CTA
+    assert (lse.double() - np.log(cap)).abs().max() <= 2.0 ** -12
+    w = ea.attn_kv8_weights(q, codes, ks, i32([cap]), lse, None, 1.0)
+    assert (w.double() * cap / (G * n) - 1).abs().max() <= 2.0 ** -11
+    status()
