@@ -9,7 +9,8 @@
 // so a value block's scale costs one constant a block: P is what the product takes and z needs
 // no second scaling (scales at the ends of their range: kv8_attend.cuh).  P enters that product as fp16 (half a step 2^-11, an eighth of the bf16
 // output's; for fp16 outputs, whose own rounding that would equal, as a pair of fp16 values and
-// two products); m_r is set so that the largest P is 2^6 and is raised only when a P would
+// two products, which for bf16 too would take 34.3 us instead of 33.4 on 256 heads of four rows and
+// 48.7 instead of 44.8 on twelve); m_r is set so that the largest P is 2^6 and is raised only when a P would
 // pass 2^14, which keeps P inside fp16 and weights down to 2^-20 of the largest at full precision
 // (the sums z and l are float32).
 //

@@ -9,7 +9,8 @@
 //     to 2^-10 (fp16: 2^-7) of the row's largest; below, what is lost is under 2^-18 of the
 //     largest.  The terms' products add up in one float32 accumulator, and two of them cost what
 //     one product on 16-bit operands would.
-//   * P V is kind::f16: V's codes are widened to fp16 on the way into shared memory (exact).
+//   * P V is kind::f16: V's codes are widened to fp16 on the way into shared memory (exact); for fp16
+//     outputs P is a pair of values (Config::kPair).
 //
 // One CTA walks its run's blocks of 128 keys with two row tiles of 128 (rows ordered by head, so
 // they lie in a row in memory): rows r0 .. and r0 + 128 .. of the same head, or, for heads of at
@@ -51,6 +52,12 @@ struct Config {
   using T8 = Tile<kRows, D / 2>;        // 128 rows of D bytes, as D / 2 16-bit columns
   using TV = Tile<kBlockKeys, D>;       // fp16
   static constexpr int kTerms = kBf16 ? 2 : 3;
+  // P as a pair of fp16 values (two products): for fp16 outputs the rounding of one would equal
+  // their own (relative error of 48 rows against 16 x 8191 keys 2.9e-4 beside the 2.1e-4 of float32
+  // P, which the pair has too).  It costs 246 to 345 us on 2048 rows of 32768 keys, 8 heads, and 88 to
+  // 117 on those 48; for bf16 outputs, whose error it would change from 1.67e-3 to 1.66e-3, 229 to 328
+  // and 83 to 113.
+  static constexpr bool kPair = !kBf16;
   static constexpr int kSK = 2, kSV = 2;  // stages of K tiles and of V tiles
   static constexpr int kSR = kBf16 ? 3 : 2;  // of raw V blocks
   static constexpr int kRaw = kBlockKeys * D;
@@ -219,7 +226,9 @@ __device__ __forceinline__ float block_max(const float (&sv)[kBlockKeys], const 
 
 // P of the row under m into TMEM at tS (over the scores), two 16-bit values a word; returns the
 // row's sum of 2^kLift P / vs.
-template <int kG>
+// kPair: what the fp16 values leave, as fp16 too, goes behind them (kLowP columns on).
+constexpr int kLowP = kBlockKeys / 2;
+template <int kG, bool kPair>
 __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], const Scales& sc, float mul, float m,
                                              uint32_t tS) {
   constexpr int kW = kBlockKeys / kG;
@@ -227,7 +236,7 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
   float2 sum[2];
 #pragma unroll
   for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
-    uint32_t pk[16];
+    uint32_t pk[16], low[kPair ? 16 : 1];
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
       const int key = c0 + k, g = key / kW;
@@ -237,19 +246,26 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
       const float2 pr = make_float2(ex2(x.x), ex2(x.y));
       sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pr);
       pk[k / 2] = pack2<false>(pr.x, pr.y);
+      if constexpr (kPair) {
+        const float2 hi = unpack16<false>(pk[k / 2]);
+        low[k / 2] = pack2<false>(pr.x - hi.x, pr.y - hi.y);
+      }
       if ((key + 2) % kW == 0) {
         const float2 s = add2(sum[0], sum[1]);
         l = fmaf(s.x + s.y, sc.inv_v[g], l);
       }
     }
     tmem_st16(tS + c0 / 2, pk);
+    if constexpr (kPair) tmem_st16(tS + kLowP + c0 / 2, low);
   }
   return l;
 }
 
 // The same for rows past kExactShift: x is rounded before m is taken from it, as the maximum was.
 // The scores are read from tensor memory again, in a rolled loop, so that the common path pays for
-// this neither registers nor instruction fetches.  `seen`: keys of the block that the row sees.
+// this neither registers nor instruction fetches.  `seen`: keys of the block that the row sees.  At such
+// scores P is uncertain by far more than a step of fp16, and its second value is 0.
+template <bool kPair>
 __device__ __forceinline__ float far_probs(const Scales& sc, float mul, float m, int seen, uint32_t tS) {
   float l = 0.0f;
 #pragma unroll 1
@@ -271,6 +287,11 @@ __device__ __forceinline__ float far_probs(const Scales& sc, float mul, float m,
       pk[k / 2] = pack2<false>(pr[0], pr[1]);
     }
     tmem_st16(tS + c0 / 2, pk);
+  }
+  if constexpr (kPair) {
+    const uint32_t zeros[16] = {};
+#pragma unroll 1
+    for (int c0 = 0; c0 < kBlockKeys / 2; c0 += 16) tmem_st16(tS + kLowP + c0, zeros);
   }
   return l;
 }
@@ -443,6 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kBlockKeys / 16; ++kk)
                 mma_ts(tO, tS + kk * 8, dv + TV::mn_step(kk), id_o, (started || kk > 0) ? 1u : 0u);
+              if constexpr (C::kPair) {
+#pragma unroll
+                for (int kk = 0; kk < kBlockKeys / 16; ++kk)
+                  mma_ts(tO, tS + kLowP + kk * 8, dv + TV::mn_step(kk), id_o, 1u);
+              }
             }
             __syncwarp();
             started = true;
@@ -705,9 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           turn_phase ^= 1u;
         }
         if (__builtin_expect(far, 0))
-          l += far_probs(sc, mul, m, lim - key0, tS);
+          l += far_probs<C::kPair>(sc, mul, m, lim - key0, tS);
         else
-          l += uniform ? block_probs<1>(sv, sc, mul, m, tS) : block_probs<kGroups>(sv, sc, mul, m, tS);
+          l += uniform ? block_probs<1, C::kPair>(sv, sc, mul, m, tS)
+                       : block_probs<kGroups, C::kPair>(sv, sc, mul, m, tS);
         __syncwarp();
         if (lane == 0 && i + t < both) mbar_arrive(&sh.turn[t ^ 1]);
         tmem_wait_st();

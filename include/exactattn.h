@@ -283,8 +283,8 @@ int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int b
  * key below lengths[b] (ATTN_MASK_BITMAP is refused).  A padding row (i >= counts[b]) gets
  * O = 0, LSE = -inf; so does a row that sees no key, which also raises ATTN_WARN_EMPTY_ROW.
  * The codes are read exactly and the queries keep their bits; probabilities enter the product
- * with V as fp16 values (half a step 2^-11), as pairs of them for ATTN_F16 and at most 16 rows
- * H / H_kv * n_q a key/value head (d = 64: 32); sums are float32.
+ * with V as fp16 values for ATTN_BF16 (half a step 2^-11, an eighth of the output's) and as pairs
+ * of them for ATTN_F16 (2^-22); sums are float32.
  *   workspace  device buffer of at least attn_fwd_kv8_workspace_bytes(...) bytes, 16-byte
  *              aligned; its contents on entry do not matter.  Calls that may overlap on the GPU
  *              need workspaces of their own.

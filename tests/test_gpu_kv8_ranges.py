@@ -104,6 +104,35 @@ def test_scores_far_past_the_step_of_float32(dtype, d, G, n, size):
     assert status() == ea.ATTN_OK
 
 
+# ------------------------------------------------------------------ probabilities
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", [(1, 1), (12, 1), (4, 6), (2, 40), (4, 75)])
+def test_fp16_outputs_keep_more_of_p_than_half_a_step(d, G, n):
+    """Two scores whose products with V all but cancel: P of 64 and of 38.421875, which lies in the
+    middle between two fp16 values.  One fp16 value for P would leave 5 / 64 of 384; as a pair, half a
+    step of P is 2^-22, beside float32 roundings of the score (values below 1) and the sums."""
+    m = 96
+    r = 38.421875 / 64
+    ca = Cache(np.random.default_rng(1), [m], 1, 128, d, 16, spread=0)
+    low = np.arange(m) % 8 < 5
+    ca.c["k8"][0, 0, :m] = 0.0
+    ca.c["k8"][0, 0, :m, 3] = np.where(low, -1.0, 0.0)
+    ca.c["v8"][0, 0, :m] = np.where(low, -1.0, 1.0)[:, None]
+    for x in ("ks", "vs"):
+        ca.c[x][0, 0, :-(-m // 16)] = 1.0
+    ca.load()
+    q = torch.zeros(1, G, n, d, dtype=torch.float16)
+    q[..., 3] = 1.0
+    c = float(np.float32(-np.log(r)))
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, c)
+    p = np.exp(-c)
+    want = (3 - 5 * p) / (3 + 5 * p)
+    assert np.abs(o.double().cpu().numpy() - want).max() <= 2.0 ** -11 * abs(want) + 2.0 ** -24 + 2.0 ** -18
+    assert np.abs(lse.double().cpu().numpy() - np.log(m / 8 * (3 + 5 * p))).max() <= 2.0 ** -18
+    status()
+
+
 # ------------------------------------------------------------------ value scales
 
 FEW_AND_MANY = [(4, 1), (4, 4), (8, 6), (4, 70)]
