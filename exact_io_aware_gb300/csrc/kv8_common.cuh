@@ -97,6 +97,23 @@ __device__ __forceinline__ void codes_to_float4(uint32_t w, float (&x)[4]) {
   x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
 }
 
+// The same in E5M2: four floats to a word of codes, and back.
+__device__ __forceinline__ uint32_t pack4_e5m2(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ void e5m2_to_float4(uint32_t w, float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w >> (16 * i))));
+    const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&r));
+    x[2 * i] = u.x, x[2 * i + 1] = u.y;
+  }
+}
+
 // Exponent of the least power of two s with amax <= 448 s, within [-100, 120].  448 = 1.75 2^8,
 // so for amax = m 2^e (1 <= m < 2) it is e - 8, one more when m > 1.75.
 __device__ __forceinline__ int scale_exp(float amax) {

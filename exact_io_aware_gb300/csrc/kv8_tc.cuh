@@ -3,12 +3,14 @@
 // The mathematics is that of kv8_attend.cu: in base 2, x_rj = log2(e) s_rj + log2(vs_j),
 // P_rj = 2^{x_rj - m_r} rounded to fp16, z = P V on the codes, l = sum P / vs.
 //   * S = Q K^T is kind::f8f6f4 on the codes as they lie in memory.  A query row over a power of
-//     two (its largest value 224 .. 448) is a sum of E4M3 terms, q = q1 + q2 (+ q3): each term
-//     takes four significant bits and leaves a remainder of at most half a step, so two terms
-//     hold the 8 bits of a bf16 value and three the 11 of an fp16 one, exactly for values down
-//     to 2^-10 (fp16: 2^-7) of the row's largest; below, what is lost is under 2^-18 of the
-//     largest.  The terms' products add up in one float32 accumulator, and two of them cost what
-//     one product on 16-bit operands would.
+//     two (its largest value 224 .. 448) is a sum of 8-bit terms, q = q1 + q2 (+ q3), whose products
+//     add up in one float32 accumulator; two of them cost what one product on 16-bit operands would.
+//     q1 is E4M3 and leaves at most half of its step, 8 units of a bf16 value's last place or 64 of an
+//     fp16 one's; the others are E5M2, whose three bits hold every whole number up to 8, and all but 4
+//     of 64.  So two terms hold a bf16 value and three an fp16 one exactly, down to 2^-6, which is at
+//     most 2^-13 of the largest.  Below, where q1 steps by 2^-9, E5M2's range is what counts: two
+//     terms lose at most 2^-14, three 2^-17 (2^-21 and 2^-24 of the largest; E4M3 terms would lose up
+//     to 2^-10 however many there were).
 //   * P V is kind::f16: V's codes are widened to fp16 on the way into shared memory (exact); for fp16
 //     outputs P is a pair of values (Config::kPair).
 //
@@ -297,7 +299,7 @@ __device__ __forceinline__ float far_probs(const Scales& sc, float mul, float m,
 }
 
 // The queries of a tile (rows of q from `q` on, `rows` of them; the tile's others are zeros) as
-// E4M3 terms, by kN threads (tid): D / 16 lanes a row.  Row r's terms go to the tiles of row tile
+// 8-bit terms (the first E4M3, the others E5M2), by kN threads (tid): D / 16 lanes a row.  Row r's terms go to the tiles of row tile
 // r / 128 and its factor, c2 times the power of two taken out, to row_mul[r].  The loop stays
 // rolled: unrolled, fetching its instructions once a tile took longer than running them.
 template <bool kBf16, int D, int kN>
@@ -335,9 +337,14 @@ __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, cons
       uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[i] = pack4_e4m3(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         float y[4];
-        codes_to_float4(c[i], y);
+        if (term == 0) {
+          c[i] = pack4_e4m3(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          codes_to_float4(c[i], y);
+        } else {
+          c[i] = pack4_e5m2(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          e5m2_to_float4(c[i], y);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[4 * i + k] -= y[k];  // exact
       }
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 2) {
       // ------------------------------------------------------------ MMA issuer of row tile t
       const int t = warp;
-      constexpr uint32_t id_s = idesc_e4m3(128, kBlockKeys);
+      constexpr uint32_t id_s = idesc_e4m3(128, kBlockKeys), id_rest = idesc_e4m3(128, kBlockKeys, true);
       constexpr uint32_t id_o = idesc_f16(128, D, 0, 0, 1);
       const uint64_t dq = T8::desc_k(smem_u32(sQ + (split ? 0 : t) * C::kTerms * T8::kBytes), 0);
       const uint64_t dk0 = T8::desc_k(smem_u32(sK), 0);
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
                   mma_ss_f8(tS, dq + term * static_cast<uint64_t>(T8::kBytes >> 4) + T8::k_step(kk),
-                            dk + T8::k_step(kk), id_s, (term > 0 || kk > 0) ? 1u : 0u);
+                            dk + T8::k_step(kk), term > 0 ? id_rest : id_s, (term > 0 || kk > 0) ? 1u : 0u);
               mma_commit(&sh.s_full[t]);
             }
             __syncwarp();

@@ -2,7 +2,7 @@
 // cores (the mathematics: kv8_weights.cu).
 //
 // S^T = K Q^T with keys as the 128 rows of the accumulator: the A operand is a tile of codes as TMA
-// brings it, the B operands are the queries' E4M3 terms (kv8_tc.cuh), so one thread holds all of a
+// brings it, the B operands are the queries' 8-bit terms (kv8_tc.cuh), so one thread holds all of a
 // key's scores and sums its weight without a word to another.  The codes are read once for up to
 // 256 rows; more rows pass in groups of 256.
 //
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = min(kMostRows, geo.R - r0), tiles = rows > kRows ? 2 : 1;
       if (warp == 0) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t id_s = idesc_e4m3(128, kRows);
+        constexpr uint32_t id_s = idesc_e4m3(128, kRows), id_rest = idesc_e4m3(128, kRows, false, true);
         const uint64_t dq = T8::desc_k(smem_u32(sQ), 0), dk0 = T8::desc_k(smem_u32(sK), 0);
         ok = mbar_wait_warp(&sh.q_full, part & 1, p.status, 0x32);
         for (int j = j0; j < j1 && ok; ++j) {
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mma_ss_f8(tmem + 128 * w,
                             dk0 + s * static_cast<uint64_t>(T8::kBytes >> 4) + T8::k_step(kk),
                             dq + (rt * C::kTerms + term) * static_cast<uint64_t>(T8::kBytes >> 4) + T8::k_step(kk),
-                            id_s, (term > 0 || kk > 0) ? 1u : 0u);
+                            term > 0 ? id_rest : id_s, (term > 0 || kk > 0) ? 1u : 0u);
               mma_commit(&sh.s_full[w]);
               if (rt + 1 == tiles) {
                 mma_commit(&sh.k_empty[s]);

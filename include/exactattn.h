@@ -282,7 +282,8 @@ int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int b
  * ATTN_MASK_CAUSAL row i sees keys j <= lengths[b] - counts[b] + i, under ATTN_MASK_NONE every
  * key below lengths[b] (ATTN_MASK_BITMAP is refused).  A padding row (i >= counts[b]) gets
  * O = 0, LSE = -inf; so does a row that sees no key, which also raises ATTN_WARN_EMPTY_ROW.
- * The codes are read exactly and the queries keep their bits; probabilities enter the product
+ * The codes are read exactly, and so are a query row's values down to 2^-13 of its largest; a
+ * smaller one may lose 2^-21 of the largest (ATTN_F16: 2^-24).  Probabilities enter the product
  * with V as fp16 values for ATTN_BF16 (half a step 2^-11, an eighth of the output's) and as pairs
  * of them for ATTN_F16 (2^-22); sums are float32.
  *   workspace  device buffer of at least attn_fwd_kv8_workspace_bytes(...) bytes, 16-byte

@@ -104,6 +104,43 @@ def test_scores_far_past_the_step_of_float32(dtype, d, G, n, size):
     assert status() == ea.ATTN_OK
 
 
+# ------------------------------------------------------------------ small values of a row
+
+@pytest.mark.parametrize("dtype,lost", [("bf16", 2.0 ** -21), ("f16", 2.0 ** -24)])
+@pytest.mark.parametrize("d,G,n", [(64, 8, 6), (128, 8, 6), (128, 4, 40), (64, 4, 1)])
+@pytest.mark.parametrize("kind", ["ties", "random"])
+def test_small_values_beside_a_large_one_in_a_row(dtype, lost, d, G, n, kind):
+    """One value of each row 2^16 times the others, in a column where every key is zero: the others
+    alone make the scores.  What a row's terms may lose of a value is `lost` of its largest, so a
+    score is off by lost max|q| c sum_r |k_r| beside the usual bound."""
+    rng = np.random.default_rng(d + n)
+    m, c = 250, 0.1
+    ca = Cache(rng, [m], 2, 256, d, 32)
+    k = ca.c["k8"]
+    if kind == "ties":  # one sign a key, so that what values lose adds up
+        k[0, :, :m] = np.abs(k[0, :, :m]) * rng.choice([-1.0, 1.0], size=(2, m, 1))
+    k[0, :, :m, 0] = 0.0
+    ca.c["ks"][:, :, :8] = 2.0 ** -9
+    ca.load()
+    x = np.full((1, 2 * G, n, d), 0.3125) if kind == "ties" else rng.normal(size=(1, 2 * G, n, d)) / 4
+    x[..., 0] = 2.0 ** 14
+    q = rounded(x, dtype)
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, c)
+    O, L, tol, ltol = attend_bounds(ca, q, c, dtype, None, False)
+    A = kv8.attend(ca.c, q.double().numpy(), c)[2]
+    off = lost * 2.0 ** 14 * c * np.abs(k[0, :, :m]).sum(-1).max() * 2.0 ** -9
+    assert off < 0.05
+    # P is off by e^off - 1 <= 1.1 off, numerator and denominator.
+    assert (np.abs(o.double().cpu().numpy() - O) <= tol + 2.2 * off * A).all()
+    assert (np.abs(lse.double().cpu().numpy() - L) <= ltol + off).all()
+    ref = kv8.add_weights(ca.c, q.double().numpy(), c, lse.double().cpu().numpy()) - ca.c["w"]
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, lse, None, c).double().cpu().numpy()
+    S = kv8.attend(ca.c, q.double().numpy(), c)[3]
+    rel = (d + 16) * 2.0 ** -23 * (S.max() + 32.0) + 2.0 ** -21 + G * n * 2.0 ** -24
+    assert (np.abs(w - ref)[..., :m] <= (rel + 1.1 * off) * ref[..., :m]).all()
+    status()
+
+
 # ------------------------------------------------------------------ probabilities
 
 @pytest.mark.parametrize("d", [64, 128])
