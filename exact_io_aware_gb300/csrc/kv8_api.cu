@@ -53,6 +53,9 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return a < b + m && b < a + n;
 }
 
+// The largest sizes: heads of a grid's y axis, tokens of a sequence, rows of a key/value head.
+constexpr int64_t kMostHeads = 65535, kMostCap = int64_t(1) << 30, kMostRows = int64_t(1) << 24;
+
 int check_cache(int B, int Hk, int d, int cap, int block, std::initializer_list<const void*> codes,
                 std::initializer_list<const void*> words) {
   if (B < 1 || Hk < 1 || cap < 1) return fail(ATTN_ERR_INVALID_ARG, "B, H_kv and cap must be positive");
@@ -60,8 +63,8 @@ int check_cache(int B, int Hk, int d, int cap, int block, std::initializer_list<
   if (block != 16 && block != 32 && block != 64 && block != 128)
     return fail(ATTN_ERR_UNSUPPORTED, "block must be 16, 32, 64 or 128");
   if (cap % block != 0) return fail(ATTN_ERR_INVALID_ARG, "cap must be a multiple of block");
-  if (cap > (1 << 30)) return fail(ATTN_ERR_UNSUPPORTED, "cap must be at most 2^30");
-  if (static_cast<int64_t>(B) * Hk > 65535)
+  if (cap > kMostCap) return fail(ATTN_ERR_UNSUPPORTED, "cap must be at most 2^30");
+  if (static_cast<int64_t>(B) * Hk > kMostHeads)
     return fail(ATTN_ERR_UNSUPPORTED, "B * H_kv must be at most 65535");
   for (const void* p : codes) {
     if (!p) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
@@ -85,7 +88,7 @@ int check_dtype(int dtype) {
 int check_query(int H, int Hk, int n_q, int mask_kind, const int32_t* counts) {
   if (n_q < 1 || H < 1) return fail(ATTN_ERR_INVALID_ARG, "H and n_q must be positive");
   if (H % Hk != 0) return fail(ATTN_ERR_INVALID_ARG, "H must be a multiple of H_kv");
-  if (static_cast<int64_t>(H / Hk) * n_q > (1 << 24))
+  if (static_cast<int64_t>(H / Hk) * n_q > kMostRows)
     return fail(ATTN_ERR_UNSUPPORTED, "H / H_kv * n_q must be at most 2^24");
   if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_BITMAP)
     return fail(ATTN_ERR_INVALID_ARG, "unknown mask kind");
@@ -145,7 +148,8 @@ int attn_kv8_append(int dtype, int B, int H_kv, int n_new, int d, int cap, int b
 
 size_t attn_fwd_kv8_workspace_bytes(int dtype, int B, int H, int H_kv, int n_q, int d, int cap) {
   if (dtype < ATTN_F16 || dtype > ATTN_BF16 || B < 1 || H < 1 || H_kv < 1 || n_q < 1 || cap < 1 ||
-      H % H_kv != 0 || (d != 64 && d != 128))
+      H % H_kv != 0 || (d != 64 && d != 128) || cap % 16 != 0 || cap > kMostCap ||
+      static_cast<int64_t>(B) * H_kv > kMostHeads || static_cast<int64_t>(H / H_kv) * n_q > kMostRows)
     return 0;
   return ea::kv8_attend_workspace_bytes(B, H_kv, H / H_kv, n_q, d, cap, ea::device_sm_count());
 }

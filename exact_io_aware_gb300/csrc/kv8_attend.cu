@@ -416,6 +416,8 @@ cudaError_t launch_attend_nt(const AttendParams<ByQuery>& p, int sms, cudaStream
 
 }  // namespace kv8
 
+namespace {
+
 // Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  16
 // sequences x 8 heads of 8187 keys, bf16, us here and there: d = 128, 16 rows 54 and 87, 24 rows
 // 123 and 88 (32-row tiles spill registers); d = 64, 32 rows 52 and 73, 48 rows 83 and 74.
@@ -433,11 +435,18 @@ size_t part_rows(int64_t R, int d, int sms) {
   return static_cast<size_t>(2) * sms * kv8::kMostCtas * rows_per_tile(R, d);
 }
 
+bool too_long(int B, int Hk, int tiles, int64_t R, int d, int cap) {
+  return kv8::list_too_long(B, Hk, tiles, cap, R > few_rows(d) ? kv8::kBlockKeys : kv8::kChunk);
+}
+
+}  // namespace
+
 size_t kv8_attend_workspace_bytes(int B, int Hk, int G, int n, int d, int cap, int sms) {
   const int64_t R = static_cast<int64_t>(G) * n;
   if (R <= few_rows(d) && cap <= kv8::kAlignedCap) return 0;  // nothing to join
-  const size_t tiles = static_cast<size_t>(B) * Hk * ((R + rows_per_tile(R, d) - 1) / rows_per_tile(R, d));
-  return part_rows(R, d, sms) * (d + 2) * sizeof(float) + tiles * sizeof(int2);
+  const int tiles = static_cast<int>((R + rows_per_tile(R, d) - 1) / rows_per_tile(R, d));
+  if (too_long(B, Hk, tiles, R, d, cap)) return 0;  // refused
+  return part_rows(R, d, sms) * (d + 2) * sizeof(float) + static_cast<size_t>(B) * Hk * tiles * sizeof(int2);
 }
 
 namespace {
@@ -471,7 +480,7 @@ kv8::AttendParams<Geo> attend_params(const Kv8Args& a, int ctas, int min_chunks)
 int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err) {
   const int64_t R = static_cast<int64_t>(a.G) * a.n;
   const int tiles = static_cast<int>((R + rows_per_tile(R, a.d) - 1) / rows_per_tile(R, a.d));
-  if (kv8::list_too_long(a.B, a.Hk, tiles, a.cap, R > few_rows(a.d) ? kv8::kBlockKeys : kv8::kChunk)) {
+  if (too_long(a.B, a.Hk, tiles, R, a.d, a.cap)) {
     err = "B * H * n_q * cap is too large for one call";
     return -2;
   }
