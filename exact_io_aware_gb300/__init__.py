@@ -437,6 +437,8 @@ class _On:
     __slots__ = ("index", "stream", "was")
 
     def __init__(self, index, stream):
+        if stream is not None and stream.device_index != index:
+            raise ValueError(f"the stream must be one of CUDA device {index}, where the tensors are")
         self.index, self.stream, self.was = index, stream, None
 
     def __enter__(self):
