@@ -418,6 +418,8 @@ def _kv8_shape(k8, k_scales):
         raise ValueError("codes must be [B,H_kv,cap,d] and scales [B,H_kv,cap/block]")
     B, Hk, cap, d = shape
     nblk = k_scales.shape[2]
+    if Hk < 1 or cap < 1:
+        raise ValueError("the 8-bit cache needs at least one head and one token of capacity")
     if nblk < 1 or cap % nblk:
         raise ValueError("scales must be [B,H_kv,cap/block]")
     return B, Hk, cap, d, cap // nblk, device

@@ -65,3 +65,13 @@ def test_a_stream_of_another_device_is_refused(op):
         calls(cache(), stream=StreamOf(1))[op]()
     with pytest.raises(AssertionError, match="reached CUDA"):  # its own device's is taken
         calls(cache(), stream=StreamOf(0))[op]()
+
+
+@pytest.mark.parametrize("op", ["append", "attend", "weights", "evict"])
+@pytest.mark.parametrize("sizes", [dict(Hk=0), dict(cap=0)])
+def test_a_cache_of_no_heads_or_no_room_is_refused(op, sizes):
+    c = cache(**sizes)
+    if "cap" in sizes:
+        c["ks"] = c["vs"] = OnGpu((1, 2, 1), torch.float32)
+    with pytest.raises(ValueError):
+        calls(c)[op]()
