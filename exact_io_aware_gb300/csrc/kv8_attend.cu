@@ -60,7 +60,7 @@ constexpr size_t merge_bytes() {
 
 // One chunk of 32 keys against the tile's rows.  kPair: P as a pair of fp16 values.
 template <int D, int NT, bool kPair>
-__device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool masked, int block,
+__device__ __forceinline__ void attend_chunk(const uint8_t* st, int key0, bool masked,
                                              const float (&kmul)[NT][2], const QFrag<D> (&q)[NT],
                                              const int (&lim)[NT][2], float (&z)[NT][D / 16][4],
                                              float (&l)[NT][2], float (&m)[NT][2], float& hi) {
@@ -234,15 +234,14 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
     pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
     if (u0 >= u1) return;
   } else {
-    const int tile = blockIdx.x;
-    pl.rt = tile % geo.tiles;
-    pl.hk = tile / geo.tiles % geo.Hk;
-    pl.b = tile / geo.tiles / geo.Hk;
+    pl.rt = 0;
+    pl.hk = blockIdx.x % geo.Hk;
+    pl.b = blockIdx.x / geo.Hk;
     pl.start = u0 = 0;
     const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
-    pl.keys = tile_keys(geo, len, cnt, pl.rt);
+    pl.keys = tile_keys(geo, len, cnt, 0);
     u1 = chunks_of(geo, pl.keys);
-    if (pl.rt == 0 && pl.hk == 0 && threadIdx.x == 0)
+    if (pl.hk == 0 && threadIdx.x == 0)
       check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
   }
   for (;;) {
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       {
-        const int r = pl.rt * kTile + j * 8 + g;
+        const int r = j * 8 + g;
         const bool real = r < geo.R && geo.query(r) < cnt;  // what padding rows hold does not matter
         float x[D / 4];
         load_q_row<kBf16, D>(real ? p.q + geo.row_offset(pl.b, pl.hk, r) * D : nullptr, x);
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int r = pl.rt * kTile + j * 8 + 2 * t + c;
+        const int r = j * 8 + 2 * t + c;
         const bool real = r < geo.R && geo.query(r) < cnt;
         lim[j][c] = real ? query_keys(geo, len, cnt, geo.query(r)) : len;
         least = min(least, lim[j][c]);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
       issue(ch + (kStages - 1) * kAttendWarps, ahead);
       const int key0 = ch * kChunk;
       const bool masked = key0 + kChunk > least;
-      attend_chunk<D, NT, !kBf16>(ring + stage * stage_bytes<D>(), key0, masked, p.block, kmul, q, lim, z, l, m, hi);
+      attend_chunk<D, NT, !kBf16>(ring + stage * stage_bytes<D>(), key0, masked, kmul, q, lim, z, l, m, hi);
       __syncwarp();
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -371,11 +370,10 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
         zs.w = fmaf(f, x.w, zs.w);
         ls = fmaf(mlm[(w * kTile + at) * 2] * half, half, ls);
       }
-      const int r = pl.rt * kTile + row;
       if (whole) {
-        if (r < geo.R)
-          write_out<kBf16, D, ByQuery>(p, geo.row_offset(pl.b, pl.hk, r), col, zs, ls, mx,
-                              geo.query(r) < cnt);
+        if (row < geo.R)
+          write_out<kBf16, D, ByQuery>(p, geo.row_offset(pl.b, pl.hk, row), col, zs, ls, mx,
+                              geo.query(row) < cnt);
       } else {
         *reinterpret_cast<float4*>(p.part_z + (slot + row) * D + col) = zs;
         if (col == 0) *reinterpret_cast<float2*>(p.part_lm + (slot + row) * 2) = make_float2(ls, mx);
@@ -396,7 +394,7 @@ cudaError_t launch_attend(AttendParams<ByQuery> p, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, allowed);
   if (e != cudaSuccess) return e;
-  const unsigned tiles = static_cast<unsigned>(p.geo.B) * p.geo.Hk * p.geo.tiles;
+  const unsigned tiles = static_cast<unsigned>(p.geo.B) * p.geo.Hk;
   const bool aligned = p.geo.cap <= kAlignedCap;
   p.ctas = aligned ? 0 : sms * attend_ctas_per_sm<NT>();
   void* args[] = {&p};

@@ -20,8 +20,8 @@ struct Geometry {
   bool all_keys;  // the work list covers every held key, not only those some row sees
 };
 
-// Rows ordered by query: row r is query i = r / G of head r % G, so a tile's queries are near one
-// another and a causal mask cuts it evenly.
+// Rows ordered by query: row r is query i = r / G of head r % G.  For few rows: one tile holds all of
+// a head's.
 struct ByQuery : Geometry {
   static constexpr int kStep = kChunk;
   __device__ __forceinline__ int query(int r) const { return r / G; }
@@ -29,11 +29,11 @@ struct ByQuery : Geometry {
   __device__ __forceinline__ int64_t row_offset(int b, int hk, int r) const {
     return (static_cast<int64_t>(b) * Hk * G + static_cast<int64_t>(hk) * G + r % G) * n + r / G;
   }
-  // Least and greatest query of rows r0 .. r1 - 1 that is below cnt; false if there is none.
-  __device__ __forceinline__ bool span(int r0, int r1, int cnt, int& lo, int& hi) const {
-    lo = r0 / G;
-    hi = min((r1 - 1) / G, cnt - 1);
-    return lo < cnt;
+  // Least and greatest query of the tile's rows that is below cnt; false if there is none.
+  __device__ __forceinline__ bool span(int, int, int cnt, int& lo, int& hi) const {
+    lo = 0;
+    hi = cnt - 1;
+    return cnt > 0;
   }
 };
 
@@ -44,6 +44,7 @@ struct ByHead : Geometry {
   __device__ __forceinline__ int64_t row_offset(int b, int hk, int r) const {
     return (static_cast<int64_t>(b) * Hk + hk) * R + r;
   }
+  // As above, for rows r0 .. r1 - 1.
   __device__ __forceinline__ bool span(int r0, int r1, int cnt, int& lo, int& hi) const {
     const int a = r0 % n, z = (r1 - 1) % n;
     const bool wraps = r1 - r0 >= n || a > z;  // past a head's last query to the next's first
