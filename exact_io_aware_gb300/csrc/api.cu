@@ -1,7 +1,6 @@
 // C ABI of the exact tiled attention library: argument checks, dispatch to the kernels,
 // error reporting and the device status word.  See include/exactattn.h for the contract.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <atomic>
@@ -11,11 +10,15 @@
 #include <mutex>
 #include <string>
 
+#include "entry.h"
 #include "exactattn.h"
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace {
+
+using ea::CallRange;
+using ea::fail;
 
 thread_local std::string g_last_error;
 
@@ -37,20 +40,6 @@ struct DeviceInfo {
   int sms = 0;
 };
 DeviceInfo g_dev[kMaxDevices];
-
-int fail(int code, const std::string& msg) {
-  g_last_error = msg;
-  return code;
-}
-
-// An NVTX range named after the entry point, open for the length of the host call (the range
-// marks the call's argument checks and launches in a timeline; the kernels are asynchronous).
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
 
 int status_ptr(uint32_t** out) {
   int dev = 0;

@@ -1,30 +1,20 @@
 // C entry points of the 8-bit key/value cache: argument checks and dispatch.
 // See include/exactattn.h for the contract.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <cstdint>
 #include <exception>
 #include <initializer_list>
 #include <string>
 
+#include "entry.h"
 #include "exactattn.h"
-#include "kernels.h"
 #include "kv8.h"
 
 namespace {
 
-int fail(int code, const std::string& msg) {
-  ea::set_last_error(msg);
-  return code;
-}
-
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
+using ea::CallRange;
+using ea::fail;
 
 // Runs an entry point's body; a C++ exception (memory for a message, a mutex) becomes a code.
 template <typename F>
