@@ -33,7 +33,9 @@ namespace kv8 {
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = kAttendWarps * 32;
 // A cache of at most this many tokens a sequence is not cut: each tile is one CTA's, and there is
-// nothing to join.
+// nothing to join.  us uncut and cut, at d = 64, G = 1 and d = 128, G = 8: 8 heads of 512 tokens 5.8, 7.4
+// and 8.1, 8.8, of 1024 8.2, 7.9 and 11.6, 8.9; 256 heads of 512 tokens 6.9, 11.6 and 10.4, 15.9 (of 1024
+// still 10.6, 14.9 and 16.4, 20.8: with many heads longer tiles fill the device, with few they do not).
 constexpr int kAlignedCap = 512;
 constexpr int kMostCtas = 3;  // of any variant, on a multiprocessor
 
@@ -416,9 +418,12 @@ cudaError_t launch_attend_nt(const AttendParams<ByQuery>& p, int sms, cudaStream
 
 namespace {
 
-// Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  16
-// sequences x 8 heads of 8187 keys, bf16, us here and there: d = 128, 16 rows 54 and 87, 24 rows
-// 123 and 88 (32-row tiles spill registers); d = 64, 32 rows 52 and 73, 48 rows 83 and 74.
+// Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  us here
+// and there, for 16 sequences and for one, each 8 heads of 8187 keys:
+//   d = 128  bf16  16 rows 57, 92 and 18, 24    fp16  16 rows 64, 140 and 19, 29
+//            bf16  24 rows 123, 88 (32-row tiles of this kernel spill registers)
+//   d = 64   bf16  32 rows 61, 80 and 21, 22    fp16  32 rows 71, 111 and 22, 24
+//            bf16  48 rows 83, 74
 constexpr int few_rows(int d) { return d == 64 ? 32 : 16; }
 
 int rows_per_tile(int64_t R, int d) {
