@@ -114,12 +114,12 @@ __device__ __forceinline__ void e5m2_to_float4(uint32_t w, float (&x)[4]) {
   }
 }
 
-// Exponent of the least power of two s with amax <= 448 s, within [-100, 120].  448 = 1.75 2^8,
+// Exponent of the least power of two s with amax <= 448 s, within [least, 120].  448 = 1.75 2^8,
 // so for amax = m 2^e (1 <= m < 2) it is e - 8, one more when m > 1.75.
-__device__ __forceinline__ int scale_exp(float amax) {
+__device__ __forceinline__ int scale_exp(float amax, int least = -100) {
   const uint32_t u = __float_as_uint(amax);
   const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return min(max(e, -100), 120);
+  return min(max(e, least), 120);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 

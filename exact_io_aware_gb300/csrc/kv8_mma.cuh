@@ -118,10 +118,11 @@ __device__ __forceinline__ void load_q_row(const uint16_t* row, float (&x)[D / 4
 
 // Exponent that brings a row's largest finite |q| to 2^14 .. 2^15: queries enter the products as
 // fp16 times a power of two of their own, so bf16 rows keep their range whatever the other rows
-// hold, and values down to 2^-31 of the row's largest keep all of their bits.
+// hold, and values down to 2^-31 of the row's largest keep all of their bits.  (At most 2^126, so
+// that the power and the inverse are normal values: rows below 2^-112 come to less than 2^14.)
 __device__ __forceinline__ int q_exp(float amax) {
   const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-  return min(max(14 - e, -100), 100);
+  return min(14 - e, 126);
 }
 
 // The lane's share `x` of its row (lane / 4 of eight) as a fragment, and in kmul the factors of the

@@ -327,7 +327,7 @@ __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, cons
     }
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const int e = scale_exp(amax);
+    const int e = scale_exp(amax, -126);
     const float mul = c2 < 0.0f ? -pow2(-e) : pow2(-e);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = nan_unless_finite(x[i]) * mul;

@@ -72,6 +72,28 @@ def test_each_row_keeps_its_bits_beside_much_larger_rows(d, G, n):
     status()
 
 
+# ------------------------------------------------------------------ rows at the ends of the type
+
+@pytest.mark.parametrize("d,G,n", [(128, 4, 1), (64, 8, 4), (128, 8, 6), (64, 4, 70)])
+@pytest.mark.parametrize("exp", [124, 110, -100, -116])
+def test_queries_at_the_ends_of_bf16(d, G, n, exp):
+    """Rows of size 2^124 to 2^-116 under a c that makes their scores of size one."""
+    rng = np.random.default_rng(d + n)
+    m = 300
+    ca = Cache(rng, [m], 1, 384, d, 32)
+    q = rounded(np.clip(rng.normal(size=(1, G, n, d)), -4, 4) * 2.0 ** exp, "bf16")
+    c = d ** -0.5 * 2.0 ** -exp
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, c)
+    check_attend(ca, q, c, "bf16", o, lse)
+    _, L, _, S, _ = kv8.attend(ca.c, q.double().numpy(), c)
+    given = torch.from_numpy(L).float()
+    ref = kv8.add_weights(ca.c, q.double().numpy(), c, given.double().numpy()) - ca.c["w"]
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, given.cuda(), None, c).double().cpu().numpy()
+    rel = (d + 16) * 2.0 ** -23 * (S.max() + 32.0) + 2.0 ** -21 + G * n * 2.0 ** -24
+    assert (np.abs(w - ref)[..., :m] <= rel * ref[..., :m]).all()
+    assert status() == ea.ATTN_OK
+
+
 # ------------------------------------------------------------------ large scores
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
