@@ -299,9 +299,10 @@ __device__ __forceinline__ float far_probs(const Scales& sc, float mul, float m,
 }
 
 // The queries of a tile (rows of q from `q` on, `rows` of them; the tile's others are zeros) as
-// 8-bit terms (the first E4M3, the others E5M2), by kN threads (tid): D / 16 lanes a row.  Row r's terms go to the tiles of row tile
-// r / 128 and its factor, c2 times the power of two taken out, to row_mul[r].  The loop stays
-// rolled: unrolled, fetching its instructions once a tile took longer than running them.
+// 8-bit terms (the first E4M3, the others E5M2), by kN threads (tid): D / 16 lanes a row.  Row r's
+// terms go to the tiles of row tile r / 128 and its factor, c2 times the power of two taken out, to
+// row_mul[r].  The loop stays rolled: unrolled, fetching its instructions once a tile took longer than
+// running them.
 template <bool kBf16, int D, int kN>
 __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, const uint16_t* q, int rows,
                                             int tile, float c2, int tid) {
@@ -332,21 +333,26 @@ __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, cons
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = nan_unless_finite(x[i]) * mul;
     uint8_t* dst = terms + row / kRows * C::kTerms * T8::kBytes + T8::offset(row % kRows, 8 * piece);
+    uint32_t c[4];
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = pack4_e4m3(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      codes_to_float4(c[i], y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[4 * i + k] -= y[k];  // exact
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
 #pragma unroll 1
-    for (int term = 0; term < C::kTerms; ++term) {
-      uint32_t c[4];
+    for (int term = 1; term < C::kTerms; ++term) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float y[4];
-        if (term == 0) {
-          c[i] = pack4_e4m3(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          codes_to_float4(c[i], y);
-        } else {
-          c[i] = pack4_e5m2(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        c[i] = pack4_e5m2(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        if (C::kTerms > 2) {  // (the last term's is not looked at)
           e5m2_to_float4(c[i], y);
-        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[4 * i + k] -= y[k];  // exact
+          for (int k = 0; k < 4; ++k) x[4 * i + k] -= y[k];
+        }
       }
       *reinterpret_cast<uint4*>(dst + term * T8::kBytes) = make_uint4(c[0], c[1], c[2], c[3]);
     }
