@@ -263,39 +263,15 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
   return l;
 }
 
-// The same for rows past kExactShift: x is rounded before m is taken from it, as the maximum was.
-// The scores are read from tensor memory again, in a rolled loop, so that the common path pays for
-// this neither registers nor instruction fetches.  `seen`: keys of the block that the row sees.  At such
-// scores P is uncertain by far more than a step of fp16, and its second value is 0.
-template <bool kPair>
-__device__ __forceinline__ float far_probs(const Scales& sc, float mul, float m, int seen, uint32_t tS) {
-  float l = 0.0f;
-#pragma unroll 1
-  for (int c0 = 0; c0 < kBlockKeys; c0 += 32) {
-    uint32_t s[32], pk[16];
-    tmem_ld32(tS + c0, s);
-    tmem_wait_ld();
+// For a row past kExactShift: scores that give block_probs, under m = 0, what x - m is with x rounded
+// first, as the maximum was.
+__device__ __forceinline__ void shift_far(float (&sv)[kBlockKeys], const Scales& sc, float mul, float m) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      const int g = (c0 + k) / 16;
-      const float f = fmaxf(sc.k[g] * mul, kLeastFactor);
-      float pr[2];
+  for (int g = 0; g < kGroups; ++g) {
+    const float f = fmaxf(sc.k[g] * mul, kLeastFactor), lvs = sc.log2_v[g], back = 1.0f / f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = fmaf(__uint_as_float(s[k + e]), f, sc.log2_v[g]);
-        pr[e] = c0 + k + e < seen ? ex2(x - m) : 0.0f;
-        l = fmaf(pr[e], sc.inv_v[g], l);
-      }
-      pk[k / 2] = pack2<false>(pr[0], pr[1]);
-    }
-    tmem_st16(tS + c0 / 2, pk);
+    for (int k = 16 * g; k < 16 * g + 16; ++k) sv[k] = (fmaf(sv[k], f, lvs) - m - lvs) * back;
   }
-  if constexpr (kPair) {
-    const uint32_t zeros[16] = {};
-#pragma unroll 1
-    for (int c0 = 0; c0 < kBlockKeys / 2; c0 += 16) tmem_st16(tS + kLowP + c0, zeros);
-  }
-  return l;
 }
 
 // The queries of a tile (rows of q from `q` on, `rows` of them; the tile's others are zeros) as
@@ -690,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
-      bool first = true, far = false;  // far: a real row of the warp has |m| past kExactShift
+
       for (int i = i0; i < steps; i += stride) {
         const uint32_t c = gi + i;
         ok = mbar_wait_warp(&sh.sc_full[c & 3], (c >> 2) & 1, p.status, 0x2D) &&
@@ -698,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after();
-        if (first) mul = sh.row_mul[seg & 1][row - sg.r0];
+        if (i == i0) mul = sh.row_mul[seg & 1][row - sg.r0];
         const Scales& sc = sh.scales[c & 3];
         const int key0 = (j0 + i) * kBlockKeys;
         float sv[kBlockKeys];
@@ -725,10 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mn;
           l = l * half * half;
         }
-        if (__builtin_expect(__any_sync(0xFFFFFFFFu, alpha != 1.0f), 0)) {
-          far = __any_sync(0xFFFFFFFFu, real && fabsf(m) > kExactShift && m != kNoMax);
+        // Seldom both: in one branch, and far rows change their scores there, so that the common blocks
+        // pay little (a second way through the exponentials cost 2048 rows 7 us of 221, 48 rows 3 of 79).
+        const bool far = real && fabsf(m) > kExactShift && m != kNoMax;
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, alpha != 1.0f || far), 0)) {
 #pragma unroll 1
-          for (int c0 = first ? D : 0; c0 < D; c0 += 16) {
+          for (int c0 = i == i0 ? D : 0; c0 < D; c0 += 16) {  // no O yet at the first block
             uint32_t rr[16];
             tmem_ld16(tO + c0, rr);
             tmem_wait_ld();
@@ -736,18 +714,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 16; ++k) rr[k] = __float_as_uint(__uint_as_float(rr[k]) * alpha);
             tmem_st16(tO + c0, rr);
           }
+          if (far) shift_far(sv, sc, mul, m);
         }
-        first = false;
         if (i < both && (t == 1 || i > 0)) {
           ok = mbar_wait_warp(&sh.turn[t], turn_phase, p.status, 0x3A);
           if (!ok) break;
           turn_phase ^= 1u;
         }
-        if (__builtin_expect(far, 0))
-          l += far_probs<C::kPair>(sc, mul, m, lim - key0, tS);
-        else
-          l += uniform ? block_probs<1, C::kPair>(sv, sc, mul, m, tS)
-                       : block_probs<kGroups, C::kPair>(sv, sc, mul, m, tS);
+        const float from = far ? 0.0f : m;
+        l += uniform ? block_probs<1, C::kPair>(sv, sc, mul, from, tS)
+                     : block_probs<kGroups, C::kPair>(sv, sc, mul, from, tS);
         __syncwarp();
         if (lane == 0 && i + t < both) mbar_arrive(&sh.turn[t ^ 1]);
         tmem_wait_st();
