@@ -27,9 +27,10 @@
 //   3  converters: one thread a key, its V codes into an fp16 tile
 // S and P share TMEM columns; O stays in TMEM for the length of a tile.
 //
-// Measured (bf16, d = 128): 2048 rows against 32768 keys of 8 heads, causal, 223 us, 1.22 PFLOP/s, 64 %
+// Measured (d = 128): 2048 rows against 32768 keys of 8 heads, causal, bf16, 225 us, 1.21 PFLOP/s, 64 %
 // of the measured bf16 rate; bound by a block's chain of products and exponentials, the tensor pipe
-// active about half of the cycles.  48 rows against up to 8191 keys of 128 heads: 80 us.
+// active about half of the cycles.  48 rows against up to 8191 keys of 128 heads: 81 us.  fp16: 345
+// and 116 us.
 //
 // The registers of 512 threads are dealt again: softmax holds a row's 128 scores, the others
 // need few (kRegs*: their sum over the warpgroups is what the block was launched with).

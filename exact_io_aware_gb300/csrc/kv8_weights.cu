@@ -7,7 +7,7 @@
 // it and the tcgen05 kernel for many (kv8_weights_tc.cu).  Scores are formed as in kv8_attend.cu
 // (S^T = K Q^T, a warp to 32 keys), the queries stay in registers, and a key's weight is summed
 // over the rows of a lane and then over the four lanes that share the key.  Measured (d = 128, four
-// rows): 256 heads of 2000 to 8192 keys, 36.5 us, 4.8 TB/s, 72 % of the measured copy rate.
+// rows): 256 heads of 2000 to 8192 keys, 36.2 us, 4.9 TB/s, 73 % of the measured copy rate.
 #include "kv8_mma.cuh"
 #include "kv8_weights.cuh"
 
@@ -161,9 +161,10 @@ cudaError_t launch_weights_nt(const WeightsParams<ByQuery>& p, int sms, cudaStre
 
 namespace {
 
-// Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  16
-// sequences x 8 heads of 8187 keys, bf16, d = 128, us here and there: 16 rows 33 and 39, 24 rows 47
-// and 41; one sequence, 24 rows, 15 and 10.
+// Rows per key/value head up to which this file's kernel is used, the tcgen05 kernel above.  us here
+// and there, 16 sequences x 8 heads of 8187 keys, d = 128: bf16 16 rows 33 and 39, 24 rows 47 and 41; fp16
+// 16 rows 33 and 47.  One sequence of 65001 keys, 16 rows: bf16 21 and 24, fp16 21 and 29.  d = 64: bf16
+// 25 and 31, fp16 25 and 34.
 constexpr int kFewRows = 16;
 
 template <class Geo>
