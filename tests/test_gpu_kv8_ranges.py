@@ -279,3 +279,24 @@ def test_a_long_sequence_of_zero_values(G, n):
     w = ea.attn_kv8_weights(q, codes, ks, i32([cap]), lse, None, 1.0)
     assert (w.double() * cap / (G * n) - 1).abs().max() <= 2.0 ** -11
     status()
+
+
+# ------------------------------------------------------------------ many rows
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64), ("f16", 128)])
+def test_more_than_2048_rows_a_head(dtype, d):
+    """A prompt's chunk: 2404 rows of a key/value head (a last tile of 100), ragged, attention and weights."""
+    rng = np.random.default_rng(d)
+    G, n, lengths, counts = 4, 601, [1500, 601, 40], [601, 599, 33]
+    ca = Cache(rng, lengths, 1, 1536, d, 64)
+    q = rounded(rng.normal(size=(3, G, n, d)), dtype)
+    kw = dict(counts=i32(counts), mask="causal")
+    o, lse = ea.attn_fwd_kv8(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, d ** -0.5, **kw)
+    check_attend(ca, q, d ** -0.5, dtype, o, lse, counts, True)
+    w = ea.attn_kv8_weights(q.cuda(), ca.k8, ca.ks, ca.lengths, lse, None, d ** -0.5, **kw).double().cpu().numpy()
+    ref = kv8.add_weights(ca.c, q.double().numpy(), d ** -0.5, lse.double().cpu().numpy(), counts, True) - ca.c["w"]
+    S = kv8.attend(ca.c, q.double().numpy(), d ** -0.5, counts, True)[3]
+    rel = (d + 16) * 2.0 ** -23 * (S.max() + 32.0) + 2.0 ** -21 + G * n * 2.0 ** -24
+    for b, m in enumerate(lengths):
+        assert (np.abs(w - ref)[b, :, :m] <= rel * ref[b, :, :m]).all()
+    assert status() == ea.ATTN_OK
