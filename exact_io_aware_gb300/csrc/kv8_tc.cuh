@@ -47,6 +47,9 @@ constexpr int kRows = 128;   // of a row tile
 constexpr int kThreads = 512;
 constexpr int kGroups = kBlockKeys / 16;  // scale groups of a block
 constexpr int kRegsIssue = 64, kRegsSoftmax = 184, kRegsConvert = 80;
+// Format fields of a kind::f8f6f4 instruction descriptor (0 is E4M3) for E5M2 in A or in B, whatever the
+// other operand is.
+constexpr uint32_t kE5m2InA = 1u << 7, kE5m2InB = 1u << 10;
 constexpr int kSegReaders = 15;  // warps that are told of each tile
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128, "more registers than launched");
 
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 2) {
       // ------------------------------------------------------------ MMA issuer of row tile t
       const int t = warp;
-      constexpr uint32_t id_s = idesc_e4m3(128, kBlockKeys), id_rest = idesc_e4m3(128, kBlockKeys, true);
+      constexpr uint32_t id_s = idesc_e4m3(128, kBlockKeys), id_rest = id_s | kE5m2InA;
       constexpr uint32_t id_o = idesc_f16(128, D, 0, 0, 1);
       const uint64_t dq = T8::desc_k(smem_u32(sQ + (split ? 0 : t) * C::kTerms * T8::kBytes), 0);
       const uint64_t dk0 = T8::desc_k(smem_u32(sK), 0);

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = min(kMostRows, geo.R - r0), tiles = rows > kRows ? 2 : 1;
       if (warp == 0) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t id_s = idesc_e4m3(128, kRows), id_rest = idesc_e4m3(128, kRows, false, true);
+        constexpr uint32_t id_s = idesc_e4m3(128, kRows), id_rest = id_s | tc::kE5m2InB;
         const uint64_t dq = T8::desc_k(smem_u32(sQ), 0), dk0 = T8::desc_k(smem_u32(sK), 0);
         ok = mbar_wait_warp(&sh.q_full, part & 1, p.status, 0x32);
         for (int j = j0; j < j1 && ok; ++j) {

@@ -389,11 +389,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Instruction descriptor for kind::f8f6f4 with E4M3 A and B and fp32 accumulation, both
-// operands K-major (the format fields, bits 7-9 of A and 10-12 of B, are 0 for E4M3 and 1 for E5M2;
-// A and B need not agree).
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool a_e5m2 = false, bool b_e5m2 = false) {
-  return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) |
-         ((N >> 3) << 17) | ((M >> 4) << 24);
+// operands K-major (the format fields are zero for E4M3).
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]ᵀ, 8-bit operands (kind::f8f6f4, K = 32 per instruction).
