@@ -13,6 +13,10 @@ CPU or PyTorch fallback, and every entry point raises if the library is not buil
     o, lse = attn_fwd_kv8(q, k8, v8, ks, vs, lengths, c)         # write, attend,
     attn_kv8_weights(q, k8, ks, lengths, lse, w, c)              # weigh the tokens, and
     attn_kv8_evict(k8, v8, ks, vs, w, lengths, keep, *smaller)   # keep the heaviest
+    tree = attn_tree_mask(parents)                               # a tree of drafted tokens: what each
+    o, lse = attn_fwd_kv8_tree(q, k8, v8, ks, vs, lengths, tree, c)  # sees, its attention, which are
+    path, accepted, token = attn_draft_verify(p, q, tokens, parents, uniforms)  # accepted, and the
+    lengths = attn_kv8_keep(k8, v8, ks, vs, lengths, path, accepted)            # cache of those
 """
 from __future__ import annotations
 
@@ -32,7 +36,8 @@ __all__ = [
     "attn_selftest_wait_timeout", "attn_fwd_split", "attn_fwd_split_count",
     "attn_fwd_split_workspace_bytes", "attn_merge", "attn_selftest_exp2",
     "attn_debug_set_ring_stages", "ATTN_WARN_CLAMPED", "attn_kv8_append", "attn_fwd_kv8",
-    "attn_fwd_kv8_workspace_bytes", "attn_kv8_weights", "attn_kv8_evict",
+    "attn_fwd_kv8_workspace_bytes", "attn_kv8_weights", "attn_kv8_evict", "attn_tree_mask",
+    "attn_fwd_kv8_tree", "attn_draft_verify", "attn_kv8_keep",
 ]
 
 
@@ -134,6 +139,14 @@ def load():
     lib.attn_kv8_weights.restype = i32
     lib.attn_kv8_evict.argtypes = [i32] * 5 + [vp] * 6 + [i32] * 4 + [vp] * 8
     lib.attn_kv8_evict.restype = i32
+    lib.attn_tree_mask.argtypes = [i32] * 2 + [vp] * 4
+    lib.attn_tree_mask.restype = i32
+    lib.attn_fwd_kv8_tree.argtypes = [i32] * 8 + [f32] + [vp] * 11 + [sz, vp]
+    lib.attn_fwd_kv8_tree.restype = i32
+    lib.attn_draft_verify.argtypes = [i32] * 4 + [vp] * 10
+    lib.attn_draft_verify.restype = i32
+    lib.attn_kv8_keep.argtypes = [i32] * 6 + [vp] * 11
+    lib.attn_kv8_keep.restype = i32
     _lib = lib
     return lib
 
@@ -495,6 +508,28 @@ def attn_fwd_kv8_workspace_bytes(dtype, B, H, H_kv, n_q, d, cap) -> int:
     return int(load().attn_fwd_kv8_workspace_bytes(code, B, H, H_kv, n_q, d, cap))
 
 
+def _kv8_outputs(q, code, B, H, Hk, n, d, cap, dev, o, lse, workspace):
+    """The attention's outputs and workspace, allocated where not given, and the workspace's size."""
+    f32, size = torch.float32, 0
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _kv8_check(dev, (o, q.dtype, (B, H, n, d), "o"))
+    if lse is None:
+        lse = torch.empty((B, H, n), dtype=f32, device=dev)
+    else:
+        _kv8_check(dev, (lse, f32, (B, H, n), "lse"))
+    if workspace is None:
+        size = _kv8_workspace(code, B, H, Hk, n, d, cap, dev)
+        if size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's device")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    return o, lse, workspace, size
+
+
 def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="none", o=None,
                  lse=None, workspace=None, stream=None):
     """Attention of q [B,H,n_q,d] (float16 or bfloat16) over the 8-bit cache of
@@ -512,26 +547,106 @@ def attn_fwd_kv8(q, k8, v8, k_scales, v_scales, lengths, c, counts=None, mask="n
                       (counts, i32, (B,), "counts"))
     lib, code = load(), DTYPE_CODE[q.dtype]
     with _On(dev, stream) as s:
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _kv8_check(dev, (o, q.dtype, rows, "o"))
-        if lse is None:
-            lse = torch.empty((B, H, n), dtype=f32, device=dev)
-        else:
-            _kv8_check(dev, (lse, f32, (B, H, n), "lse"))
-        if workspace is None:
-            size = _kv8_workspace(code, B, H, Hk, n, d, cap, dev)
-            if size > 0:
-                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        elif workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the call's device")
-        else:
-            size = workspace.numel() * workspace.element_size()
+        o, lse, workspace, size = _kv8_outputs(q, code, B, H, Hk, n, d, cap, dev, o, lse, workspace)
         _check(lib.attn_fwd_kv8(code, B, H, Hk, n, d, cap, block, c, *ptrs, kind, o.data_ptr(),
                                 lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
                                 size, s))
     return o, lse
+
+
+def attn_tree_mask(parents, counts=None, tree=None, stream=None):
+    """The words ``attn_fwd_kv8_tree`` takes, int32 [B,n,ceil(n/32)]: bit j of row i is set iff
+    node j is node i or one of its ancestors.  ``parents`` int32 [B,n] has each node's parent, a
+    lower number, and -1 for node 0; rows from counts[b] (int32 [B]; None: n) on are 0."""
+    if parents.get_device() < 0 or parents.dim() != 2 or 0 in parents.shape:
+        raise ValueError("parents must be a CUDA tensor [B,n]")
+    (B, n), dev, i32 = parents.shape, parents.get_device(), torch.int32
+    ptrs = _kv8_check(dev, (parents, i32, (B, n), "parents"), (counts, i32, (B,), "counts"))
+    with _On(dev, stream) as s:
+        if tree is None:
+            tree = torch.empty((B, n, (n + 31) // 32), dtype=i32, device=dev)
+        else:
+            _kv8_check(dev, (tree, i32, (B, n, (n + 31) // 32), "tree"))
+        _check(load().attn_tree_mask(B, n, *ptrs, tree.data_ptr(), s))
+    return tree
+
+
+def attn_fwd_kv8_tree(q, k8, v8, k_scales, v_scales, lengths, tree, c, counts=None, o=None, lse=None,
+                      workspace=None, stream=None):
+    """``attn_fwd_kv8`` for a tree of drafted tokens: the rows of q are each sequence's last counts[b]
+    (None: n_q) positions, and a row sees every key before them and those of them whose bits are
+    set in its row of ``tree`` (int32 [B,n_q,ceil(n_q/32)], ``attn_tree_mask``).  Returns (o, lse)."""
+    B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
+    H, n, _ = _kv8_heads(q, B, Hk, "none")
+    _kv8_types((k8, v8), (q,))
+    f32, i32, rows = torch.float32, torch.int32, (B, H, n, d)
+    codes, scales = (B, Hk, cap, d), (B, Hk, cap // block)
+    if tree is None:
+        raise ValueError("tree must be given")
+    ptrs = _kv8_check(dev, (q, q.dtype, rows, "q"), (k8, k8.dtype, codes, "k8"),
+                      (v8, v8.dtype, codes, "v8"), (k_scales, f32, scales, "k_scales"),
+                      (v_scales, f32, scales, "v_scales"), (lengths, i32, (B,), "lengths"),
+                      (counts, i32, (B,), "counts"), (tree, i32, (B, n, (n + 31) // 32), "tree"))
+    lib, code = load(), DTYPE_CODE[q.dtype]
+    with _On(dev, stream) as s:
+        o, lse, workspace, size = _kv8_outputs(q, code, B, H, Hk, n, d, cap, dev, o, lse, workspace)
+        _check(lib.attn_fwd_kv8_tree(code, B, H, Hk, n, d, cap, block, c, *ptrs, o.data_ptr(),
+                                     lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                                     size, s))
+    return o, lse
+
+
+def attn_draft_verify(target, draft, tokens, parents, uniforms, counts=None, path=None, accepted=None,
+                      next_token=None, stream=None):
+    """Which nodes of each sequence's tree of drafted tokens are accepted, and the token after them.
+    ``target`` [B,n,V] (float32, float16 or bfloat16) has the target's probabilities after each
+    node, ``draft`` the draft's that the children were drawn from, or None for children that were
+    chosen; ``tokens`` int32 [B,n], ``parents`` as for ``attn_tree_mask``, ``uniforms`` float32 [B,n]
+    random numbers in [0, 1) (node 0's draws the token after).  Returns (path int32 [B,n], the accepted
+    nodes, ascending, then -1; accepted int32 [B]; next_token int32 [B])."""
+    if target.get_device() < 0 or target.dim() != 3 or 0 in target.shape:
+        raise ValueError("target must be a CUDA tensor [B,n,V]")
+    if target.dtype not in DTYPE_CODE:
+        raise ValueError("probabilities must be float32, float16 or bfloat16")
+    (B, n, V), dev, i32, dt = target.shape, target.get_device(), torch.int32, target.dtype
+    ptrs = _kv8_check(dev, (target, dt, (B, n, V), "target"), (draft, dt, (B, n, V), "draft"),
+                      (tokens, i32, (B, n), "tokens"), (parents, i32, (B, n), "parents"),
+                      (counts, i32, (B,), "counts"), (uniforms, torch.float32, (B, n), "uniforms"))
+    with _On(dev, stream) as s:
+        path = torch.empty((B, n), dtype=i32, device=dev) if path is None else path
+        accepted = torch.empty((B,), dtype=i32, device=dev) if accepted is None else accepted
+        next_token = torch.empty((B,), dtype=i32, device=dev) if next_token is None else next_token
+        outs = _kv8_check(dev, (path, i32, (B, n), "path"), (accepted, i32, (B,), "accepted"),
+                          (next_token, i32, (B,), "next_token"))
+        _check(load().attn_draft_verify(DTYPE_CODE[dt], B, n, V, *ptrs, *outs, s))
+    return path, accepted, next_token
+
+
+def attn_kv8_keep(k8, v8, k_scales, v_scales, lengths, path, accepted, counts=None, weights=None,
+                  lengths_out=None, stream=None):
+    """Brings the 8-bit cache from a tree of n nodes at each sequence's end to its accepted ones, in
+    place: the tokens of nodes path[b, :accepted[b]] (int32 [B,n] and [B], ``attn_draft_verify``) move
+    next to those before the tree, quantized again by ``attn_kv8_append``'s rule, with their
+    ``weights`` (float32 [B,H_kv,cap], optional).  Returns the new lengths (another tensor than
+    ``lengths``)."""
+    B, Hk, cap, d, block, dev = _kv8_shape(k8, k_scales)
+    _kv8_types((k8, v8), ())
+    if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1:
+        raise ValueError("path must be [B,n]")
+    n, f32, i32 = path.shape[1], torch.float32, torch.int32
+    codes, scales = (B, Hk, cap, d), (B, Hk, cap // block)
+    ptrs = _kv8_check(dev, (k8, k8.dtype, codes, "k8"), (v8, v8.dtype, codes, "v8"),
+                      (k_scales, f32, scales, "k_scales"), (v_scales, f32, scales, "v_scales"),
+                      (lengths, i32, (B,), "lengths"), (counts, i32, (B,), "counts"),
+                      (path, i32, (B, n), "path"), (accepted, i32, (B,), "accepted"),
+                      (weights, f32, (B, Hk, cap), "weights"))
+    with _On(dev, stream) as s:
+        if lengths_out is None:
+            lengths_out = torch.empty((B,), dtype=i32, device=dev)
+        else:
+            _kv8_check(dev, (lengths_out, i32, (B,), "lengths_out"))
+        _check(load().attn_kv8_keep(B, Hk, n, d, cap, block, *ptrs, lengths_out.data_ptr(), s))
+    return lengths_out
 
 
 def attn_kv8_weights(q, k8, k_scales, lengths, lse, weights, c, counts=None, mask="none", out=None,

@@ -25,6 +25,7 @@ struct Kv8Args {
   float* v_scales;
   const int32_t* lengths;
   const int32_t* counts;  // null: n new tokens in every sequence
+  const uint32_t* tree;  // attend: what the rows see of the call's own tokens; null: by `causal`
   void* o;
   float* lse;
   const float* weights;
@@ -54,11 +55,28 @@ struct Kv8EvictArgs {
   int sms;
 };
 
+// A tree of drafted tokens at the sequences' ends, down to the accepted ones.
+struct Kv8KeepArgs {
+  int B, Hk, n, d, cap, block;
+  uint8_t* k8;
+  uint8_t* v8;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* lengths;
+  const int32_t* counts;  // null: n tokens in every sequence's tree
+  const int32_t* path;
+  const int32_t* accepted;
+  float* weights;  // or null
+  int32_t* lengths_out;
+  uint32_t* status;
+};
+
 // Each launcher returns 0 or a negative ATTN_ERR_* code and fills `err` on failure.
 int launch_kv8_append(const Kv8Args& a, cudaStream_t s, std::string& err);
 int launch_kv8_attend(const Kv8Args& a, cudaStream_t s, std::string& err);
 int launch_kv8_weights(const Kv8Args& a, cudaStream_t s, std::string& err);
 int launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t s, std::string& err);
+int launch_kv8_keep(const Kv8KeepArgs& a, cudaStream_t s, std::string& err);
 
 size_t kv8_attend_workspace_bytes(int B, int Hk, int G, int n, int d, int cap, int sms);
 

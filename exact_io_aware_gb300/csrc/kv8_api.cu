@@ -3,7 +3,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <exception>
 #include <initializer_list>
 #include <string>
 
@@ -13,35 +12,11 @@
 
 namespace {
 
-using ea::CallRange;
+using ea::entry;
 using ea::fail;
-
-// Runs an entry point's body; a C++ exception (memory for a message, a mutex) becomes a code.
-template <typename F>
-int entry(const char* name, F&& body) noexcept {
-  CallRange range(name);
-  try {
-    return body();
-  } catch (...) {
-    return ATTN_ERR_CUDA;
-  }
-}
-
-// A launcher's outcome as the entry point's.  The runtime keeps a refused launch as its last error;
-// it is taken here, so that no later call reads it as its own.
-int outcome(int rc, const std::string& err) {
-  if (rc == 0) return ATTN_OK;
-  (void)cudaGetLastError();
-  return fail(rc, err);
-}
-
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
-// Bytes [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
-}
+using ea::misaligned;
+using ea::outcome;
+using ea::overlap;
 
 // The largest sizes: heads of a grid's y axis, tokens of a sequence, rows of a key/value head.
 constexpr int64_t kMostHeads = 65535, kMostCap = int64_t(1) << 30, kMostRows = int64_t(1) << 24;
@@ -75,16 +50,21 @@ int check_dtype(int dtype) {
 }
 
 // Query heads and rows of the attention and weights calls.
-int check_query(int H, int Hk, int n_q, int mask_kind, const int32_t* counts) {
+int check_rows(int H, int Hk, int n_q, const int32_t* counts) {
   if (n_q < 1 || H < 1) return fail(ATTN_ERR_INVALID_ARG, "H and n_q must be positive");
   if (H % Hk != 0) return fail(ATTN_ERR_INVALID_ARG, "H must be a multiple of H_kv");
   if (static_cast<int64_t>(H / Hk) * n_q > kMostRows)
     return fail(ATTN_ERR_UNSUPPORTED, "H / H_kv * n_q must be at most 2^24");
+  if (misaligned(counts, 4)) return fail(ATTN_ERR_ALIGNMENT, "counts must be 4-byte aligned");
+  return ATTN_OK;
+}
+
+int check_query(int H, int Hk, int n_q, int mask_kind, const int32_t* counts) {
+  if (int rc = check_rows(H, Hk, n_q, counts)) return rc;
   if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_BITMAP)
     return fail(ATTN_ERR_INVALID_ARG, "unknown mask kind");
   if (mask_kind == ATTN_MASK_BITMAP)
     return fail(ATTN_ERR_UNSUPPORTED, "the 8-bit cache takes no bitmap mask");
-  if (misaligned(counts, 4)) return fail(ATTN_ERR_ALIGNMENT, "counts must be 4-byte aligned");
   return ATTN_OK;
 }
 
@@ -101,6 +81,30 @@ ea::Kv8Args cache_args(int B, int Hk, int G, int n, int d, int cap, int block, c
   a.lengths = lengths;
   a.counts = counts;
   return a;
+}
+
+// The rest of an attention call whose other arguments are in `a`.
+int attend(ea::Kv8Args& a, const void* q, const void* k8, const void* v8, const float* k_scales,
+           const float* v_scales, void* o, float* lse, void* workspace, size_t workspace_bytes,
+           void* stream) {
+  a.sms = ea::device_sm_count();
+  const size_t need = ea::kv8_attend_workspace_bytes(a.B, a.Hk, a.G, a.n, a.d, a.cap, a.sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(ATTN_ERR_WORKSPACE, "workspace missing or smaller than attn_fwd_kv8_workspace_bytes");
+  if (misaligned(workspace, 16)) return fail(ATTN_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (int rc = ea::device_status_word(&a.status)) return rc;
+  if (a.sms < 1) return fail(ATTN_ERR_CUDA, "the device's multiprocessor count is unknown");
+  a.q = q;
+  a.k8 = static_cast<uint8_t*>(const_cast<void*>(k8));
+  a.v8 = static_cast<uint8_t*>(const_cast<void*>(v8));
+  a.k_scales = const_cast<float*>(k_scales);
+  a.v_scales = const_cast<float*>(v_scales);
+  a.o = o;
+  a.lse = lse;
+  a.workspace = workspace;
+  std::string err;
+  const int rc = ea::launch_kv8_attend(a, static_cast<cudaStream_t>(stream), err);
+  return outcome(rc, err);
 }
 
 }  // namespace
@@ -156,27 +160,29 @@ int attn_fwd_kv8(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int
       return rc;
     if (int rc = check_query(H, H_kv, n_q, mask_kind, counts)) return rc;
     ea::Kv8Args a = cache_args(B, H_kv, H / H_kv, n_q, d, cap, block, lengths, counts);
-    a.sms = ea::device_sm_count();
-    const size_t need = ea::kv8_attend_workspace_bytes(B, H_kv, a.G, n_q, d, cap, a.sms);
-    if (need > 0 && (!workspace || workspace_bytes < need))
-      return fail(ATTN_ERR_WORKSPACE, "workspace missing or smaller than attn_fwd_kv8_workspace_bytes");
-    if (misaligned(workspace, 16)) return fail(ATTN_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
-    if (int rc = ea::device_status_word(&a.status)) return rc;
-    if (a.sms < 1) return fail(ATTN_ERR_CUDA, "the device's multiprocessor count is unknown");
     a.bf16 = dtype == ATTN_BF16;
     a.causal = mask_kind == ATTN_MASK_CAUSAL;
     a.c = c;
-    a.q = q;
-    a.k8 = static_cast<uint8_t*>(const_cast<void*>(k8));
-    a.v8 = static_cast<uint8_t*>(const_cast<void*>(v8));
-    a.k_scales = const_cast<float*>(k_scales);
-    a.v_scales = const_cast<float*>(v_scales);
-    a.o = o;
-    a.lse = lse;
-    a.workspace = workspace;
-    std::string err;
-    const int rc = ea::launch_kv8_attend(a, static_cast<cudaStream_t>(stream), err);
-    return outcome(rc, err);
+    return attend(a, q, k8, v8, k_scales, v_scales, o, lse, workspace, workspace_bytes, stream);
+  });
+}
+
+int attn_fwd_kv8_tree(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int block, float c,
+                      const void* q, const void* k8, const void* v8, const float* k_scales,
+                      const float* v_scales, const int32_t* lengths, const int32_t* counts,
+                      const uint32_t* tree, void* o, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  return entry("attn_fwd_kv8_tree", [&]() -> int {
+    if (int rc = check_dtype(dtype)) return rc;
+    if (int rc = check_cache(B, H_kv, d, cap, block, {q, k8, v8, o},
+                             {k_scales, v_scales, lengths, tree, lse}))
+      return rc;
+    if (int rc = check_rows(H, H_kv, n_q, counts)) return rc;
+    ea::Kv8Args a = cache_args(B, H_kv, H / H_kv, n_q, d, cap, block, lengths, counts);
+    a.bf16 = dtype == ATTN_BF16;
+    a.c = c;
+    a.tree = tree;
+    return attend(a, q, k8, v8, k_scales, v_scales, o, lse, workspace, workspace_bytes, stream);
   });
 }
 
@@ -253,6 +259,37 @@ int attn_kv8_evict(int B, int H_kv, int d, int cap, int block, const void* k8, c
     if (int rc = ea::device_status_word(&a.status)) return rc;
     std::string err;
     const int rc = ea::launch_kv8_evict(a, static_cast<cudaStream_t>(stream), err);
+    return outcome(rc, err);
+  });
+}
+
+int attn_kv8_keep(int B, int H_kv, int n, int d, int cap, int block, void* k8, void* v8,
+                  float* k_scales, float* v_scales, const int32_t* lengths, const int32_t* counts,
+                  const int32_t* path, const int32_t* accepted, float* weights,
+                  int32_t* lengths_out, void* stream) {
+  return entry("attn_kv8_keep", [&]() -> int {
+    if (int rc = check_cache(B, H_kv, d, cap, block, {k8, v8},
+                             {k_scales, v_scales, lengths, path, accepted, lengths_out}))
+      return rc;
+    if (n < 1) return fail(ATTN_ERR_INVALID_ARG, "n must be positive");
+    if (n > (1 << 30)) return fail(ATTN_ERR_UNSUPPORTED, "n must be at most 2^30");
+    if (misaligned(counts, 4) || misaligned(weights, 4))
+      return fail(ATTN_ERR_ALIGNMENT, "counts and weights must be 4-byte aligned");
+    const size_t seqs = static_cast<size_t>(B) * 4, heads = static_cast<size_t>(B) * H_kv;
+    struct Range { const void* p; size_t n; };
+    const Range all[] = {{k8, heads * cap * d}, {v8, heads * cap * d},
+                         {k_scales, heads * (cap / block) * 4}, {v_scales, heads * (cap / block) * 4},
+                         {weights, weights ? heads * cap * 4 : 0}, {lengths_out, seqs},
+                         {lengths, seqs}, {counts, counts ? seqs : 0}, {path, seqs * n}, {accepted, seqs}};
+    for (int i = 0; i < 6; ++i)  // what is written against all that comes after it
+      for (int j = i + 1; j < 10; ++j)
+        if (all[i].n && all[j].n && overlap(all[i].p, all[i].n, all[j].p, all[j].n))
+          return fail(ATTN_ERR_INVALID_ARG, "the cache, lengths_out and the inputs must not overlap");
+    ea::Kv8KeepArgs a{B, H_kv, n, d, cap, block, static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8),
+                      k_scales, v_scales, lengths, counts, path, accepted, weights, lengths_out, nullptr};
+    if (int rc = ea::device_status_word(&a.status)) return rc;
+    std::string err;
+    const int rc = ea::launch_kv8_keep(a, static_cast<cudaStream_t>(stream), err);
     return outcome(rc, err);
   });
 }

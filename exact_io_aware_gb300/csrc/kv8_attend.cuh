@@ -6,6 +6,14 @@
 namespace ea {
 namespace kv8 {
 
+constexpr int kAttendWarps = 4;  // of a CTA (few rows)
+// A cache of at most this many tokens a sequence is not cut: each tile is one CTA's, and there is
+// nothing to join.  us uncut and cut, at d = 64, G = 1 and d = 128, G = 8: 8 heads of 512 tokens 5.8, 7.4
+// and 8.1, 8.8, of 1024 8.2, 7.9 and 11.6, 8.9; 256 heads of 512 tokens 6.9, 11.6 and 10.4, 15.9 (of 1024
+// still 10.6, 14.9 and 16.4, 20.8: with many heads longer tiles fill the device, with few they do not).
+constexpr int kAlignedCap = 512;
+constexpr int kMostCtas = 3;  // of any variant, on a multiprocessor
+
 constexpr float kTop = 6.0f;     // log2 of the largest P when m is set
 constexpr float kRaise = 14.0f;  // a larger log2 P raises m
 constexpr float kNoMax = -3.0e38f;
@@ -46,7 +54,25 @@ struct AttendParams {
   int ctas;        // runs the work is cut into; 0: one CTA a tile, and no parts
   int min_chunks;  // a run has at least this many
   uint32_t* status;
+  const uint32_t* tree;  // [B][n][tree_words]: of a tree's rows, the query rows that each sees
+  int tree_words;
 };
+
+// Keys key0 .. key0 + 31 that query row i of a tree (-1: a padding row) sees, one bit each: all before
+// the call's own cnt tokens, and of those the row's.
+template <class Geo>
+__device__ __forceinline__ uint32_t tree_window(const AttendParams<Geo>& p, int b, int i, int key0, int len, int cnt) {
+  const int left = len - key0;
+  const uint32_t held = left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+  if (i < 0) return held;
+  const uint32_t* row = p.tree + (static_cast<int64_t>(b) * p.geo.n + i) * p.tree_words;
+  const int at = key0 - (len - cnt);  // of the row's bits, the first key's
+  if (at <= -32) return held;
+  if (at < 0) return held & ((__ldg(row) << -at) | ((1u << -at) - 1u));
+  const int w = at >> 5;
+  const uint32_t lo = w < p.tree_words ? __ldg(row + w) : 0u, hi = w + 1 < p.tree_words ? __ldg(row + w + 1) : 0u;
+  return held & __funnelshift_r(lo, hi, at & 31);
+}
 
 // Writes four columns of a finished row and, with the first of them, its LSE.  l = 0 is a row
 // that sees no key: O = 0, LSE = -inf.
@@ -173,7 +199,10 @@ cudaError_t launch_join(AttendParams<Geo>& p, cudaStream_t s) {
 // Attention of many rows on the tcgen05 tensor cores (kv8_tc_*.cu), in tiles of 256 rows, or of 128
 // where a head has no more.
 constexpr int kTcTileRows = 256;
-template <bool kBf16, int D>
+template <bool kBf16, int D, bool kTree>
 cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s);
+// Of few rows (kv8_attend_few.cuh), in tiles of 8, 16 or 32.
+template <bool kBf16, int D, bool kTree>
+cudaError_t launch_kv8_few(const kv8::AttendParams<kv8::ByQuery>& p, int sms, cudaStream_t s);
 
 }  // namespace ea

@@ -1,6 +1,6 @@
 // Attention of many query rows over the 8-bit cache, on the tcgen05 tensor cores.
 //
-// The mathematics is that of kv8_attend.cu: in base 2, x_rj = log2(e) s_rj + log2(vs_j),
+// The mathematics is that of kv8_attend_few.cuh: in base 2, x_rj = log2(e) s_rj + log2(vs_j),
 // P_rj = 2^{x_rj - m_r} rounded to fp16, z = P V on the codes, l = sum P / vs.
 //   * S = Q K^T is kind::f8f6f4 on the codes as they lie in memory.  A query row over a power of
 //     two (its largest value 224 .. 448) is a sum of 8-bit terms, q = q1 + q2 (+ q3), whose products
@@ -118,6 +118,7 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+template <bool kTree>
 __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int u0, int u1, int cta) {
   Seg s;
   s.b = pl.b, s.hk = pl.hk;
@@ -137,7 +138,7 @@ __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int u0,
     int lo, hi;
     const bool any = a < g.R && g.span(a, z, s.cnt, lo, hi);
     s.reach[t] = any ? chunks_of(g, query_keys(g, s.len, s.cnt, hi)) : 0;
-    s.least[t] = any ? query_keys(g, s.len, s.cnt, lo) : s.len;
+    s.least[t] = !any ? s.len : kTree ? max(s.len - s.cnt, 0) : query_keys(g, s.len, s.cnt, lo);
   }
   return s;
 }
@@ -340,7 +341,8 @@ __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, cons
   }
 }
 
-template <bool kBf16, int D>
+// kTree: the last cnt keys are seen by the rows of p.tree.
+template <bool kBf16, int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const AttendParams<ByHead> p) {
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ the run's tiles
       for (int seg = 0;; ++seg) {
         if (!mbar_wait_warp(&sh.seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, p.status, 0x31)) break;
-        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
+        const Seg sg = segment<kTree>(geo, pl, u0, u1, blockIdx.x);
         if (lane == 0) {
           sh.seg[seg & 3] = sg;
           if (sg.j0 == 0) note_run(p, pl, u0, u1);
@@ -692,10 +694,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kBlockKeys; ++k) sv[k] = __uint_as_float(rr[k]);
         }
         if (__builtin_expect(key0 + kBlockKeys > least, 0)) {
-          const int seen = lim - key0;
+          if constexpr (kTree) {
 #pragma unroll
-          for (int k = 0; k < kBlockKeys; ++k)
-            if (k >= seen) sv[k] = -INFINITY;
+            for (int k = 0; k < kBlockKeys; k += 32) {
+              const uint32_t see = tree_window(p, sg.b, real ? query : -1, key0 + k, sg.len, sg.cnt);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(see >> e & 1u)) sv[k + e] = -INFINITY;
+            }
+          } else {
+            const int seen = lim - key0;
+#pragma unroll
+            for (int k = 0; k < kBlockKeys; ++k)
+              if (k >= seen) sv[k] = -INFINITY;
+          }
         }
         const float mx = uniform ? block_max<1>(sv, sc, mul) : block_max<kGroups>(sv, sc, mul);
         float alpha = 1.0f;
@@ -795,7 +807,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int k1 = min(lim, (sg.j0 + sg.steps) * kBlockKeys);
           const uint32_t* vw = reinterpret_cast<const uint32_t*>(
               p.v8 + ((static_cast<int64_t>(sg.b) * geo.Hk + sg.hk) * geo.cap) * D);
-          for (int key = k0; key < k1; ++key)
+          for (int key = k0; key < k1; ++key) {
+            if (kTree && !(tree_window(p, sg.b, real ? query : -1, key, sg.len, sg.cnt) & 1u)) continue;
             for (int w = 0; w < D / 4; ++w) {
               const uint32_t x = __ldg(vw + static_cast<int64_t>(key) * (D / 4) + w);
               const uint32_t eq = __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & 0x08040201u;
@@ -804,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < D / 32; ++i)
                 if (i == w / 8) bad[i] |= bits;
             }
+          }
         }
         const bool write = row < geo.R;
         const bool none = l == 0.0f || !real;  // a padding row, or one that sees no key
@@ -890,10 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace tc
 }  // namespace kv8
 
-template <bool kBf16, int D>
+template <bool kBf16, int D, bool kTree>
 cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
   using C = kv8::tc::Config<kBf16, D>;
-  auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D>;
+  auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D, kTree>;
   constexpr size_t smem = C::kOffShared + sizeof(kv8::tc::Shared);
   static_assert(smem <= 227 * 1024, "shared memory overflow");
   CUtensorMap tm_k, tm_v;

@@ -1,0 +1,6 @@
+// Attention of many rows over the 8-bit cache under a tree: bf16, head dimension 64.
+#include "kv8_tc.cuh"
+
+namespace ea {
+template cudaError_t launch_kv8_tc<true, 64, true>(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s);
+}  // namespace ea

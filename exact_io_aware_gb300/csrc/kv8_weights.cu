@@ -4,7 +4,7 @@
 // fixed order, so the result does not depend on the launch.
 //
 // This file: the kernel for few rows, which is bound by reading the codes, and the choice between
-// it and the tcgen05 kernel for many (kv8_weights_tc.cu).  Scores are formed as in kv8_attend.cu
+// it and the tcgen05 kernel for many (kv8_weights_tc.cu).  Scores are formed as in kv8_attend_few.cuh
 // (S^T = K Q^T, a warp to 32 keys), the queries stay in registers, and a key's weight is summed
 // over the rows of a lane and then over the four lanes that share the key.  Measured (d = 128, four
 // rows): 256 heads of 2000 to 8192 keys, 36.2 us, 4.9 TB/s, 73 % of the measured copy rate.

@@ -5,6 +5,7 @@ For profilers (ncu) and for timing one shape or one named workload:
     python -m exact_io_aware_gb300.run --B 1 --H 64 --n 4096 --d 128 --iters 2
     python -m exact_io_aware_gb300.run --workload longctx_bf16_n65536 --iters 5
     python -m exact_io_aware_gb300.run --kv8 --B 32 --H 32 --H-kv 8 --n 1 --n-kv 4096 --keep 1024
+    python -m exact_io_aware_gb300.run --kv8-tree --B 16 --H 32 --H-kv 8 --n 26 --n-kv 8192
 
 Inputs are seeded N(0,1) tensors generated on the device (the workload's query scale
 applied); a bitmap workload uses the seeded allowed-key sets of ``synth``.  Prints the mean
@@ -49,8 +50,12 @@ def main(argv=None):
     ap.add_argument("--kv8", action="store_true",
                     help="8-bit key/value cache of --n-kv tokens: append of --n tokens, attention of "
                          "--n rows, their weights, and eviction down to --keep tokens")
-    ap.add_argument("--H-kv", type=int, default=0, help="with --kv8: key/value heads (default: H)")
-    ap.add_argument("--block", type=int, default=64, help="with --kv8: tokens of a scale block")
+    ap.add_argument("--kv8-tree", action="store_true",
+                    help="decoding round over an 8-bit cache of --n-kv tokens, the last --n of them a tree of "
+                         "drafted tokens: its mask, append, attention, verification, and the accepted ones kept")
+    ap.add_argument("--vocab", type=int, default=32768, help="with --kv8-tree: size of the vocabulary")
+    ap.add_argument("--H-kv", type=int, default=0, help="with --kv8, --kv8-tree: key/value heads (default: H)")
+    ap.add_argument("--block", type=int, default=64, help="with --kv8, --kv8-tree: tokens of a scale block")
     ap.add_argument("--keep", type=int, default=0, help="with --kv8: tokens kept (default: a quarter)")
     ap.add_argument("--fp8", action="store_true", help="forward through attn_fwd_fp8 (E4M3 inputs)")
     ap.add_argument("--fp8-blocks", action="store_true",
@@ -83,6 +88,8 @@ def main(argv=None):
     ea.load()
     if a.kv8:
         return _run_kv8(a, B, H, n, a.n_kv or 4096, d, dt, mask, c)
+    if a.kv8_tree:
+        return _run_kv8_tree(a, B, H, n, a.n_kv or 4096, d, dt, c)
     if a.n_kv:
         return _run_kv(a, B, H, n, a.n_kv, d, dt, mask, c, kvb)
     if a.fp8:
@@ -225,6 +232,40 @@ def _run_kv(a, B, H, nq, nk, d, dt, mask, c, kvb):
     return 0 if status == ea.ATTN_OK else 1
 
 
+def _normals():
+    """A function of sizes: seeded N(0,1) values on the device."""
+    import torch
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    return lambda *s: torch.randn(s, device="cuda", generator=g)
+
+
+def _kv8_cache(B, Hk, cap, d, block):
+    import torch
+
+    codes = [torch.zeros((B, Hk, cap, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones((B, Hk, cap // block), device="cuda") for _ in range(2)]
+    return [*codes, *scales]
+
+
+def _time_each(ops, iters):
+    """Mean time of each operator's calls in us, after one untimed call."""
+    import torch
+
+    out = {}
+    for name, op in ops.items():
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        op()
+        ev[0].record()
+        for _ in range(iters):
+            op()
+        ev[1].record()
+        torch.cuda.synchronize()
+        out[f"{name}_us"] = ev[0].elapsed_time(ev[1]) * 1e3 / iters
+    return out
+
+
 def _run_kv8(a, B, H, n, nk, d, dt, mask, c):
     """One round over an 8-bit cache of nk tokens, the last n of them appended in it: time of each
     operator, and the cache bytes a second of the attention and weights calls."""
@@ -235,17 +276,9 @@ def _run_kv8(a, B, H, n, nk, d, dt, mask, c):
     cap = (nk + block - 1) // block * block
     keep = a.keep or max(1, nk // 4)
     small = (keep + block - 1) // block * block
-    g = torch.Generator(device="cuda")
-    g.manual_seed(0)
-    rand = lambda *s: torch.randn(s, device="cuda", generator=g)
-
-    def cache(m):
-        codes = [torch.zeros((B, Hk, m, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
-        scales = [torch.ones((B, Hk, m // block), device="cuda") for _ in range(2)]
-        return [*codes, *scales]
-
-    k8, v8, ks, vs = cache(cap)
-    k8b, v8b, ksb, vsb = cache(small)
+    rand = _normals()
+    k8, v8, ks, vs = _kv8_cache(B, Hk, cap, d, block)
+    k8b, v8b, ksb, vsb = _kv8_cache(B, Hk, small, d, block)
     w, wb = rand(B, Hk, cap).abs(), torch.zeros((B, Hk, small), device="cuda")
     lens = torch.full((B,), nk, dtype=torch.int32, device="cuda")
     lens_b = torch.zeros_like(lens)
@@ -262,18 +295,53 @@ def _run_kv8(a, B, H, n, nk, d, dt, mask, c):
     }
     out = {"workload": "kv8", "B": B, "H": H, "H_kv": Hk, "n": n, "n_kv": nk, "d": d, "block": block,
            "keep": keep, "dtype": str(dt).split(".")[-1], "mask": mask}
-    for name, op in ops.items():
-        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
-        op()
-        ev[0].record()
-        for _ in range(a.iters):
-            op()
-        ev[1].record()
-        torch.cuda.synchronize()
-        out[f"{name}_us"] = ev[0].elapsed_time(ev[1]) * 1e3 / a.iters
+    out.update(_time_each(ops, a.iters))
     out["status"] = ea.attn_device_status()
     out["attend_gbs"] = 2 * B * Hk * nk * d / out["attend_us"] / 1e3
     out["weights_gbs"] = B * Hk * nk * d / out["weights_us"] / 1e3
+    print(json.dumps(out) if a.json else " ".join(f"{k}={v}" for k, v in out.items()))
+    return 0 if out["status"] == ea.ATTN_OK else 1
+
+
+def _run_kv8_tree(a, B, H, n, nk, d, dt, c):
+    """One decoding round over an 8-bit cache of nk tokens, the last n of them a random tree whose nodes
+    were drawn from a draft near the target: time of each operator, and the nodes accepted a sequence."""
+    import torch
+
+    import exact_io_aware_gb300 as ea
+    Hk, block, V = a.H_kv or H, a.block, a.vocab
+    cap = (nk + block - 1) // block * block
+    rand = _normals()
+    k8, v8, ks, vs = _kv8_cache(B, Hk, cap, d, block)
+    lens = torch.full((B,), nk, dtype=torch.int32, device="cuda")
+    new = torch.empty_like(lens)
+    ea.attn_kv8_append(rand(B, Hk, nk, d).to(dt), rand(B, Hk, nk, d).to(dt), k8, v8, ks, vs, lens)
+    q, k, v = (rand(B, x, n, d).to(dt) for x in (H, Hk, Hk))
+    # A node's parent is one of the eight before it.
+    node = torch.arange(n, device="cuda")
+    parents = (node - 1 - (rand(B, n).abs() * 4).long().clamp(max=7)).clamp(min=0)
+    parents[:, 0] = -1
+    logits = 2.0 * rand(B, n, V)
+    target, draft = torch.softmax(logits, -1), torch.softmax(logits + 0.5 * rand(B, n, V), -1)
+    rows = draft[torch.arange(B, device="cuda")[:, None], parents.clamp(min=0)]
+    uniform = lambda: 0.5 * (1 + torch.erf(rand(B, n) / 2 ** 0.5)).clamp(0, 1 - 2.0 ** -24)
+    tokens = torch.searchsorted(rows.cumsum(-1), uniform()[..., None]).clamp(max=V - 1)[..., 0].int()
+    parents, uniforms = parents.int(), uniform()
+    tree = ea.attn_tree_mask(parents)
+    path, accepted, token = ea.attn_draft_verify(target, draft, tokens, parents, uniforms)
+    ops = {
+        "mask": lambda: ea.attn_tree_mask(parents, tree=tree),
+        "append": lambda: ea.attn_kv8_append(k, v, k8, v8, ks, vs, lens),
+        "attend": lambda: ea.attn_fwd_kv8_tree(q, k8, v8, ks, vs, lens, tree, c),
+        "verify": lambda: ea.attn_draft_verify(target, draft, tokens, parents, uniforms, path=path,
+                                               accepted=accepted, next_token=token),
+        "keep": lambda: ea.attn_kv8_keep(k8, v8, ks, vs, lens, path, accepted, lengths_out=new),
+    }
+    out = {"workload": "kv8_tree", "B": B, "H": H, "H_kv": Hk, "n": n, "n_kv": nk, "d": d, "block": block,
+           "vocab": V, "dtype": str(dt).split(".")[-1]}
+    out.update(_time_each(ops, a.iters))
+    out["status"] = ea.attn_device_status()
+    out["accepted"] = float(accepted.float().mean())
     print(json.dumps(out) if a.json else " ".join(f"{k}={v}" for k, v in out.items()))
     return 0 if out["status"] == ea.ATTN_OK else 1
 

@@ -333,6 +333,96 @@ int attn_kv8_evict(int B, int H_kv, int d, int cap, int block, const void* k8, c
                    void* k8_out, void* v8_out, float* k_scales_out, float* v_scales_out,
                    float* weights_out, int32_t* lengths_out, int32_t* kept, void* stream);
 
+/*
+ * Decoding by a tree of drafted tokens over the 8-bit cache (no counterpart on the pages).  Sequence b
+ * of a call has counts[b] nodes (NULL: n): node 0 is the token decided last, the others are drafts.
+ * parents (int32 [B][n]) has a node's parent, a node of a lower number, and -1 for node 0; a parent
+ * outside [-1, i) counts as -1 and raises ATTN_WARN_CLAMPED, as does a count outside [0, n].  One round:
+ * attn_kv8_append writes the nodes' keys and values at the sequence's end (lengths count them),
+ * attn_fwd_kv8_tree lets each node attend to the tokens before the tree and to its own ancestors,
+ * attn_draft_verify decides which nodes the target's probabilities accept and which token follows,
+ * and attn_kv8_keep brings the cache to the accepted ones.  All calls are asynchronous on `stream`, can
+ * be captured, and allocate nothing; what they read must not change until they have finished.
+ */
+
+/*
+ * The words attn_fwd_kv8_tree takes: tree [B][n][ceil(n / 32)], bit j % 32 of word j / 32 of row i
+ * is set iff j is node i or one of its ancestors.  Rows i >= counts[b] are written as 0.
+ * n: 1 .. 1024; B at most 2^24.  tree must not overlap the inputs.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_ALIGNMENT (4 bytes), ATTN_ERR_CUDA.
+ */
+int attn_tree_mask(int B, int n, const int32_t* parents, const int32_t* counts, uint32_t* tree,
+                   void* stream);
+
+/*
+ * attn_fwd_kv8 for a tree: the rows are the nodes, at positions lengths[b] - counts[b] + i, and row i
+ * sees every key before the tree (j < lengths[b] - counts[b]) and of the tree the nodes whose bits
+ * are set in its row of `tree` ([B][n_q][ceil(n_q / 32)] words, 4-byte aligned, shared by all heads).  The
+ * words may be any, not only a tree's; bits from counts[b] on do not matter.  Workspace
+ * (attn_fwd_kv8_workspace_bytes), other arguments, padding and empty rows, precision and errors as
+ * for attn_fwd_kv8.
+ */
+int attn_fwd_kv8_tree(int dtype, int B, int H, int H_kv, int n_q, int d, int cap, int block, float c,
+                      const void* q, const void* k8, const void* v8, const float* k_scales,
+                      const float* v_scales, const int32_t* lengths, const int32_t* counts,
+                      const uint32_t* tree, void* o, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Which drafted nodes are accepted, and the token after them, so that the tokens are distributed as if
+ * the target had been sampled token by token.  From node 0 on, with p = target[b][a] and
+ * q = draft[b][a] the probabilities after the node a at hand, a's children are asked in order of their
+ * numbers.  The residual starts as p with mass W = 1.
+ *   draft given: the children were drawn from q, independently.  Child i of token x is accepted iff
+ *       uniforms[b][i] q(x) W < r(x);
+ *     a refusal turns the residual r into max(r - W q, 0) and W into its sum (if that is 0, both
+ *     stay as they were).
+ *   draft NULL: the children were chosen, not drawn.  Child i is accepted iff
+ *       uniforms[b][i] W < r(x);
+ *     a refusal takes r(x) off W and sets it to 0.
+ * An accepted child becomes the node at hand, with a residual of its own.  When no child is left,
+ * the token that follows is the least v with r(0) + .. + r(v) > uniforms[b][0] (the sum of r).
+ *   dtype       ATTN_F32, ATTN_F16 or ATTN_BF16: type of target and draft
+ *   target      [B][n][V] probabilities after each node, 16-byte aligned; values count within
+ *               [0, 1], NaN as 0.  Rows need not sum to 1 exactly.
+ *   draft       the same of the draft, or NULL
+ *   tokens      int32 [B][n]: the nodes' tokens (node 0's is not read); one outside [0, V) has
+ *               probability 0 and raises ATTN_WARN_CLAMPED
+ *   uniforms    float32 [B][n] random numbers in [0, 1)
+ *   path        int32 [B][n]: the accepted nodes, ascending, node 0 first, then -1
+ *   accepted    int32 [B]: how many (0 for a sequence of no nodes)
+ *   next_token  int32 [B]: the token that follows; -1 for a sequence of no nodes, and where the
+ *               residual is 0 everywhere, which raises ATTN_WARN_EMPTY_ROW
+ * n: 1 .. 1024; V: 1 .. 2^30; B at most 2^24.  Decisions and masses are taken to 2^-40 relative at
+ * least; the result repeats bit for bit.  Outputs must not overlap inputs or one another.  Errors
+ * as for attn_tree_mask.
+ */
+int attn_draft_verify(int dtype, int B, int n, int V, const void* target, const void* draft,
+                      const int32_t* tokens, const int32_t* parents, const int32_t* counts,
+                      const float* uniforms, int32_t* path, int32_t* accepted, int32_t* next_token,
+                      void* stream);
+
+/*
+ * Brings the 8-bit cache from a tree of n nodes (counts[b] of them, at the sequences' ends) to the
+ * accepted ones, in place: the token of node path[b][i] moves to position
+ * lengths[b] - counts[b] + i, for i < accepted[b], and lengths_out[b] becomes
+ * lengths[b] - counts[b] + accepted[b] (0 if that is negative).  The tokens' values are quantized again
+ * where they land by attn_kv8_append's rule: blocks that hold tokens before the tree keep the larger of
+ * their scale and the one the tokens that land there need.  With weights != NULL the tokens'
+ * weights move too.  Positions from lengths_out[b] on are left as they were.
+ *   path      int32 [B][n], accepted int32 [B], as attn_draft_verify writes them.  An entry below
+ *             its own place i or not below counts[b] counts as the nearest of i and
+ *             counts[b] - 1, an `accepted` outside [0, counts[b]] as the nearest end; both raise
+ *             ATTN_WARN_CLAMPED.  Entries whose position would be negative are dropped.
+ *   n         1 .. 2^30
+ * The other arguments, sizes and errors as for attn_kv8_append.  The cache, lengths_out and the inputs
+ * must not overlap one another (ATTN_ERR_INVALID_ARG).
+ */
+int attn_kv8_keep(int B, int H_kv, int n, int d, int cap, int block, void* k8, void* v8,
+                  float* k_scales, float* v_scales, const int32_t* lengths, const int32_t* counts,
+                  const int32_t* path, const int32_t* accepted, float* weights,
+                  int32_t* lengths_out, void* stream);
+
 /* The number of key shares attn_fwd_kv uses when num_splits = 0 on the current device. */
 int attn_fwd_kv_split_count(int dtype, int B, int H, int n_q, int n_kv, int d, int kv_block);
 

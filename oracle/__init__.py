@@ -12,6 +12,8 @@ the pages on exact IO-aware attention:
 * ``fp8``        — E4M3 rounding and the FP8 forward's exact reference with its error bound.
 * ``kv8``        — the 8-bit key/value cache: writing into it, attention over it, accumulated
                    weights and eviction.
+* ``draft``      — a decoding round over a tree of drafted tokens: what each node sees, attention
+                   over the 8-bit cache, which nodes are accepted, and the cache of those.
 * ``dropout``    — the dropout extension with a replayed realised mask (Philox4x32-10 mask,
                    forward and reverse pass with the mask held fixed).
 
@@ -20,4 +22,4 @@ this package.  The GPU library never does, and this package imports nothing from
 Every function here is pinned by ``-m "not gpu"`` tests against worked examples, closed
 forms, invariants or brute force; none is marked "parity unpinned".
 """
-from . import attention, dropout, fp8, io_model, kv8, masks, tiled  # noqa: F401
+from . import attention, draft, dropout, fp8, io_model, kv8, masks, tiled  # noqa: F401
