@@ -32,6 +32,7 @@ struct DraftVerifyArgs {
   int32_t* accepted;
   int32_t* next_token;
   uint32_t* status;
+  int sms;
 };
 
 // Each launcher returns 0 or a negative ATTN_ERR_* code and fills `err` on failure.

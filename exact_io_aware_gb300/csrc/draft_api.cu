@@ -72,7 +72,7 @@ int attn_draft_verify(int dtype, int B, int n, int V, const void* target, const 
           return fail(ATTN_ERR_INVALID_ARG, "the outputs must not overlap the inputs or one another");
     const int type = dtype == ATTN_F32 ? ea::kProbF32 : dtype == ATTN_F16 ? ea::kProbF16 : ea::kProbBf16;
     ea::DraftVerifyArgs a{type, B, n, V, target, draft, tokens, parents, counts, uniforms,
-                          path, accepted, next_token, nullptr};
+                          path, accepted, next_token, nullptr, ea::device_sm_count()};
     if (int rc = ea::device_status_word(&a.status)) return rc;
     std::string err;
     const int rc = ea::launch_draft_verify(a, static_cast<cudaStream_t>(stream), err);

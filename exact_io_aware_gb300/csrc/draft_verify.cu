@@ -13,12 +13,13 @@
 //
 // A cluster of CTAs takes a sequence.  Its first CTA gathers the nodes' few probabilities and walks
 // the tree; the others only follow its commands (so that all take the same way whatever the inputs
-// do meanwhile): sum the masses at a node, each warp a contiguous share of the vocabulary, and, by the
-// one warp whose share the drawn number falls in, find the token.
+// do meanwhile): sum the masses at a node, each warp a contiguous share of the vocabulary.  After
+// the last sum every CTA looks for the share that the drawn number falls in, and the one that has it
+// for the token.
 //
-// Decisions are taken in 64 bits.  Sums over the vocabulary would be bound by the device's few 64-bit
-// units, so their terms and partial sums are pairs of float32 values (error-free sums and products),
-// about 2^-46 relative; each warp's is rounded to 64 bits once.
+// The device has two 64-bit units a multiprocessor and takes hundreds of cycles for a dependent step,
+// so sums are pairs of float32 values (error-free sums and products, about 2^-46 relative; two
+// elements an instruction), and a child's test is float32 unless its sides lie within 10^-6.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -49,43 +50,135 @@ struct VerifyParams {
   uint32_t* status;
 };
 
-enum Op : int { kSum, kFind, kDone };
-
 struct Command {  // of the first CTA to all
-  int op, node;
-  int warp;           // kFind: of the cluster
-  int refused;        // tokens taken out of the target's probabilities (drafts that were not drawn)
-  double S;
-  double goal, below;  // kFind: what the cumulative sum has to pass, and where the warp's share starts
+  bool done;      // nothing more to do
+  bool refusing;  // the sum is a refusal's: it counts only if it is not 0
+  bool last;      // no child is left: the token is drawn from the sum's shares
+  int node;
+  int refused;  // tokens taken out of the target's probabilities (drafts that were not drawn)
+  float2 S;     // (as a Pair)
 };
 
 struct Shared {
   Command cmd;
-  double mass[kMostRanks * kWarps];  // first CTA: of each warp's share
+  float2 mass[kMostRanks * kWarps];  // of each warp's share (first CTA; all of them for the last sum)
+  float2 tile[kWarps];
+  float2 goal, below;                // drawing the token: what the cumulative sum has to pass, and
+  int from;                          // the warp whose share it passes it in, with the sum before that
   float p[kMostNodes], q[kMostNodes], u[kMostNodes];
   int up[kMostNodes], token[kMostNodes];
   int refused[kMostNodes];
 };
 
-// A value as the unevaluated sum of two float32 values.
+// A value as the unevaluated sum of two float32 values.  (Explicit roundings: a product and a sum made
+// one by the compiler would no longer be error-free.)
 struct Pair {
   float hi, lo;
+  __device__ __forceinline__ Pair() : hi(0.0f), lo(0.0f) {}
+  __device__ __forceinline__ Pair(float h, float l) : hi(h), lo(l) {}
+  __device__ __forceinline__ explicit Pair(float2 x) : hi(x.x), lo(x.y) {}
+  __device__ __forceinline__ float2 raw() const { return make_float2(hi, lo); }
   __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+  __device__ __forceinline__ bool positive() const { return hi > 0.0f; }
 };
-__device__ __forceinline__ void add(Pair& a, Pair x) {
-  const float s = a.hi + x.hi, b = s - a.hi;
-  a.lo += ((a.hi - (s - b)) + (x.hi - b)) + x.lo;
-  a.hi = s;
+__device__ __forceinline__ Pair norm(Pair x) {  // |lo| at most half of hi's last place
+  const float s = __fadd_rn(x.hi, x.lo);
+  return {s, __fsub_rn(x.lo, __fsub_rn(s, x.hi))};
 }
-// max(p - S q, 0), S = sh + sl.
-__device__ __forceinline__ Pair residual(float p, float q, float sh, float sl) {
-  const float h = sh * q, e = fmaf(sl, q, fmaf(sh, q, -h));
-  const float d = p - h, b = d - p;
-  const float lo = ((p - (d - b)) - (h + b)) - e;
-  const float hi = d + lo;
-  if (!(hi > 0.0f)) return {0.0f, 0.0f};
-  return {hi, lo - (hi - d)};
+__device__ __forceinline__ Pair operator+(Pair a, Pair x) {
+  const float s = __fadd_rn(a.hi, x.hi), b = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, b)), __fsub_rn(x.hi, b));
+  return norm({s, __fadd_rn(__fadd_rn(a.lo, x.lo), e)});
 }
+__device__ __forceinline__ Pair operator*(float u, Pair x) {
+  const float h = __fmul_rn(u, x.hi);
+  return norm({h, fmaf(u, x.lo, fmaf(u, x.hi, -h))});
+}
+__device__ __forceinline__ bool operator>(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ Pair shfl(Pair x, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
+}
+__device__ __forceinline__ Pair shfl_up(Pair x, int by) {
+  return {__shfl_up_sync(0xFFFFFFFFu, x.hi, by), __shfl_up_sync(0xFFFFFFFFu, x.lo, by)};
+}
+// A warp's inclusive sums of x over its lanes.
+__device__ __forceinline__ Pair scan(Pair x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair y = shfl_up(x, o);
+    if (static_cast<int>(lane_id()) >= o) x = y + x;
+  }
+  return x;
+}
+
+// Two elements at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, both(-1.0f), a); }  // (one rounding)
+
+__device__ __forceinline__ float2 max2(float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y)); }
+
+struct Pair2 {
+  float2 hi, lo;
+};
+// Which residual: the probabilities themselves (S = 0), after a first refusal (S = 1), or after more.
+enum Kind : int { kAll, kFirst, kMore };
+__device__ __forceinline__ Kind kind_of(Pair S) { return S.hi == 0.0f ? kAll : S.hi == 1.0f && S.lo == 0.0f ? kFirst : kMore; }
+// max(p - S q, 0) of two elements.  With h = S q rounded, m = max(p, h) and d = m - h rounded, what d leaves
+// is (m - d) - h, exactly, as m >= h.  (An element with p = h counts as 0, though S q may lie 2^-25 of it off.)
+template <int kKind>
+__device__ __forceinline__ Pair2 residual(float2 p, float2 q, Pair S) {
+  if (kKind == kAll) return {p, both(0.0f)};
+  const float2 h = kKind == kFirst ? q : mul2(both(S.hi), q), m = max2(p, h), d = sub2(m, h);
+  float2 lo = sub2(sub2(m, d), h);
+  if (kKind == kMore) {
+    const float2 e = fma2(both(-S.lo), q, fma2(both(-S.hi), q, h));  // h - S q
+    lo = add2(lo, make_float2(d.x > 0.0f ? e.x : 0.0f, d.y > 0.0f ? e.y : 0.0f));
+  }
+  return {d, lo};
+}
+__device__ __forceinline__ Pair2 residual(float2 p, float2 q, Pair S) {
+  const Kind k = kind_of(S);
+  return k == kAll ? residual<kAll>(p, q, S) : k == kFirst ? residual<kFirst>(p, q, S) : residual<kMore>(p, q, S);
+}
+
+// A sum of nonnegative values.  It starts at kFrom, so that the sum is never below a value of at most kFrom
+// and what an addition rounds off comes out of two more (of any value: five).
+struct Sum {
+  static constexpr float kFrom = 1.0f / 64.0f;
+  Pair2 x{both(kFrom), both(0.0f)};
+  template <bool kSmall>  // values of at most kFrom
+  __device__ __forceinline__ void add(const Pair2& v) {
+    const float2 s = add2(x.hi, v.hi), b = sub2(s, x.hi);
+    const float2 e = kSmall ? sub2(v.hi, b) : add2(sub2(x.hi, sub2(s, b)), sub2(v.hi, b));
+    x.lo = add2(add2(x.lo, v.lo), e);
+    x.hi = s;
+  }
+  __device__ __forceinline__ Pair total() const {
+    return Pair{__fsub_rn(x.hi.x, kFrom), x.lo.x} + Pair{__fsub_rn(x.hi.y, kFrom), x.lo.y};
+  }
+};
 
 // A probability as it counts: NaN as 0, and within [0, 1].
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
@@ -117,17 +210,25 @@ struct Vec {
         c[i * 4 / kN] |= static_cast<uint32_t>(__ldg(static_cast<const Word*>(row) + v + i)) << (kN == 4 ? 0 : 16 * (i & 1));
     w = make_uint4(c[0], c[1], c[2], c[3]);
   }
-  __device__ __forceinline__ void values(float (&x)[kN]) const {
-    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kType == kProbF32) {
-        x[i] = prob(__uint_as_float(c[i]));
-      } else {
-        const float2 f = kv8::unpack16<kType == kProbBf16>(c[i]);
-        x[2 * i] = prob(f.x), x[2 * i + 1] = prob(f.y);
-      }
+  // The largest value's bits: a probability's are at most kOne; negative values' and NaN's are more.
+  __device__ __forceinline__ uint32_t most() const {
+    if constexpr (kType == kProbF32) {
+      return max(max(w.x, w.y), max(w.z, w.w));
+    } else {
+      const uint32_t m = __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
+      return max(m >> 16, m & 0xFFFFu);
     }
+  }
+  // Bits of 1 and of Sum::kFrom = 2^-6.
+  static constexpr uint32_t kOne = kType == kProbF32 ? 0x3F800000u : kType == kProbBf16 ? 0x3F80u : 0x3C00u;
+  static constexpr uint32_t kFrom = kType == kProbF32 ? 0x3C800000u : kType == kProbBf16 ? 0x3C80u : 0x2400u;
+  // Elements 2i and 2i + 1, as they count if kClamp.
+  template <bool kClamp>
+  __device__ __forceinline__ float2 values(int i) const {
+    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+    const float2 f = kType == kProbF32 ? make_float2(__uint_as_float(c[2 * i & 3]), __uint_as_float(c[(2 * i + 1) & 3]))
+                                       : kv8::unpack16<kType == kProbBf16>(c[i & 3]);
+    return kClamp ? make_float2(prob(f.x), prob(f.y)) : f;
   }
 };
 
@@ -139,148 +240,232 @@ struct Share {
   const typename Vec<kType>::Word* draft;   // null where S is 0
   int V;
   int v0, v1;  // vectors start at 16-byte boundaries, so the first may lie before 0, and the last past V
-  float sh, sl;  // S
-  const int* refused;
-  int refusals;  // tokens to be taken out; 0 if none lies in the share
+  Pair S;
+  const int* refused;  // tokens to be taken out
+  int refusals;
+  int mine;  // the lane's of them, if they are at most 32
 
   __device__ __forceinline__ Share(const VerifyParams& p, int b, const Command& c, const int* list, int warp, int warps)
-      : V(p.V), refused(list) {
+      : V(p.V), S(c.S), refused(list) {
     const int64_t row = (static_cast<int64_t>(b) * p.n + c.node) * V;
     target = static_cast<const typename Vec<kType>::Word*>(p.target) + row;
     const int before = static_cast<int>(row & (kN - 1));  // elements past a 16-byte boundary
     const int tiles = (V + before + kTile - 1) / kTile, per = (tiles + warps - 1) / warps;
     v0 = min(warp * per, tiles) * kTile - before;
     v1 = min((warp + 1) * per, tiles) * kTile - before;
-    sh = static_cast<float>(c.S);
-    sl = static_cast<float>(c.S - static_cast<double>(sh));
-    draft = kDrawn && sh != 0.0f ? static_cast<const typename Vec<kType>::Word*>(p.draft) + row : nullptr;
-    refusals = 0;
-    if constexpr (!kDrawn) {
-      bool here = false;
-      for (int i = lane_id(); i < c.refused; i += 32) here |= list[i] >= v0 && list[i] < v1;
-      if (__any_sync(0xFFFFFFFFu, here)) refusals = c.refused;
-    }
+    draft = kDrawn && S.hi != 0.0f ? static_cast<const typename Vec<kType>::Word*>(p.draft) + row : nullptr;
+    refusals = kDrawn ? 0 : c.refused;
+    mine = static_cast<int>(lane_id()) < refusals ? list[lane_id()] : -1;
   }
   __device__ __forceinline__ bool inside(int v, int tiles) const { return v >= 0 && v + tiles * kTile <= V; }
   // The vectors at v: of a tile inside the row, and of one that reaches past its ends.
+  template <bool kBoth>
   __device__ __forceinline__ void load(int v, Vec<kType>& t, Vec<kType>& q) const {
     t.load(target, v);
     q.w = make_uint4(0u, 0u, 0u, 0u);
-    if (kDrawn && draft) q.load(draft, v);
+    if (kBoth) q.load(draft, v);
   }
+  template <bool kBoth>
   __device__ __forceinline__ void load_edge(int v, Vec<kType>& t, Vec<kType>& q) const {
     t.load_edge(target, v, V);
     q.w = make_uint4(0u, 0u, 0u, 0u);
-    if (kDrawn && draft) q.load_edge(draft, v, V);
+    if (kBoth) q.load_edge(draft, v, V);
   }
-  // The residuals of the vectors at v.
-  __device__ __forceinline__ void terms(int v, const Vec<kType>& t, const Vec<kType>& q, Pair (&r)[kN]) const {
-    float x[kN], y[kN];
-    t.values(x);
-    if (kDrawn) q.values(y);
+  // The residuals of the vectors at v, whatever they hold.
+  __device__ __forceinline__ void terms(int v, const Vec<kType>& t, const Vec<kType>& q, Pair2 (&r)[kN / 2]) const {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) r[i] = kDrawn ? residual(x[i], y[i], sh, sl) : Pair{x[i], 0.0f};
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 p = t.template values<true>(i);
+      r[i] = kDrawn ? residual(p, q.template values<true>(i), S) : Pair2{p, both(0.0f)};
+    }
     if constexpr (!kDrawn) {
       for (int k = 0; k < refusals; ++k) {
         const int at = refused[k] - v;
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (at == i) r[i].hi = 0.0f;
+        for (int i = 0; i < kN / 2; ++i) {
+          if (at == 2 * i) r[i].hi.x = 0.0f;
+          if (at == 2 * i + 1) r[i].hi.y = 0.0f;
+        }
       }
     }
   }
+  // Adds them to a sum, by the whole warp, for the tile at v0: most tiles hold nothing but small
+  // probabilities, and no refused token.
+  template <int kKind>
+  __device__ __forceinline__ void add_to(Sum& sum, int v0, const Vec<kType>& t, const Vec<kType>& q) const {
+    const int v = v0 + static_cast<int>(lane_id()) * kN;
+    bool odd = t.most() > Vec<kType>::kFrom || (kKind != kAll && q.most() > Vec<kType>::kOne);
+    if (!kDrawn) odd |= refusals > 32 || (mine >= v0 && mine < v0 + kTile);
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, odd), 0)) {
+      Pair2 r[kN / 2];
+      terms(v, t, q, r);
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) sum.template add<false>(r[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i)
+      sum.template add<true>(residual<kKind>(t.template values<false>(i), q.template values<false>(i), S));
+  }
 };
 
-// A warp's inclusive sums of x over its lanes.
-__device__ __forceinline__ double scan(double x) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (static_cast<int>(lane_id()) >= o) x += y;
-  }
-  return x;
-}
-
-// The mass of the warp's share.
-template <int kType, bool kDrawn>
-__device__ __forceinline__ double share_mass(const Share<kType, kDrawn>& s) {
+// The mass of the warp's share (in lane 31).
+template <int kKind, int kType, bool kDrawn>
+__device__ __forceinline__ Pair share_mass_of(const Share<kType, kDrawn>& s) {
   using S = Share<kType, kDrawn>;
-  constexpr int kAhead = 4;  // tiles whose loads are in flight together
+  constexpr int kAhead = kKind == kAll ? 4 : 2;  // tiles whose loads are in flight together
   const int mine = static_cast<int>(lane_id()) * S::kN;
-  Pair sum{0.0f, 0.0f};
-  auto take = [&](int v, const Vec<kType>& t, const Vec<kType>& q) {
-    Pair r[S::kN];
-    s.terms(v, t, q, r);
-#pragma unroll
-    for (int i = 0; i < S::kN; ++i) add(sum, r[i]);
-  };
+  Sum sum;
   for (int v = s.v0; v < s.v1;) {
     Vec<kType> t[kAhead], q[kAhead];
     if (v + kAhead * S::kTile <= s.v1 && s.inside(v, kAhead)) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) s.load(v + i * S::kTile + mine, t[i], q[i]);
+      for (int i = 0; i < kAhead; ++i) s.template load<kKind != kAll>(v + i * S::kTile + mine, t[i], q[i]);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) take(v + i * S::kTile + mine, t[i], q[i]);
+      for (int i = 0; i < kAhead; ++i) s.template add_to<kKind>(sum, v + i * S::kTile, t[i], q[i]);
       v += kAhead * S::kTile;
     } else {
       if (s.inside(v, 1)) {
-        s.load(v + mine, t[0], q[0]);
+        s.template load<kKind != kAll>(v + mine, t[0], q[0]);
       } else {
-        s.load_edge(v + mine, t[0], q[0]);
+        s.template load_edge<kKind != kAll>(v + mine, t[0], q[0]);
       }
-      take(v + mine, t[0], q[0]);
+      s.template add_to<kKind>(sum, v, t[0], q[0]);
       v += S::kTile;
     }
   }
-  double x = sum.value();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-  return x;
+  return scan(sum.total());
+}
+template <int kType, bool kDrawn>
+__device__ __forceinline__ Pair share_mass(const Share<kType, kDrawn>& s) {
+  if constexpr (kDrawn) {
+    const Kind k = kind_of(s.S);
+    if (k == kFirst) return share_mass_of<kFirst>(s);
+    if (k == kMore) return share_mass_of<kMore>(s);
+  }
+  return share_mass_of<kAll>(s);
 }
 
-// The least token of the share whose cumulative residual, `below` before the share, passes goal; by
-// roundings at the share's end there may be none, and the last with any residual is it.
-template <int kType, bool kDrawn>
-__device__ __forceinline__ int share_find(const Share<kType, kDrawn>& s, double goal, double below) {
-  using S = Share<kType, kDrawn>;
-  int last = -1;
-  for (int v0 = s.v0; v0 < s.v1; v0 += S::kTile) {
-    const int v = v0 + static_cast<int>(lane_id()) * S::kN;
-    Vec<kType> t, q;
-    Pair r[S::kN];
-    if (s.inside(v0, 1)) {
-      s.load(v, t, q);
-    } else {
-      s.load_edge(v, t, q);
-    }
-    s.terms(v, t, q, r);
-    double x = 0.0;
+// The sum of the shares' masses, 4 to a lane: up to each lane, and before each of its four.
+struct Masses {
+  Pair m[4], upto, before;
+  __device__ __forceinline__ Masses(const float2* mass, int warps) {
+    const int lane = lane_id();
+    Pair x;
 #pragma unroll
-    for (int i = 0; i < S::kN; ++i) {
-      x += r[i].value();
-      if (r[i].hi > 0.0f) last = v + i;
+    for (int k = 0; k < 4; ++k) {
+      if (4 * lane + k < warps) m[k] = Pair(mass[4 * lane + k]);
+      x = x + m[k];
     }
-    const double upto = below + scan(x);
-    // (x > 0: a lane's sum may pass its neighbour's by roundings alone.)
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, x > 0.0 && upto > goal);
-    if (past) {
-      double cum = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
-      if (lane_id() == 0) cum = below;
+    upto = scan(x);
+    before = shfl_up(upto, 1);
+    if (lane == 0) before = Pair();
+  }
+  __device__ __forceinline__ Pair total() const { return shfl(upto, 31); }
+  // The share in which the cumulative sum passes goal, and the sum before it (by one warp).  By roundings
+  // it may pass in none: then the last share with any mass.
+  __device__ __forceinline__ int find(Pair goal, Pair& below) const {
+    bool some = false, passed = false;
+    int mine = 0;
+    Pair cum = before, at = before;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!passed && m[k].positive()) {
+        some = true;
+        mine = 4 * static_cast<int>(lane_id()) + k;
+        at = cum;
+        passed = cum + m[k] > goal;
+      }
+      cum = cum + m[k];
+    }
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, some), past = __ballot_sync(0xFFFFFFFFu, passed);
+    const int lane = past ? __ffs(past) - 1 : any ? 31 - __clz(static_cast<int>(any)) : 0;
+    below = shfl(at, lane);
+    return __shfl_sync(0xFFFFFFFFu, mine, lane);
+  }
+};
+
+// The token of that share: the least whose cumulative sum passes goal, or the share's last with any
+// residual where by roundings none does.  Executed by all warps of a CTA, a tile each; the one that has
+// the token writes it.
+template <int kType, bool kDrawn>
+__device__ __forceinline__ void find_token(const Share<kType, kDrawn>& s, Shared& sh, int32_t* token) {
+  using S = Share<kType, kDrawn>;
+  const int lane = lane_id(), warp = warp_id();
+  const Pair goal(sh.goal);
+  Pair below(sh.below);
+  int last = s.v0;  // the last tile with any residual
+  for (int g = s.v0;; g += kWarps * S::kTile) {
+    const bool over = g >= s.v1;  // past the share: its last token, from one tile that all warps look at
+    const int v0 = over ? last : g + warp * S::kTile, v = v0 + lane * S::kN;
+    Pair2 r[S::kN / 2];
+    Pair x;
+#pragma unroll
+    for (int i = 0; i < S::kN / 2; ++i) r[i] = {both(0.0f), both(0.0f)};
+    if (v0 < s.v1) {
+      Vec<kType> t, q;
+      const bool two = kDrawn && s.draft;
+      if (s.inside(v0, 1)) {
+        two ? s.template load<true>(v, t, q) : s.template load<false>(v, t, q);
+      } else {
+        two ? s.template load_edge<true>(v, t, q) : s.template load_edge<false>(v, t, q);
+      }
+      s.terms(v, t, q, r);
+      Sum sum;
+#pragma unroll
+      for (int i = 0; i < S::kN / 2; ++i) sum.template add<false>(r[i]);
+      x = sum.total();
+    }
+    const Pair upto = scan(x);
+    if (lane == 31) sh.tile[warp] = upto.raw();
+    __syncthreads();
+    const Pair m = lane < kWarps ? Pair(sh.tile[lane]) : Pair(), cum = below + scan(m);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, m.positive());
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, m.positive() && cum > goal);
+    if (past || over) {
+      const int w = over ? 0 : __ffs(past) - 1;
+      if (warp != w) return;
+      const Pair start = w == 0 ? below : shfl(cum, w - 1), end = start + upto;
+      // (Only lanes with a residual: another's sum may pass its neighbour's by roundings alone.)
+      const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, x.positive());
+      const uint32_t here = __ballot_sync(0xFFFFFFFFu, x.positive() && end > goal);
+      const int at = !over && here ? __ffs(here) - 1 : 31 - __clz(static_cast<int>(lanes));
+      Pair c = shfl_up(end, 1);
+      if (lane == 0) c = start;
       int found = -1;
-      bool done = false;
+      bool passed = false;
 #pragma unroll
       for (int i = 0; i < S::kN; ++i) {
-        cum += r[i].value();
-        if (!done && r[i].hi > 0.0f) {
+        const Pair e = norm(i & 1 ? Pair{r[i / 2].hi.y, r[i / 2].lo.y} : Pair{r[i / 2].hi.x, r[i / 2].lo.x});
+        c = c + e;
+        if (!passed && e.positive()) {
           found = v + i;
-          done = cum > goal;
+          passed = !over && c > goal;
         }
       }
-      return __shfl_sync(0xFFFFFFFFu, found, __ffs(past) - 1);
+      if (lane == at) *token = found;
+      return;
     }
-    below = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (some) last = g + (31 - __clz(static_cast<int>(some))) * S::kTile;
+    below = shfl(cum, 31);
+    __syncthreads();  // sh.tile is read
   }
-  return __reduce_max_sync(0xFFFFFFFFu, last);
+}
+
+// Whether u q W < t, t = max(p - S q, 0) (drawn), or u W < t, t = p (q = 1, S = 0).
+template <bool kDrawn>
+__device__ __forceinline__ bool accepts(float u, float p, float q, Pair S, Pair W) {
+  float right = p;
+  if constexpr (kDrawn) {
+    const Pair2 r = residual(both(p), both(q), S);
+    right = r.hi.x + r.lo.x;
+  }
+  const float left = u * q * W.hi;
+  // Both sides are within 2^-22 of theirs, and t's cancellation within 2^-44 of p.
+  if (fabsf(left - right) > 1e-6f * (fabsf(left) + right) + 1e-12f * p && fabsf(left) + right > 1e-30f)
+    return left < right;
+  const double t = fmax(__dsub_rn(p, __dmul_rn(S.value(), q)), 0.0);
+  return __dmul_rn(__dmul_rn(u, q), W.value()) < t;
 }
 
 template <int kType, bool kDrawn>
@@ -288,167 +473,122 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   __shared__ Shared sh;
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank(), b = blockIdx.x / ranks;
-  const int lane = lane_id(), warp = warp_id();
+  const int lane = lane_id(), warp = warp_id(), warps = ranks * kWarps;
   const Shared* leader = cluster.map_shared_rank(&sh, 0);
-  const int cnt = kv8::seq_count(p.counts, b, p.n);
+  const int64_t nodes = static_cast<int64_t>(b) * p.n;
+  const float u0 = __ldg(p.uniforms + nodes);
+  int cnt = 0;
 
   if (rank == 0) {
-    const int64_t at = static_cast<int64_t>(b) * p.n;
-    bool odd = threadIdx.x == 0 && p.counts && __ldg(p.counts + b) != cnt;
-    for (int i = 1 + static_cast<int>(threadIdx.x); i < cnt; i += kThreads) {
-      int up = __ldg(p.parents + at + i);
-      const int x = __ldg(p.tokens + at + i);
+    uint32_t odd_at = 0, bit = 1;  // of the thread's nodes, those with a token or parent out of range
+    for (int i = threadIdx.x; i < p.n; i += kThreads, bit <<= 1) {
+      int up = __ldg(p.parents + nodes + i);
+      const int x = __ldg(p.tokens + nodes + i);
+      const float u = __ldg(p.uniforms + nodes + i);
       const bool known = up >= 0 && up < i, real = x >= 0 && x < p.V;
-      odd |= !real || up < -1 || up >= i;
-      if (!known) up = -1;  // no node's child: never asked
-      const int64_t v = known && real ? (at + up) * p.V + x : 0;
-      sh.up[i] = up;
+      if (i > 0 && (!real || up < -1 || up >= i)) odd_at |= bit;
+      const int64_t v = known && real ? (nodes + up) * p.V + x : 0;
+      sh.up[i] = known ? up : -1;  // -1: no node's child, never asked
       sh.token[i] = real ? x : -1;
       sh.p[i] = known && real ? load_prob<kType>(p.target, v) : 0.0f;
       sh.q[i] = kDrawn && known && real ? load_prob<kType>(p.draft, v) : 0.0f;
-      sh.u[i] = __ldg(p.uniforms + at + i);
+      sh.u[i] = u;
     }
+    cnt = kv8::seq_count(p.counts, b, p.n);
+    bool odd = threadIdx.x == 0 && p.counts && __ldg(p.counts + b) != cnt;
+    bit = 1;
+    for (int i = threadIdx.x; i < cnt; i += kThreads, bit <<= 1) odd |= (odd_at & bit) != 0;
     if (odd) raise_clamped(p.status);
     __syncthreads();
   }
 
   // The walk, in warp 0 of the first CTA (whose other warps, like the other CTAs', only follow).
   const bool leads = rank == 0 && warp == 0;
-  int node = 0, next = 1, len = 0, refused = 0;
-  double S = 0.0, W = 1.0, total = 0.0;
-  bool summed = false;    // sh.mass holds the shares of the residual at (node, S)
-  bool refusing = false;  // the sum asked for is a refusal's, at S + W
+  int node = 0, next = 1, len = cnt > 0 ? 1 : 0, refused = 0;
+  Pair S, W{1.0f, 0.0f};
+  if (leads && lane == 0 && cnt > 0) p.path[nodes] = 0;
+  // The first child of the node at hand from number `from` on; cnt if there is none.
+  auto child_from = [&](int from) {
+    for (int j0 = from & ~31; j0 < cnt; j0 += 32) {
+      const int j = j0 + lane;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, j >= from && j < cnt && sh.up[j] == node);
+      if (m) return j0 + __ffs(m) - 1;
+    }
+    return cnt;
+  };
+  int child = leads ? child_from(next) : 0;
   Command cmd;
-  if (leads && cnt > 0) {
-    if (lane == 0) p.path[static_cast<int64_t>(b) * p.n] = 0;
-    len = 1;
-  }
   for (;;) {
     if (leads) {
-      cmd = Command{kSum, node, 0, refused, S, 0.0, 0.0};
-      if (cnt == 0) {
-        cmd.op = kDone;
-      } else {
-        bool over = false;  // no child left to ask
-        for (;;) {
-          int child = cnt;
-          for (int j0 = next & ~31; j0 < cnt; j0 += 32) {
-            const int j = j0 + lane;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, j >= next && j < cnt && sh.up[j] == node);
-            if (m) {
-              child = j0 + __ffs(m) - 1;
-              break;
-            }
-          }
-          if (child >= cnt) {
-            over = true;
-            break;
-          }
-          next = child + 1;
-          const double pc = sh.p[child], qc = sh.q[child], u = sh.u[child];
-          double t;
-          bool yes;
-          if constexpr (kDrawn) {
-            t = fmax(__dsub_rn(pc, __dmul_rn(S, qc)), 0.0);
-            yes = __dmul_rn(__dmul_rn(u, qc), W) < t;
-          } else {
-            bool gone = false;
-            for (int k = lane; k < refused; k += 32) gone |= sh.refused[k] == sh.token[child];
-            t = __any_sync(0xFFFFFFFFu, gone) ? 0.0 : pc;
-            yes = __dmul_rn(u, W) < t;
-          }
-          if (yes) {
-            node = child;
-            if (lane == 0) p.path[static_cast<int64_t>(b) * p.n + len] = child;
-            ++len;
-            S = 0.0, W = 1.0, refused = 0, summed = false;
-          } else if constexpr (kDrawn) {
-            refusing = true;
-            break;
-          } else if (t > 0.0) {
-            W = __dsub_rn(W, t);
-            if (lane == 0) sh.refused[refused] = sh.token[child];
-            ++refused;
-            __syncwarp();
-          }
+      bool refusing = false;
+      while (child < cnt && !refusing) {
+        bool gone = false;
+        for (int k = lane; k < refused; k += 32) gone |= sh.refused[k] == sh.token[child];
+        const float pc = !kDrawn && __any_sync(0xFFFFFFFFu, gone) ? 0.0f : sh.p[child];
+        if (accepts<kDrawn>(sh.u[child], pc, kDrawn ? sh.q[child] : 1.0f, S, W)) {
+          node = child;
+          if (lane == 0) p.path[nodes + len] = child;
+          ++len;
+          S = Pair(), W = Pair{1.0f, 0.0f}, refused = 0;
+        } else if constexpr (kDrawn) {
+          refusing = true;
+        } else if (pc > 0.0f) {
+          W = W + Pair{-pc, 0.0f};
+          if (lane == 0) sh.refused[refused] = sh.token[child];
+          ++refused;
+          __syncwarp();
         }
-        cmd.node = node;
-        cmd.refused = refused;
-        cmd.S = refusing ? __dadd_rn(S, W) : S;
-        if (over && summed && !(total > 0.0)) {
-          cmd.op = kDone;
-        } else if (over && summed) {
-          // The token: the warp whose share the drawn number falls in finds it.
-          const int warps = ranks * kWarps;
-          double m[4], x = 0.0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            m[k] = 4 * lane + k < warps ? sh.mass[4 * lane + k] : 0.0;
-            x += m[k];
-          }
-          const double upto = scan(x), goal = __dmul_rn(static_cast<double>(__ldg(p.uniforms + static_cast<int64_t>(b) * p.n)), total);
-          double cum = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
-          if (lane == 0) cum = 0.0;
-          uint32_t past = __ballot_sync(0xFFFFFFFFu, x > 0.0 && upto > goal);
-          // By roundings there may be none: the last with any mass.
-          if (!past) past = 0x80000000u >> __clz(static_cast<int>(__ballot_sync(0xFFFFFFFFu, x > 0.0)));
-          int mine = 0;
-          double below = cum;
-          bool done = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (!done && m[k] > 0.0) {
-              mine = 4 * lane + k;
-              below = cum;
-              done = cum + m[k] > goal;
-            }
-            cum += m[k];
-          }
-          const int from = __ffs(past) - 1;
-          cmd.op = kFind;
-          cmd.warp = __shfl_sync(0xFFFFFFFFu, mine, from);
-          cmd.below = __shfl_sync(0xFFFFFFFFu, below, from);
-          cmd.goal = goal;
-        }
+        child = child_from(child + 1);
       }
+      cmd = Command{cnt == 0, refusing, child >= cnt, node, refused, (refusing ? S + W : S).raw()};
       if (lane < ranks) cluster.map_shared_rank(&sh, lane)->cmd = cmd;
     }
     cluster.sync();
     cmd = sh.cmd;
-    if (cmd.op == kDone) break;
-    const Share<kType, kDrawn> share(p, b, cmd, leader->refused, rank * kWarps + warp, ranks * kWarps);
-    if (cmd.op == kFind) {
-      if (cmd.warp == rank * kWarps + warp) {
-        const int token = share_find(share, cmd.goal, cmd.below);
-        if (lane == 0) p.next_token[b] = token;
-      }
-      break;
+    if (cmd.done) break;
+    if (!kDrawn && rank > 0 && cmd.refused > 0) {
+      for (int i = threadIdx.x; i < cmd.refused; i += kThreads) sh.refused[i] = leader->refused[i];
+      __syncthreads();
     }
-    const double mass = share_mass(share);
-    if (lane == 0) cluster.map_shared_rank(&sh, 0)->mass[rank * kWarps + warp] = mass;
+    {
+      const Share<kType, kDrawn> share(p, b, cmd, sh.refused, rank * kWarps + warp, warps);
+      const float2 mass = shfl(share_mass(share), 31).raw();
+      if (cmd.last ? lane < ranks : lane == 0)
+        cluster.map_shared_rank(&sh, lane)->mass[rank * kWarps + warp] = mass;
+    }
     cluster.sync();
-    if (leads) {
-      double x = 0.0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x += 4 * lane + k < ranks * kWarps ? sh.mass[4 * lane + k] : 0.0;
-      const double sum = __shfl_sync(0xFFFFFFFFu, scan(x), 31);
-      summed = true;
-      if (!refusing) {
-        total = sum;
-      } else if (sum > 0.0) {
-        S = cmd.S;
-        W = total = sum;
-      } else {
-        summed = false;  // a refusal that would leave nothing leaves the residual as it was
+    if (cmd.last) {  // every CTA finds the share, and the one that has it the token
+      if (warp == 0) {
+        const Masses all(sh.mass, warps);
+        const Pair total = all.total(), goal = u0 * total;
+        Pair below;
+        const int from = all.find(goal, below);
+        if (lane == 0) sh.goal = goal.raw(), sh.below = below.raw(), sh.from = total.positive() ? from : -1;
       }
-      refusing = false;
+      __syncthreads();
+      if (sh.from >= 0) {
+        if (sh.from / kWarps == rank) {
+          const Share<kType, kDrawn> share(p, b, cmd, sh.refused, sh.from, warps);
+          find_token(share, sh, p.next_token + b);
+        }
+        break;
+      }
+      if (!cmd.refusing) break;  // no residual at all
+      continue;                  // the refusal leaves nothing, and so the residual as it was
+    }
+    if (leads) {
+      const Pair mass = Masses(sh.mass, warps).total();
+      if (mass.positive()) {
+        S = Pair(cmd.S);
+        W = mass;
+      }
     }
   }
   if (leads) {
-    for (int i = len + lane; i < p.n; i += 32) p.path[static_cast<int64_t>(b) * p.n + i] = -1;
+    for (int i = len + lane; i < p.n; i += 32) p.path[nodes + i] = -1;
     if (lane == 0) {
       p.accepted[b] = len;
-      if (cmd.op == kDone) {
+      if (cmd.done || sh.from < 0) {
         p.next_token[b] = -1;
         if (cnt > 0) raise_empty_row(p.status);
       }
@@ -461,10 +601,11 @@ template <int kType, bool kDrawn>
 cudaError_t launch(const DraftVerifyArgs& a, cudaStream_t s) {
   VerifyParams p{a.n, a.V, a.target, a.draft, a.tokens, a.parents, a.counts, a.uniforms, a.path, a.accepted,
                  a.next_token, a.status};
-  // CTAs of a cluster: doubled while each warp has more than two tiles of the vocabulary.
+  // CTAs of a cluster: doubled while each warp has more than two tiles of the vocabulary, and all
+  // clusters are on the device at once.
   const int tiles = (a.V + Share<kType, kDrawn>::kTile - 1) / Share<kType, kDrawn>::kTile;
   int ranks = 1;
-  while (ranks < kMostRanks && tiles > 2 * ranks * kWarps) ranks *= 2;
+  while (ranks < kMostRanks && tiles > 2 * ranks * kWarps && ranks * static_cast<int64_t>(a.B) <= a.sms) ranks *= 2;
   void* args[] = {&p};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
