@@ -613,12 +613,20 @@ def attn_draft_verify(target, draft, tokens, parents, uniforms, counts=None, pat
                       (tokens, i32, (B, n), "tokens"), (parents, i32, (B, n), "parents"),
                       (counts, i32, (B,), "counts"), (uniforms, torch.float32, (B, n), "uniforms"))
     with _On(dev, stream) as s:
-        path = torch.empty((B, n), dtype=i32, device=dev) if path is None else path
-        accepted = torch.empty((B,), dtype=i32, device=dev) if accepted is None else accepted
-        next_token = torch.empty((B,), dtype=i32, device=dev) if next_token is None else next_token
-        outs = _kv8_check(dev, (path, i32, (B, n), "path"), (accepted, i32, (B,), "accepted"),
-                          (next_token, i32, (B,), "next_token"))
-        _check(load().attn_draft_verify(DTYPE_CODE[dt], B, n, V, *ptrs, *outs, s))
+        if path is None:
+            path = torch.empty_like(parents)
+        else:
+            _kv8_check(dev, (path, i32, (B, n), "path"))
+        if accepted is None:
+            accepted = torch.empty((B,), dtype=i32, device=dev)
+        else:
+            _kv8_check(dev, (accepted, i32, (B,), "accepted"))
+        if next_token is None:
+            next_token = torch.empty((B,), dtype=i32, device=dev)
+        else:
+            _kv8_check(dev, (next_token, i32, (B,), "next_token"))
+        _check(load().attn_draft_verify(DTYPE_CODE[dt], B, n, V, *ptrs, path.data_ptr(),
+                                        accepted.data_ptr(), next_token.data_ptr(), s))
     return path, accepted, next_token
 
 
@@ -642,7 +650,7 @@ def attn_kv8_keep(k8, v8, k_scales, v_scales, lengths, path, accepted, counts=No
                       (weights, f32, (B, Hk, cap), "weights"))
     with _On(dev, stream) as s:
         if lengths_out is None:
-            lengths_out = torch.empty((B,), dtype=i32, device=dev)
+            lengths_out = torch.empty_like(lengths)
         else:
             _kv8_check(dev, (lengths_out, i32, (B,), "lengths_out"))
         _check(load().attn_kv8_keep(B, Hk, n, d, cap, block, *ptrs, lengths_out.data_ptr(), s))

@@ -1,4 +1,6 @@
 // Attention over the 8-bit cache: which kernel a call takes, and the work its CTAs are given.
+#include <type_traits>
+
 #include "kv8_attend.cuh"
 
 namespace ea {
@@ -74,10 +76,11 @@ namespace {
 template <bool kTree>
 cudaError_t dispatch(const Kv8Args& a, bool many, cudaStream_t s) {
   if (many) {
-    auto p = attend_params<kv8::ByHead>(a, a.sms, 2);
+    using Geo = std::conditional_t<kTree, kv8::ByNode, kv8::ByHead>;
+    auto p = attend_params<Geo>(a, a.sms, 2);
     if (a.bf16)
-      return a.d == 128 ? launch_kv8_tc<true, 128, kTree>(p, s) : launch_kv8_tc<true, 64, kTree>(p, s);
-    return a.d == 128 ? launch_kv8_tc<false, 128, kTree>(p, s) : launch_kv8_tc<false, 64, kTree>(p, s);
+      return a.d == 128 ? launch_kv8_tc<true, 128>(p, s) : launch_kv8_tc<true, 64>(p, s);
+    return a.d == 128 ? launch_kv8_tc<false, 128>(p, s) : launch_kv8_tc<false, 64>(p, s);
   }
   const auto p = attend_params<kv8::ByQuery>(a, kv8::kMostCtas * a.sms, 2 * kv8::kAttendWarps);
   if (a.bf16)

@@ -120,17 +120,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
   pl.hk = id % geo.Hk;
   pl.b = id / geo.Hk;
   const int lane = lane_id();
-  const int row = blockIdx.y * kJoinWarps + warp_id(), r = pl.rt * geo.tile + row;
+  int row = blockIdx.y * kJoinWarps + warp_id();
+  const int r = pl.rt * geo.tile + row;  // as the rows lie in memory
   const int len = seq_len(geo.lengths, pl.b, geo.cap), cnt = seq_count(geo.counts, pl.b, geo.n);
   if (pl.rt == 0 && pl.hk == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     check_seq(geo.lengths, geo.counts, pl.b, geo.cap, geo.n, p.status);
-  pl.keys = tile_keys(geo, len, cnt, pl.rt);
+  int tile_id = blockIdx.x;
+  if constexpr (Geo::kPacked) {  // its tile, and its row there, are those of its place among the real rows
+    const int i = r % geo.n, at = r / geo.n * cnt + i;
+    pl.keys = 0;
+    if (r < geo.R && i < cnt) {
+      tile_id += at / geo.tile - pl.rt;
+      row = at % geo.tile;
+      pl.keys = len;
+    }
+  } else {
+    pl.keys = tile_keys(geo, len, cnt, pl.rt);
+  }
   grid_dependency_wait();  // by every warp: what follows on the stream may rely on this kernel
   int first = 0, last = 0;
   if (pl.keys > 0) {
     // Kept inside the parts even if the lengths changed since the first kernel read them (which
     // leaves the result undefined, but not the addresses).
-    const int2 run = p.runs[blockIdx.x];
+    const int2 run = p.runs[tile_id];
     first = min(max(run.x, 0), p.ctas - 1);
     last = min(max(run.y, first), p.ctas - 1);
   }
@@ -181,8 +193,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     out.w = __shfl_down_sync(0xFFFFFFFFu, z[1], 1);
     if (lane & 1) return;
   }
-  write_out<kBf16, D, Geo>(p, geo.row_offset(pl.b, pl.hk, r), lane * kCols, out, l, mx,
-                      geo.query(r) < cnt);
+  if constexpr (Geo::kPacked) {
+    write_out<kBf16, D, Geo>(p, (static_cast<int64_t>(pl.b) * geo.Hk + pl.hk) * geo.R + r, lane * kCols, out, l, mx,
+                             r % geo.n < cnt);
+  } else {
+    write_out<kBf16, D, Geo>(p, geo.row_offset(pl.b, pl.hk, r), lane * kCols, out, l, mx, geo.query(r) < cnt);
+  }
 }
 
 template <bool kBf16, int D, class Geo>
@@ -199,8 +215,8 @@ cudaError_t launch_join(AttendParams<Geo>& p, cudaStream_t s) {
 // Attention of many rows on the tcgen05 tensor cores (kv8_tc_*.cu), in tiles of 256 rows, or of 128
 // where a head has no more.
 constexpr int kTcTileRows = 256;
-template <bool kBf16, int D, bool kTree>
-cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s);
+template <bool kBf16, int D, class Geo>
+cudaError_t launch_kv8_tc(kv8::AttendParams<Geo>& p, cudaStream_t s);
 // Of few rows (kv8_attend_few.cuh), in tiles of 8, 16 or 32.
 template <bool kBf16, int D, bool kTree>
 cudaError_t launch_kv8_few(const kv8::AttendParams<kv8::ByQuery>& p, int sms, cudaStream_t s);

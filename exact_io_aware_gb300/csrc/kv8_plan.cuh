@@ -24,6 +24,7 @@ struct Geometry {
 // a head's.
 struct ByQuery : Geometry {
   static constexpr int kStep = kChunk;
+  static constexpr bool kPacked = false;
   __device__ __forceinline__ int query(int r) const { return r / G; }
   // Row of q and o, [B][Hk G][n][D].
   __device__ __forceinline__ int64_t row_offset(int b, int hk, int r) const {
@@ -40,7 +41,11 @@ struct ByQuery : Geometry {
 // Rows ordered as they lie in memory: row r is query r % n of head r / n.
 struct ByHead : Geometry {
   static constexpr int kStep = kBlockKeys;
+  static constexpr bool kPacked = false;
+  __device__ __forceinline__ int rows(int) const { return R; }
   __device__ __forceinline__ int query(int r) const { return r % n; }
+  __device__ __forceinline__ int query(int r, int) const { return query(r); }
+  __device__ __forceinline__ int64_t row_offset(int b, int hk, int r, int) const { return row_offset(b, hk, r); }
   __device__ __forceinline__ int64_t row_offset(int b, int hk, int r) const {
     return (static_cast<int64_t>(b) * Hk + hk) * R + r;
   }
@@ -51,6 +56,24 @@ struct ByHead : Geometry {
     lo = wraps ? 0 : a;
     hi = wraps ? (r1 - r0 >= n || a < cnt ? cnt - 1 : min(z, cnt - 1)) : min(z, cnt - 1);
     return lo < cnt && hi >= lo;
+  }
+};
+
+// Real rows alone, in the order they lie in memory: row r is query r % cnt of head r / cnt.  For a tree's
+// rows, which all see every tile's keys up to the sequence's end: padding would cost what real rows do
+// (4 x 8 heads of four times 128 to 256 rows over 16384 keys, d = 64: TREE_PAD).
+struct ByNode : Geometry {
+  static constexpr int kStep = kBlockKeys;
+  static constexpr bool kPacked = true;
+  __device__ __forceinline__ int rows(int cnt) const { return G * cnt; }
+  __device__ __forceinline__ int query(int r, int cnt) const { return r % cnt; }
+  __device__ __forceinline__ int64_t row_offset(int b, int hk, int r, int cnt) const {
+    return (static_cast<int64_t>(b) * Hk * G + static_cast<int64_t>(hk) * G + r / cnt) * n + r % cnt;
+  }
+  __device__ __forceinline__ bool span(int r0, int, int cnt, int& lo, int& hi) const {
+    lo = 0;
+    hi = cnt - 1;
+    return r0 < G * cnt;
   }
 };
 

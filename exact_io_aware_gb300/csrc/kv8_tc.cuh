@@ -118,8 +118,8 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-template <bool kTree>
-__device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int u0, int u1, int cta) {
+template <class Geo>
+__device__ __forceinline__ Seg segment(const Geo& g, const Place& pl, int u0, int u1, int cta) {
   Seg s;
   s.b = pl.b, s.hk = pl.hk;
   s.len = seq_len(g.lengths, pl.b, g.cap);
@@ -138,7 +138,7 @@ __device__ __forceinline__ Seg segment(const ByHead& g, const Place& pl, int u0,
     int lo, hi;
     const bool any = a < g.R && g.span(a, z, s.cnt, lo, hi);
     s.reach[t] = any ? chunks_of(g, query_keys(g, s.len, s.cnt, hi)) : 0;
-    s.least[t] = !any ? s.len : kTree ? max(s.len - s.cnt, 0) : query_keys(g, s.len, s.cnt, lo);
+    s.least[t] = !any ? s.len : Geo::kPacked ? max(s.len - s.cnt, 0) : query_keys(g, s.len, s.cnt, lo);
   }
   return s;
 }
@@ -213,7 +213,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // A row's largest x of a block, from its raw scores: their factor is uniform and not negative in a
-// scale group.  kG: groups of a block that differ (1 where the cache's blocks are of 128 tokens).
+// scale group.  kG: groups of a block that differ (1 where the cache's blocks are of 128 tokens); the
+// scales have one entry for each 16 keys.
 template <int kG>
 __device__ __forceinline__ float block_max(const float (&sv)[kBlockKeys], const Scales& sc, float mul) {
   constexpr int kW = kBlockKeys / kG;
@@ -226,7 +227,7 @@ __device__ __forceinline__ float block_max(const float (&sv)[kBlockKeys], const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) a[e] = fmax3(a[e], sv[kW * g + k + 2 * e], sv[kW * g + k + 2 * e + 1]);
     const float t = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
-    mx = fmaxf(mx, fmaf(t, fmaxf(sc.k[g] * mul, kLeastFactor), sc.log2_v[g]));
+    mx = fmaxf(mx, fmaf(t, fmaxf(sc.k[g * (kGroups / kG)] * mul, kLeastFactor), sc.log2_v[g * (kGroups / kG)]));
   }
   return mx;
 }
@@ -239,6 +240,7 @@ template <int kG, bool kPair>
 __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], const Scales& sc, float mul, float m,
                                              uint32_t tS) {
   constexpr int kW = kBlockKeys / kG;
+  constexpr int kRun = kG == 1 ? kBlockKeys : 16;  // keys of a partial sum: the same for every kG but 1
   float l = 0.0f;
   float2 sum[2];
 #pragma unroll
@@ -246,9 +248,9 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
     uint32_t pk[16], low[kPair ? 16 : 1];
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      const int key = c0 + k, g = key / kW;
+      const int key = c0 + k, g = key / kW * (kGroups / kG);
       const float f = fmaxf(sc.k[g] * mul, kLeastFactor), shift = sc.log2_v[g] - m;
-      if (key % kW == 0) sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+      if (key % kRun == 0) sum[0] = sum[1] = make_float2(0.0f, 0.0f);
       const float2 x = fma2(make_float2(sv[key], sv[key + 1]), make_float2(f, f), make_float2(shift, shift));
       const float2 pr = make_float2(ex2(x.x), ex2(x.y));
       sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pr);
@@ -257,7 +259,7 @@ __device__ __forceinline__ float block_probs(const float (&sv)[kBlockKeys], cons
         const float2 hi = unpack16<false>(pk[k / 2]);
         low[k / 2] = pack2<false>(pr.x - hi.x, pr.y - hi.y);
       }
-      if ((key + 2) % kW == 0) {
+      if ((key + 2) % kRun == 0) {
         const float2 s = add2(sum[0], sum[1]);
         l = fmaf(s.x + s.y, sc.inv_v[g], l);
       }
@@ -279,14 +281,14 @@ __device__ __forceinline__ void shift_far(float (&sv)[kBlockKeys], const Scales&
   }
 }
 
-// The queries of a tile (rows of q from `q` on, `rows` of them; the tile's others are zeros) as
+// The queries of a tile (row r at src(r), the first `rows` of them; the tile's others are zeros) as
 // 8-bit terms (the first E4M3, the others E5M2), by kN threads (tid): D / 16 lanes a row.  Row r's
 // terms go to the tiles of row tile r / 128 and its factor, c2 times the power of two taken out, to
 // row_mul[r].  The loop stays rolled: unrolled, fetching its instructions once a tile took longer than
 // running them.
-template <bool kBf16, int D, int kN>
-__device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, const uint16_t* q, int rows,
-                                            int tile, float c2, int tid) {
+template <bool kBf16, int D, int kN, class Src>
+__device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, Src&& src_of, int rows, int tile,
+                                            float c2, int tid) {
   using C = Config<kBf16, D>;
   using T8 = typename C::T8;
   constexpr int kLanes = D / 16;
@@ -295,7 +297,7 @@ __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, cons
     const int row = idx / kLanes, piece = idx % kLanes;
     uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (row < rows) {
-      const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(row) * D + piece * 16);
+      const uint4* src = reinterpret_cast<const uint4*>(src_of(row) + piece * 16);
       u[0] = __ldg(src);
       u[1] = __ldg(src + 1);
     }
@@ -341,12 +343,22 @@ __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, cons
   }
 }
 
-// kTree: the last cnt keys are seen by the rows of p.tree.
-template <bool kBf16, int D, bool kTree>
+// A q whose rows lie one after another from `q` on.
+template <int D>
+struct Rows {
+  const uint16_t* q;
+  __device__ __forceinline__ const uint16_t* operator()(int row) const { return q + static_cast<int64_t>(row) * D; }
+};
+
+// Geo = ByNode: the last cnt keys are seen by the rows of p.tree.
+// kG: scale groups of a block of keys, where the kernel is for one number of them; 0: 1 or kGroups, as the
+// call says.
+template <bool kBf16, int D, class Geo, int kG>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const AttendParams<ByHead> p) {
+                     const AttendParams<Geo> p) {
   using C = Config<kBf16, D>;
+  constexpr bool kTree = Geo::kPacked;
   using T8 = typename C::T8;
   using TV = typename C::TV;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sR = smem + C::kOffR;
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kOffShared);
   const int warp = warp_id(), lane = lane_id(), group = warp >> 2;
-  const ByHead& geo = p.geo;
+  const Geo& geo = p.geo;
   const bool split = geo.tile == kRows;  // the two tiles are the same rows, of alternate blocks
   grid_launch_dependents();
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it
@@ -581,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ the run's tiles
       for (int seg = 0;; ++seg) {
         if (!mbar_wait_warp(&sh.seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, p.status, 0x31)) break;
-        const Seg sg = segment<kTree>(geo, pl, u0, u1, blockIdx.x);
+        const Seg sg = segment(geo, pl, u0, u1, blockIdx.x);
         if (lane == 0) {
           sh.seg[seg & 3] = sg;
           if (sg.j0 == 0) note_run(p, pl, u0, u1);
@@ -650,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Seg& sg = sh.seg[seg & 3];
       const int row = sg.r0 + (split ? 0 : t * kRows) + r;
-      const int query = geo.query(row < geo.R ? row : 0);
-      const bool real = row < geo.R && query < sg.cnt;
+      const int rows = geo.rows(sg.cnt), query = geo.query(row < rows ? row : 0, sg.cnt);
+      const bool real = row < rows && query < sg.cnt;
       const int lim = real ? query_keys(geo, sg.len, sg.cnt, query) : sg.len;
       const int reach = sg.reach[t], least = sg.least[t], j0 = sg.j0;
       // The tile's blocks: all up to its reach, or every other one.
@@ -667,8 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = seg == 0 || mbar_wait_warp(&sh.q_free, (seg - 1) & 1, p.status, 0x26);
       if (!ok) break;
       if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
-      put_queries<kBf16, D, 2 * kRows>(sQ, sh.row_mul[seg & 1], p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D,
-                            geo.R - sg.r0, geo.tile, p.c2, t * kRows + r);
+      if constexpr (Geo::kPacked) {
+        put_queries<kBf16, D, 2 * kRows>(
+            sQ, sh.row_mul[seg & 1],
+            [&](int i) { return p.q + geo.row_offset(sg.b, sg.hk, sg.r0 + i, sg.cnt) * D; }, rows - sg.r0, geo.tile,
+            p.c2, t * kRows + r);
+      } else {
+        put_queries<kBf16, D, 2 * kRows>(sQ, sh.row_mul[seg & 1],
+                                         Rows<D>{p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D}, geo.R - sg.r0, geo.tile,
+                                         p.c2, t * kRows + r);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
@@ -709,7 +729,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (k >= seen) sv[k] = -INFINITY;
           }
         }
-        const float mx = uniform ? block_max<1>(sv, sc, mul) : block_max<kGroups>(sv, sc, mul);
+        float mx;
+        if constexpr (kG > 0) {
+          mx = block_max<kG>(sv, sc, mul);
+        } else {
+          mx = uniform ? block_max<1>(sv, sc, mul) : block_max<kGroups>(sv, sc, mul);
+        }
         float alpha = 1.0f;
         if (mx - m > kRaise) {
           const float mn = mx - kTop, half = ex2(0.5f * (m - mn));
@@ -738,8 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           turn_phase ^= 1u;
         }
         const float from = far ? 0.0f : m;
-        l += uniform ? block_probs<1, C::kPair>(sv, sc, mul, from, tS)
-                     : block_probs<kGroups, C::kPair>(sv, sc, mul, from, tS);
+        if constexpr (kG > 0) {
+          l += block_probs<kG, C::kPair>(sv, sc, mul, from, tS);
+        } else {
+          l += uniform ? block_probs<1, C::kPair>(sv, sc, mul, from, tS)
+                       : block_probs<kGroups, C::kPair>(sv, sc, mul, from, tS);
+        }
         __syncwarp();
         if (lane == 0 && i + t < both) mbar_arrive(&sh.turn[t ^ 1]);
         tmem_wait_st();
@@ -819,10 +848,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const bool write = row < geo.R;
+        const bool write = row < rows;
         const bool none = l == 0.0f || !real;  // a padding row, or one that sees no key
         const float inv = kLiftFactor / l;
-        const int64_t orow = geo.row_offset(sg.b, sg.hk, row);
+        const int64_t orow = geo.row_offset(sg.b, sg.hk, row, sg.cnt);
         const int64_t prow = static_cast<int64_t>(sg.slot) * geo.tile + (row - sg.r0);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -904,10 +933,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace tc
 }  // namespace kv8
 
-template <bool kBf16, int D, bool kTree>
-cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
+template <bool kBf16, int D, int kG, class Geo>
+cudaError_t launch_tc(kv8::AttendParams<Geo>& p, cudaStream_t s) {
   using C = kv8::tc::Config<kBf16, D>;
-  auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D, kTree>;
+  auto* kernel = kv8::tc::attend_tc_kernel<kBf16, D, Geo, kG>;
   constexpr size_t smem = C::kOffShared + sizeof(kv8::tc::Shared);
   static_assert(smem <= 227 * 1024, "shared memory overflow");
   CUtensorMap tm_k, tm_v;
@@ -931,6 +960,20 @@ cudaError_t launch_kv8_tc(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s) {
                        smem, s);
   if (e != cudaSuccess) return e;
   return kv8::launch_join<kBf16, D>(p, s);
+}
+
+template <bool kBf16, int D, class Geo>
+cudaError_t launch_kv8_tc(kv8::AttendParams<Geo>& p, cudaStream_t s) {
+  if constexpr (Geo::kPacked) {
+    switch (p.block) {
+      case 16: return launch_tc<kBf16, D, 8>(p, s);
+      case 32: return launch_tc<kBf16, D, 4>(p, s);
+      case 64: return launch_tc<kBf16, D, 2>(p, s);
+      default: return launch_tc<kBf16, D, 1>(p, s);
+    }
+  } else {
+    return launch_tc<kBf16, D, 0>(p, s);
+  }
 }
 
 }  // namespace ea

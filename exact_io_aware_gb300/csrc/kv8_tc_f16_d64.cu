@@ -2,5 +2,5 @@
 #include "kv8_tc.cuh"
 
 namespace ea {
-template cudaError_t launch_kv8_tc<false, 64, false>(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s);
+template cudaError_t launch_kv8_tc<false, 64>(kv8::AttendParams<kv8::ByHead>& p, cudaStream_t s);
 }  // namespace ea

@@ -211,6 +211,24 @@ def test_padding_nodes_do_not_matter(G, n):
     status()
 
 
+@pytest.mark.parametrize("dtype,d,block", [("bf16", 128, 32), ("f16", 64, 64), ("bf16", 64, 16), ("f16", 128, 128)])
+@pytest.mark.parametrize("G,n", [(4, 200), (1, 129), (6, 50), (2, 33)])
+def test_rows_of_few_nodes_among_many(dtype, d, block, G, n):
+    """Counts from none to all, so that the real rows fill other tiles than all rows would: real rows
+    as the oracle's, padding rows 0 and -inf wherever they lie."""
+    rng = np.random.default_rng(G + n)
+    counts = [0, 1, n, n // 2, n - 1, 3, n // 3, 0, 17]
+    lengths = [300, 1, 900, 257, n - 1, 640, 0, 0, 17]
+    ca = Cache(rng, lengths, 2, 1024, d, block)
+    seen = draft.sees(trees(rng, 9, n, 7), counts)
+    q = rounded(rng.normal(size=(9, 2 * G, n, d)), dtype)
+    o, lse = torch.full(q.shape, 7.0, dtype=DT[dtype], device="cuda"), torch.full(q.shape[:3], 7.0, device="cuda")
+    ea.attn_fwd_kv8_tree(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, tree_words(seen), d ** -0.5,
+                         counts=i32(counts), o=o, lse=lse)
+    check_attend(ca, q, d ** -0.5, dtype, o, lse, seen, counts)
+    assert status() == ea.ATTN_WARN_EMPTY_ROW                         # sequence 6 has nodes and no keys
+
+
 def test_attend_clamps_and_tells():
     rng = np.random.default_rng(4)
     ca = Cache(rng, [32, 0, 20], 2, 32, 64, 16)
