@@ -286,35 +286,66 @@ __device__ __forceinline__ void shift_far(float (&sv)[kBlockKeys], const Scales&
 // terms go to the tiles of row tile r / 128 and its factor, c2 times the power of two taken out, to
 // row_mul[r].  The loop stays rolled: unrolled, fetching its instructions once a tile took longer than
 // running them.
-template <bool kBf16, int D, int kN, class Src>
+// kAhead: pieces whose loads are in flight before the one at hand (0: each waits for its own).
+template <bool kBf16, int D, int kN, int kAhead, class Src>
 __device__ __forceinline__ void put_queries(uint8_t* terms, float* row_mul, Src&& src_of, int rows, int tile,
                                             float c2, int tid) {
   using C = Config<kBf16, D>;
   using T8 = typename C::T8;
   constexpr int kLanes = D / 16;
-#pragma unroll 1
-  for (int idx = tid; idx < tile * kLanes; idx += kN) {
+  uint4 ring[kAhead > 0 ? kAhead : 1][2];
+  auto fetch = [&](int idx, uint4 (&u)[2]) {
     const int row = idx / kLanes, piece = idx % kLanes;
-    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (row < rows) {
+    u[0] = u[1] = make_uint4(0, 0, 0, 0);
+    if (row < rows && row < tile) {
       const uint4* src = reinterpret_cast<const uint4*>(src_of(row) + piece * 16);
       u[0] = __ldg(src);
       u[1] = __ldg(src + 1);
     }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(tid + i * kN, ring[i]);
+#pragma unroll 1
+  for (int idx = tid; idx < tile * kLanes; idx += kN) {
+    const int row = idx / kLanes, piece = idx % kLanes;
+    uint4 u[2];
+    if constexpr (kAhead == 0) {
+      fetch(idx, u);
+    } else {
+      u[0] = ring[0][0], u[1] = ring[0][1];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) ring[i][0] = ring[i + 1][0], ring[i][1] = ring[i + 1][1];
+      fetch(idx + kAhead * kN, ring[kAhead - 1]);
+    }
     const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-    float x[16], amax = 0.0f;
+    // Magnitudes are ordered as their bits; those that are not finite lie above all others.
+    uint32_t most = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = __vmaxu2(most, w[e] & 0x7FFF7FFFu);
+    most = max(most >> 16, most & 0xFFFFu);
+    const bool strange = __any_sync(0xFFFFFFFFu, most >= (kBf16 ? 0x7F80u : 0x7C00u));
+    float x[16], amax;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float2 f = unpack16<kBf16>(w[e]);
       x[2 * e] = f.x, x[2 * e + 1] = f.y;
-      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+    }
+    if (__builtin_expect(strange, 0)) {
+      amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        amax = fmaxf(amax, finite_abs(x[i]));
+        x[i] = nan_unless_finite(x[i]);
+      }
+    } else {
+      amax = unpack16<kBf16>(most).x;
     }
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     const int e = scale_exp(amax, -126);
     const float mul = c2 < 0.0f ? -pow2(-e) : pow2(-e);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = nan_unless_finite(x[i]) * mul;
+    for (int i = 0; i < 16; ++i) x[i] *= mul;
     uint8_t* dst = terms + row / kRows * C::kTerms * T8::kBytes + T8::offset(row % kRows, 8 * piece);
     uint32_t c[4];
     float y[4];
@@ -349,6 +380,31 @@ struct Rows {
   const uint16_t* q;
   __device__ __forceinline__ const uint16_t* operator()(int row) const { return q + static_cast<int64_t>(row) * D; }
 };
+
+// Pieces v[i] of a lane's row become piece lane % kN of the rows of the kN lanes around it: kN lanes then
+// store a row's pieces side by side.  (A lane storing its own row would touch as many lines as lanes, half
+// a sector each: a tile of 256 rows took 8,000 to 12,000 cycles to write, and takes TILE_WRITE.)
+template <int kN>
+__device__ __forceinline__ void swap_pieces(uint4 (&v)[kN]) {
+#pragma unroll
+  for (int s = 1; s < kN; s <<= 1) {
+    const bool up = (lane_id() & s) != 0;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      if (j & s) continue;
+      uint4 x = up ? v[j] : v[j | s];
+      x.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, s);
+      x.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, s);
+      x.z = __shfl_xor_sync(0xFFFFFFFFu, x.z, s);
+      x.w = __shfl_xor_sync(0xFFFFFFFFu, x.w, s);
+      if (up) {
+        v[j] = x;
+      } else {
+        v[j | s] = x;
+      }
+    }
+  }
+}
 
 // Geo = ByNode: the last cnt keys are seen by the rows of p.tree.
 // kG: scale groups of a block of keys, where the kernel is for one number of them; 0: 1 or kGroups, as the
@@ -680,14 +736,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
       if constexpr (Geo::kPacked) {
-        put_queries<kBf16, D, 2 * kRows>(
+        put_queries<kBf16, D, 2 * kRows, 4>(
             sQ, sh.row_mul[seg & 1],
             [&](int i) { return p.q + geo.row_offset(sg.b, sg.hk, sg.r0 + i, sg.cnt) * D; }, rows - sg.r0, geo.tile,
             p.c2, t * kRows + r);
       } else {
-        put_queries<kBf16, D, 2 * kRows>(sQ, sh.row_mul[seg & 1],
-                                         Rows<D>{p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D}, geo.R - sg.r0, geo.tile,
-                                         p.c2, t * kRows + r);
+        put_queries<kBf16, D, 2 * kRows, 4>(sQ, sh.row_mul[seg & 1],
+                                            Rows<D>{p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D}, geo.R - sg.r0,
+                                            geo.tile, p.c2, t * kRows + r);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -853,6 +909,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = kLiftFactor / l;
         const int64_t orow = geo.row_offset(sg.b, sg.hk, row, sg.cnt);
         const int64_t prow = static_cast<int64_t>(sg.slot) * geo.tile + (row - sg.r0);
+        const uint32_t writes = __ballot_sync(0xFFFFFFFFu, write);
+        int64_t orows[4];  // of the four rows whose pieces this lane stores
+#pragma unroll
+        for (int k = 0; k < 4; ++k) orows[k] = __shfl_sync(0xFFFFFFFFu, orow, (lane & ~3) + k);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t rr[32];
@@ -883,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 32; ++k)
               if (nan >> k & 1u) rr[k] = 0x7FC00000u;
           }
-          if (write && sg.whole) {
+          if (sg.whole) {
             uint4 w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -893,14 +953,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 h[i] = none ? 0u : pack2<kBf16>(__uint_as_float(rr[8 * k + 2 * i]) * inv,
                                                 __uint_as_float(rr[8 * k + 2 * i + 1]) * inv);
               w[k] = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(p.o + orow * D + c0 + 8 * k) = w[k];
             }
-          } else if (write) {
+            swap_pieces(w);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(p.part_z + prow * D + c0 + k) =
-                  make_float4(__uint_as_float(rr[k]), __uint_as_float(rr[k + 1]), __uint_as_float(rr[k + 2]),
-                              __uint_as_float(rr[k + 3]));
+            for (int k = 0; k < 4; ++k)
+              if (writes >> ((lane & ~3) + k) & 1u)
+                *reinterpret_cast<uint4*>(p.o + orows[k] * D + c0 + 8 * (lane & 3)) = w[k];
+          } else {
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              uint4 w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = make_uint4(rr[h + 4 * k], rr[h + 4 * k + 1], rr[h + 4 * k + 2], rr[h + 4 * k + 3]);
+              swap_pieces(w);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (writes >> ((lane & ~3) + k) & 1u)
+                  *reinterpret_cast<uint4*>(p.part_z + (prow - (lane & 3) + k) * D + c0 + h + 4 * (lane & 3)) = w[k];
+            }
           }
         }
         if (write && sg.whole) {

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         if (part > 0) ok = mbar_wait_warp(&sh.q_free, (part - 1) & 1, p.status, 0x36);
         if (!ok) break;
-        tc::put_queries<kBf16, D, 128 * kTeams>(sQ, sh.row_mul, tc::Rows<D>{p.q + geo.row_offset(pl.b, pl.hk, r0) * D}, rows, tiles * kRows,
+        tc::put_queries<kBf16, D, 128 * kTeams, 0>(sQ, sh.row_mul, tc::Rows<D>{p.q + geo.row_offset(pl.b, pl.hk, r0) * D}, rows, tiles * kRows,
                                   p.c2, tid);
         if (tid < kMostRows) {
           const int r = r0 + tid;
