@@ -87,16 +87,19 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(KeepParams p) {
         sc[it] = scales[src >> shift] * kDown;
       }
     }
+    // (a warp into whose positions nothing moves has nothing to look at)
+    if (__any_sync(0xFFFFFFFFu, src16 >= 0)) {
 #pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      float x[4], y[4];
-      codes_to_float4(raw[it].x, x);
-      codes_to_float4(raw[it].y, y);
+      for (int it = 0; it < kIters; ++it) {
+        float x[4], y[4];
+        codes_to_float4(raw[it].x, x);
+        codes_to_float4(raw[it].y, y);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        amax = fmaxf(amax, fmaxf(finite_abs(x[e] * sc[it]), finite_abs(y[e] * sc[it])));
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(finite_abs(x[e] * sc[it]), finite_abs(y[e] * sc[it])));
+      }
+      amax = warp_max(amax);
     }
-    amax = warp_max(amax);
     if (lane == 0) red[warp] = amax;
     __syncthreads();  // the span is read
     if (takes) {

@@ -229,6 +229,44 @@ def test_rows_of_few_nodes_among_many(dtype, d, block, G, n):
     assert status() == ea.ATTN_WARN_EMPTY_ROW                         # sequence 6 has nodes and no keys
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,most", [(150, 140), (60, 1500)])
+def test_tiles_of_more_and_of_fewer_real_rows_in_turn(dtype, B, most):
+    """Many tiles in each CTA's run, of up to 180 real rows: with more than 128 and with fewer, whole and cut,
+    some ending in a NaN value, some with nothing to see."""
+    rng = np.random.default_rng(B)
+    Hk, G, n, d = 5, 3, 60, 64
+    lengths = [int(x) for x in rng.integers(0, most, B)]
+    counts = [min(int(x), m) for x, m in zip(rng.integers(0, n + 1, B), lengths)]
+    ca = Cache(rng, lengths, Hk, 1536, d, 32)
+    seen = draft.sees(trees(rng, B, n, 9), counts)
+    sick = [b for b in range(B) if b % 7 == 3 and counts[b] > 2]
+    for b in sick:
+        ca.c["v8"][b, :, lengths[b] - 1, 5] = np.nan                  # the last node's: a leaf
+    ca.load()
+    q = rounded(rng.normal(size=(B, Hk * G, n, d)), dtype)
+    args = (q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, tree_words(seen), 0.125)
+    o, lse = ea.attn_fwd_kv8_tree(*args, counts=i32(counts))
+    again = ea.attn_fwd_kv8_tree(*args, counts=i32(counts))
+    assert torch.equal(o.view(torch.int16), again[0].view(torch.int16)) and torch.equal(lse, again[1])
+    want = np.zeros(o.shape, bool)
+    for b in sick:
+        want[b, :, counts[b] - 1, 5] = True
+    nan = torch.isnan(o).cpu().numpy()
+    assert (nan == want).all(), np.argwhere(nan != want)[:5].tolist()
+    for b in sick:
+        ca.c["v8"][b, :, lengths[b] - 1, 5] = 0.0
+    some = rng.choice(B, 10, replace=False)
+    sub = type("Sub", (), {})()
+    sub.c, sub.k8 = {key: val[some] for key, val in ca.c.items()}, ca.k8
+    o2 = o[some].clone()
+    O = draft.attend(sub.c, q[some].double().numpy(), 0.125, seen[some], [counts[b] for b in some])[0]
+    fix = torch.from_numpy(want[some]).cuda()
+    o2[fix] = torch.from_numpy(O).to(o2)[fix]
+    check_attend(sub, q[some], 0.125, dtype, o2, lse[some], seen[some], [counts[b] for b in some])
+    status()
+
+
 def test_attend_clamps_and_tells():
     rng = np.random.default_rng(4)
     ca = Cache(rng, [32, 0, 20], 2, 32, 64, 16)
