@@ -601,11 +601,13 @@ template <int kType, bool kDrawn>
 cudaError_t launch(const DraftVerifyArgs& a, cudaStream_t s) {
   VerifyParams p{a.n, a.V, a.target, a.draft, a.tokens, a.parents, a.counts, a.uniforms, a.path, a.accepted,
                  a.next_token, a.status};
-  // CTAs of a cluster: doubled while each warp has more than two tiles of the vocabulary, and all
-  // clusters are on the device at once.
+  // CTAs of a cluster: doubled while each warp has more than one tile of the vocabulary and the device
+  // holds the clusters of all sequences at once (two CTAs a multiprocessor).  us with 2, 4 and 8: 64 sequences
+  // of 100003 bf16 values 14.8, 14.8, 21.2 (4 fill the device); with 4 and 8: 32 of 131072 float32 values
+  // 30.1, 25.2 (8); with 1, 2 and 4: 150 of 32000 bf16 values 28.6, 23.0, 31.9 (2).
   const int tiles = (a.V + Share<kType, kDrawn>::kTile - 1) / Share<kType, kDrawn>::kTile;
   int ranks = 1;
-  while (ranks < kMostRanks && tiles > 2 * ranks * kWarps && ranks * static_cast<int64_t>(a.B) <= a.sms) ranks *= 2;
+  while (ranks < kMostRanks && tiles > ranks * kWarps && ranks * static_cast<int64_t>(a.B) <= a.sms) ranks *= 2;
   void* args[] = {&p};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
