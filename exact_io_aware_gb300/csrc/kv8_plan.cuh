@@ -61,7 +61,7 @@ struct ByHead : Geometry {
 
 // Real rows alone, in the order they lie in memory: row r is query r % cnt of head r / cnt.  For a tree's
 // rows, which all see every tile's keys up to the sequence's end: padding would cost what real rows do
-// (4 x 8 heads of four times 128 to 256 rows over 16384 keys, d = 64: TREE_PAD).
+// (4 x 8 heads of four times 128 to 256 rows over 16384 keys, d = 64, fp16: 280 us with it, 247 packed).
 struct ByNode : Geometry {
   static constexpr int kStep = kBlockKeys;
   static constexpr bool kPacked = true;

@@ -27,10 +27,12 @@
 //   3  converters: one thread a key, its V codes into an fp16 tile
 // S and P share TMEM columns; O stays in TMEM for the length of a tile.
 //
-// Measured (d = 128): 2048 rows against 32768 keys of 8 heads, causal, bf16, 225 us, 1.21 PFLOP/s, 64 %
+// Measured (d = 128): 2048 rows against 32768 keys of 8 heads, causal, bf16, 220 us, 1.24 PFLOP/s, 66 %
 // of the measured bf16 rate; bound by a block's chain of products and exponentials, the tensor pipe
 // active about half of the cycles.  48 rows against up to 8191 keys of 128 heads: 81 us.  fp16: 345
-// and 116 us.
+// and 116 us.  Trees: 256 rows against 120001 to 131072 keys of 16 heads 207 us, 68 %; up to 208 rows against 4001
+// to 8191 keys of 128 heads 111 us, where a CTA has two tiles and spends a quarter of its time between
+// them (queries into terms 4.6 us, rows written 4.2 us each).
 //
 // The registers of 512 threads are dealt again: softmax holds a row's 128 scores, the others
 // need few (kRegs*: their sum over the warpgroups is what the block was launched with).
@@ -64,6 +66,10 @@ struct Config {
   // 117 on those 48; for bf16 outputs, whose error it would change from 1.67e-3 to 1.66e-3, 229 to 328
   // and 83 to 113.
   static constexpr bool kPair = !kBf16;
+  // Pieces of queries fetched ahead between tiles (put_queries).  Each holds eight registers; the fp16 kernels
+  // have none left over and pay in every block: us of 2048 rows of 32768 keys, 8 heads, blocks of 64, with 4, 2
+  // and 1: d = 64 296, 280, 272, d = 128 343, 328, 338.
+  static constexpr int kAhead = kBf16 ? 4 : D == 64 ? 1 : 2;
   static constexpr int kSK = 2, kSV = 2;  // stages of K tiles and of V tiles
   static constexpr int kSR = kBf16 ? 3 : 2;  // of raw V blocks
   static constexpr int kRaw = kBlockKeys * D;
@@ -383,7 +389,7 @@ struct Rows {
 
 // Pieces v[i] of a lane's row become piece lane % kN of the rows of the kN lanes around it: kN lanes then
 // store a row's pieces side by side.  (A lane storing its own row would touch as many lines as lanes, half
-// a sector each: a tile of 256 rows took 8,000 to 12,000 cycles to write, and takes TILE_WRITE.)
+// a sector each: writing 256 rows took 10,500 cycles, and takes 8,000.)
 template <int kN>
 __device__ __forceinline__ void swap_pieces(uint4 (&v)[kN]) {
 #pragma unroll
@@ -408,7 +414,9 @@ __device__ __forceinline__ void swap_pieces(uint4 (&v)[kN]) {
 
 // Geo = ByNode: the last cnt keys are seen by the rows of p.tree.
 // kG: scale groups of a block of keys, where the kernel is for one number of them; 0: 1 or kGroups, as the
-// call says.
+// call says.  (us of 2048 rows of 32768 keys, 8 heads, fp16, d = 64, in blocks of 64 tokens: 340 with kG = 0, 299
+// with a kernel for its two groups, 374 with a branch over 1, 2, 4 and 8 in one kernel; d = 128, bf16: 242, 225,
+// 246.  The sums are the same bit for bit.)
 template <bool kBf16, int D, class Geo, int kG>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -736,12 +744,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (t == 0 && r == 0) sh.nan_seen[(seg + 2) & 3] = 0;  // read last two tiles ago
       if constexpr (Geo::kPacked) {
-        put_queries<kBf16, D, 2 * kRows, 4>(
+        put_queries<kBf16, D, 2 * kRows, C::kAhead>(
             sQ, sh.row_mul[seg & 1],
             [&](int i) { return p.q + geo.row_offset(sg.b, sg.hk, sg.r0 + i, sg.cnt) * D; }, rows - sg.r0, geo.tile,
             p.c2, t * kRows + r);
       } else {
-        put_queries<kBf16, D, 2 * kRows, 4>(sQ, sh.row_mul[seg & 1],
+        put_queries<kBf16, D, 2 * kRows, C::kAhead>(sQ, sh.row_mul[seg & 1],
                                             Rows<D>{p.q + geo.row_offset(sg.b, sg.hk, sg.r0) * D}, geo.R - sg.r0,
                                             geo.tile, p.c2, t * kRows + r);
       }
