@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
       const int x = __ldg(p.tokens + nodes + i);
       const float u = __ldg(p.uniforms + nodes + i);
       const bool known = up >= 0 && up < i, real = x >= 0 && x < p.V;
-      if (i > 0 && (!real || up < -1 || up >= i)) odd_at |= bit;
+      if (up < -1 || up >= i || (i > 0 && !real)) odd_at |= bit;
       const int64_t v = known && real ? (nodes + up) * p.V + x : 0;
       sh.up[i] = known ? up : -1;  // -1: no node's child, never asked
       sh.token[i] = real ? x : -1;

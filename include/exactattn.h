@@ -337,7 +337,8 @@ int attn_kv8_evict(int B, int H_kv, int d, int cap, int block, const void* k8, c
  * Decoding by a tree of drafted tokens over the 8-bit cache (no counterpart on the pages).  Sequence b
  * of a call has counts[b] nodes (NULL: n): node 0 is the token decided last, the others are drafts.
  * parents (int32 [B][n]) has a node's parent, a node of a lower number, and -1 for node 0; a parent
- * outside [-1, i) counts as -1 and raises ATTN_WARN_CLAMPED, as does a count outside [0, n].  One round:
+ * outside [-1, i) counts as -1 and raises ATTN_WARN_CLAMPED, as does a count outside [0, n].  (Another
+ * node of parent -1 starts a tree of its own: attn_draft_verify never reaches it.)  One round:
  * attn_kv8_append writes the nodes' keys and values at the sequence's end (lengths count them),
  * attn_fwd_kv8_tree lets each node attend to the tokens before the tree and to its own ancestors,
  * attn_draft_verify decides which nodes the target's probabilities accept and which token follows,
