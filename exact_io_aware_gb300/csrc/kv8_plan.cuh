@@ -175,6 +175,105 @@ __device__ __forceinline__ Place plan_run(const Geo& g, int cta, int ctas, int m
   return p;
 }
 
+// The same for a tree's rows, all of whose tiles of a sequence have its every chunk.  Equal runs across the list
+// cut tiles where they happen to end, and a run has the end of one tile and the start of another; so where the
+// tiles are no more than the CTAs, a CTA takes one tile or an equal part of one, if the parts are not much longer than
+// runs would be; and where there are more and all are alike, whole ones.  In chunks of work, what a tile's
+// start and end cost is kTurn (13 us), what parts and their join cost kParts.  us in equal runs and so, 256 rows a
+// head, d = 128: 128 heads of 1024, 2048 and 6144 keys PLAN_A; 32 of 4096 PLAN_B; 512 of 1024 PLAN_C.
+constexpr int kTurn = 7, kParts = 3;
+__device__ __forceinline__ Place plan_run(const ByNode& g, int cta, int ctas, int min_chunks, int& u0, int& u1) {
+  const int lane = lane_id(), tile_shift = 31 - __clz(g.tile);
+  // Row tiles of a head of sequence b, and chunks of each.
+  auto tiles_of = [&](int b, int& c) {
+    c = 0;
+    if (b >= g.B) return 0;
+    c = chunks_of(g, seq_len(g.lengths, b, g.cap));
+    return c > 0 ? (g.G * seq_count(g.counts, b, g.n) + g.tile - 1) >> tile_shift : 0;
+  };
+  int c0;
+  const int t0 = tiles_of(lane, c0);  // the lane's first sequence's
+  // Over all heads, tiles cut into parts of at most `part` chunks.
+  auto parts_of = [&](int part) {
+    int sum = t0 * ((c0 + part - 1) / part), c;
+    for (int b = lane + 32; b < g.B; b += 32) sum += tiles_of(b, c) * ((c + part - 1) / part);
+    return __reduce_add_sync(0xFFFFFFFFu, sum) * g.Hk;
+  };
+  int total = t0 * c0, tiles = t0, least = t0 > 0 ? c0 : 1 << 30, most = t0 > 0 ? c0 : 0;
+  for (int b = lane + 32; b < g.B; b += 32) {
+    int c;
+    const int t = tiles_of(b, c);
+    total += t * c;
+    tiles += t;
+    if (t > 0) least = min(least, c), most = max(most, c);
+  }
+  total = __reduce_add_sync(0xFFFFFFFFu, total) * g.Hk;
+  tiles = __reduce_add_sync(0xFFFFFFFFu, tiles) * g.Hk;
+  least = __reduce_min_sync(0xFFFFFFFFu, least);
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  int per = run_length(total, ctas, min_chunks);
+  int part = 0;  // > 0: a CTA takes one part, of at most so many chunks, of a tile
+  if (tiles <= ctas) {
+    // The least part (at least `per`) at which there are no more of them than CTAs.
+    int lo = per, hi = min(per + kTurn + kParts, max(most, per));
+    if (least == most) lo = hi = min(max((most + ctas / tiles - 1) / (ctas / tiles), per), hi);
+    if (parts_of(hi) <= ctas) {
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (parts_of(mid) <= ctas) {
+          hi = mid;
+        } else {
+          lo = mid + 1;
+        }
+      }
+      if (lo <= per + kTurn + (lo < most ? 0 : kParts)) part = lo;
+    }
+  } else if (least == most) {
+    const int whole = (tiles + ctas - 1) / ctas;
+    if (whole * (most + kTurn) <= per + kTurn * (1 + whole) + kParts) per = whole * most;
+  }
+  u0 = part > 0 ? cta : cta * per;  // the first part or chunk: find its sequence
+  u1 = part > 0 ? cta + 1 : min(u0 + per, total);
+  Place p{0, 0, 0, 0, 0};
+  if (u0 >= u1) return p;
+  int base = 0, t = 0, units = 0;  // of the sequence: tiles of a head, and parts or chunks of a tile
+  for (int b0 = 0;; b0 += 32) {
+    if (b0 >= g.B) {  // more CTAs than parts
+      u0 = u1 = 0;
+      return p;
+    }
+    int c = c0;
+    const int mine = b0 == 0 ? t0 : tiles_of(b0 + lane, c), each = part > 0 ? (c + part - 1) / part : c, v = mine * each * g.Hk;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + x > u0);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      p.b = b0 + l;
+      t = __shfl_sync(0xFFFFFFFFu, mine, l);
+      units = __shfl_sync(0xFFFFFFFFu, each, l);
+      base += __shfl_sync(0xFFFFFFFFu, x - v, l);
+      break;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, x, 31);
+  }
+  const int tile = (u0 - base) / units;
+  p.hk = tile / t;
+  p.rt = tile % t;
+  p.keys = seq_len(g.lengths, p.b, g.cap);
+  if (part > 0) {  // a list of this tile alone
+    u0 = (u0 - base) % units * part;
+    u1 = min(u0 + part, chunks_of(g, p.keys));
+  } else {
+    p.start = base + tile * units;
+  }
+  return p;
+}
+
 // The next tile of the list with at least one chunk (the caller knows that there is one).
 template <class Geo>
 __device__ __forceinline__ void next_place(const Geo& g, Place& p) {
