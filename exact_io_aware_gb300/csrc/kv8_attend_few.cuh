@@ -242,7 +242,11 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas_per_sm<NT>())
   int u0, u1;
   Place pl;
   if (p.ctas > 0) {
-    pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    if constexpr (kTree) {
+      pl = plan_trees(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    } else {
+      pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    }
     if (u0 >= u1) return;
   } else {
     pl.rt = 0;

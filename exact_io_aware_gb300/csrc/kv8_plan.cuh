@@ -24,6 +24,8 @@ struct Geometry {
 // a head's.
 struct ByQuery : Geometry {
   static constexpr int kStep = kChunk;
+  static constexpr int kTurn = 10, kParts = 2, kLongRun = 60;  // (plan_trees)
+  __device__ __forceinline__ int row_tiles(int cnt) const { return cnt > 0 ? 1 : 0; }
   static constexpr bool kPacked = false;
   __device__ __forceinline__ int query(int r) const { return r / G; }
   // Row of q and o, [B][Hk G][n][D].
@@ -65,6 +67,8 @@ struct ByHead : Geometry {
 struct ByNode : Geometry {
   static constexpr int kStep = kBlockKeys;
   static constexpr bool kPacked = true;
+  static constexpr int kTurn = 7, kParts = 3, kLongRun = 1 << 30;  // (plan_trees)
+  __device__ __forceinline__ int row_tiles(int cnt) const { return (G * cnt + tile - 1) >> (31 - __clz(tile)); }
   __device__ __forceinline__ int rows(int cnt) const { return G * cnt; }
   __device__ __forceinline__ int query(int r, int cnt) const { return r % cnt; }
   __device__ __forceinline__ int64_t row_offset(int b, int hk, int r, int cnt) const {
@@ -179,17 +183,21 @@ __device__ __forceinline__ Place plan_run(const Geo& g, int cta, int ctas, int m
 // cut tiles where they happen to end, and a run has the end of one tile and the start of another; so where the
 // tiles are no more than the CTAs, a CTA takes one tile or an equal part of one, if the parts are not much longer than
 // runs would be; and where there are more and all are alike, whole ones.  In chunks of work, what a tile's
-// start and end cost is kTurn (13 us), what parts and their join cost kParts.  us in equal runs and so, 256 rows a
-// head, d = 128: 128 heads of 1024, 2048 and 6144 keys PLAN_A; 32 of 4096 PLAN_B; 512 of 1024 PLAN_C.
-constexpr int kTurn = 7, kParts = 3;
-__device__ __forceinline__ Place plan_run(const ByNode& g, int cta, int ctas, int min_chunks, int& u0, int& u1) {
-  const int lane = lane_id(), tile_shift = 31 - __clz(g.tile);
+// start and end cost is kTurn, what parts and their join cost kParts.  us in equal runs and so, d = 128:
+//   256 rows (kTurn: 13 us)   128 heads of 1024 keys 51, 33, of 6144 112, 103; 32 of 4096 41, 33; 512 of 1024 145,
+//                             123; 24 of 1024 to 4096 37, 27; 16 of 49152 101, 94
+//   16 rows (4 us)            32 heads of 4096 keys 21.4, 17.3, of 16384 40.2, 36.5; 256 of 1024 26.2, 21.4; 8 of 256 to
+//                             1024 14.8, 11.3; runs longer than kLongRun gain nothing (64 heads of 16384 58.2, 58.5)
+template <class Geo>
+__device__ __forceinline__ Place plan_trees(const Geo& g, int cta, int ctas, int min_chunks, int& u0, int& u1) {
+  constexpr int kTurn = Geo::kTurn, kParts = Geo::kParts;
+  const int lane = lane_id();
   // Row tiles of a head of sequence b, and chunks of each.
   auto tiles_of = [&](int b, int& c) {
     c = 0;
     if (b >= g.B) return 0;
     c = chunks_of(g, seq_len(g.lengths, b, g.cap));
-    return c > 0 ? (g.G * seq_count(g.counts, b, g.n) + g.tile - 1) >> tile_shift : 0;
+    return c > 0 ? g.row_tiles(seq_count(g.counts, b, g.n)) : 0;
   };
   int c0;
   const int t0 = tiles_of(lane, c0);  // the lane's first sequence's
@@ -213,7 +221,8 @@ __device__ __forceinline__ Place plan_run(const ByNode& g, int cta, int ctas, in
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   int per = run_length(total, ctas, min_chunks);
   int part = 0;  // > 0: a CTA takes one part, of at most so many chunks, of a tile
-  if (tiles <= ctas) {
+  if (per > Geo::kLongRun) {
+  } else if (tiles <= ctas) {
     // The least part (at least `per`) at which there are no more of them than CTAs.
     int lo = per, hi = min(per + kTurn + kParts, max(most, per));
     if (least == most) lo = hi = min(max((most + ctas / tiles - 1) / (ctas / tiles), per), hi);

@@ -442,7 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   int u0 = 0, u1 = 0;
   Place pl{};
   if (warp == 3) {
-    pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    if constexpr (kTree) {
+      pl = plan_trees(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    } else {
+      pl = plan_run(geo, blockIdx.x, p.ctas, p.min_chunks, u0, u1);
+    }
     if (lane == 0) sh.idle = u0 >= u1;
   }
 

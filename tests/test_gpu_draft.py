@@ -143,10 +143,11 @@ def test_attend_long(dtype, d, G, n, cap, lengths):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G,n", [(1, 5), (4, 4), (2, 16), (8, 12), (8, 30)])
 def test_a_chain_and_a_full_square_are_the_masks_that_there_were(dtype, d, G, n):
-    """Bit for bit: the same rows, keys and order of sums."""
+    """Bit for bit, at sizes whose work both divide alike (no tile is cut: caches of at most 512 tokens for few
+    rows, two blocks of 128 keys for many): the same rows, keys and order of sums."""
     rng = np.random.default_rng(n)
-    lengths = [n, 100, 256, 1000, 131]
-    ca = Cache(rng, lengths, 2, 1024, d, 32)
+    lengths = [200, 131, 256, 129, 224]
+    ca = Cache(rng, lengths, 2, 384, d, 32)
     q = rounded(rng.normal(size=(5, 2 * G, n, d)), dtype).cuda()
     args = (ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths)
     chain = ea.attn_tree_mask(i32(trees(rng, 5, n, "chain")))
@@ -227,6 +228,35 @@ def test_rows_of_few_nodes_among_many(dtype, d, block, G, n):
                          counts=i32(counts), o=o, lse=lse)
     check_attend(ca, q, d ** -0.5, dtype, o, lse, seen, counts)
     assert status() == ea.ATTN_WARN_EMPTY_ROW                         # sequence 6 has nodes and no keys
+
+
+@pytest.mark.parametrize("B,G,n,lengths", [
+    (100, 1, 4, [320]),             # more heads than CTAs, all alike: whole heads a CTA
+    (100, 8, 5, [320]),
+    (30, 8, 5, [320]),              # as many as CTAs, nearly
+    (7, 8, 40, [1100]),             # equal parts of a head
+    (7, 2, 4, [1100]),
+    (11, 3, 50, [1100, 700, 130]),  # parts of unequal heads
+    (40, 2, 3, [1100, 20, 600]),
+])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+def test_every_way_work_is_divided(dtype, d, B, G, n, lengths):
+    """Heads that CTAs take whole, in parts, or in runs across them: some sequences against the oracle, and
+    the whole call the same once more."""
+    rng = np.random.default_rng(B + G + n)
+    lengths = [lengths[b % len(lengths)] for b in range(B)]
+    ca = Cache(rng, lengths, 5, 1152 if max(lengths) > 320 else 640, d, 64)
+    seen = draft.sees(trees(rng, B, n, 4))
+    q = rounded(rng.normal(size=(B, 5 * G, n, d)), dtype)
+    args = (q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, tree_words(seen), d ** -0.5)
+    o, lse = ea.attn_fwd_kv8_tree(*args)
+    again = ea.attn_fwd_kv8_tree(*args)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    some = rng.choice(B, min(B, 7), replace=False)
+    sub = type("Sub", (), {})()
+    sub.c, sub.k8 = {key: val[some] for key, val in ca.c.items()}, ca.k8
+    check_attend(sub, q[some], d ** -0.5, dtype, o[some], lse[some], seen[some])
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all() and status() == ea.ATTN_OK
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
