@@ -30,7 +30,7 @@
 // Measured (d = 128): 2048 rows against 32768 keys of 8 heads, causal, bf16, 220 us, 1.24 PFLOP/s, 66 %
 // of the measured bf16 rate; bound by a block's chain of products and exponentials, the tensor pipe
 // active about half of the cycles.  48 rows against up to 8191 keys of 128 heads: 81 us.  fp16: 345
-// and 116 us.  Trees: 256 rows against 120001 to 131072 keys of 16 heads 207 us, 68 %; up to 208 rows against 4001
+// and 116 us.  Trees: 256 rows against 120001 to 131072 keys of 16 heads 202 us, 70 %; up to 208 rows against 4001
 // to 8191 keys of 128 heads 111 us, where a CTA has two tiles and spends a quarter of its time between
 // them (queries into terms 4.6 us, rows written 4.2 us each).
 //

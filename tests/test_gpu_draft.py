@@ -158,6 +158,22 @@ def test_a_chain_and_a_full_square_are_the_masks_that_there_were(dtype, d, G, n)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), mask
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", [(1, 5), (4, 4), (2, 16), (8, 12), (8, 30)])
+def test_chains_and_full_squares_whose_tiles_are_cut(dtype, d, G, n):
+    """At sizes whose work the two divide differently, so that sums may be in another order: both masks
+    against the oracle."""
+    rng = np.random.default_rng(n)
+    lengths = [n, 100, 256, 1000, 131]
+    ca = Cache(rng, lengths, 2, 1024, d, 32)
+    q = rounded(rng.normal(size=(5, 2 * G, n, d)), dtype)
+    for seen in (draft.sees(trees(rng, 5, n, "chain")), np.ones((5, n, n), bool)):
+        o, lse = ea.attn_fwd_kv8_tree(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, tree_words(seen), d ** -0.5)
+        check_attend(ca, q, d ** -0.5, dtype, o, lse, seen)
+    status()
+
+
 @pytest.mark.parametrize("G,n", [(2, 3), (1, 24), (4, 40)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_nan_reaches_only_the_rows_that_see_it(d, G, n):
