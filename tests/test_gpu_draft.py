@@ -246,6 +246,28 @@ def test_rows_of_few_nodes_among_many(dtype, d, block, G, n):
     assert status() == ea.ATTN_WARN_EMPTY_ROW                         # sequence 6 has nodes and no keys
 
 
+@pytest.mark.parametrize("dtype,d,block", [("bf16", 128, 32), ("f16", 64, 64), ("bf16", 64, 16), ("f16", 128, 128)])
+@pytest.mark.parametrize("B,G,n", [(9, 4, 4), (9, 5, 3), (90, 2, 8), (90, 1, 16), (230, 1, 5)])
+def test_few_rows_of_few_nodes_among_many(dtype, d, block, B, G, n):
+    """The same for few rows, in caches that are cut: fewer heads than CTAs, about as many, and more."""
+    rng = np.random.default_rng(G + n)
+    counts = [(0, 1, n, n // 2, n - 1, 3, 2, 0, n)[b % 9] for b in range(B)]
+    lengths = [(300, 1, 900, 257, n - 1, 640, 0, 0, n)[b % 9] for b in range(B)]
+    ca = Cache(rng, lengths, 2, 1024, d, block)
+    seen = draft.sees(trees(rng, B, n, 7), counts)
+    q = rounded(rng.normal(size=(B, 2 * G, n, d)), dtype)
+    o, lse = torch.full(q.shape, 7.0, dtype=DT[dtype], device="cuda"), torch.full(q.shape[:3], 7.0, device="cuda")
+    ea.attn_fwd_kv8_tree(q.cuda(), ca.k8, ca.v8, ca.ks, ca.vs, ca.lengths, tree_words(seen), d ** -0.5,
+                         counts=i32(counts), o=o, lse=lse)
+    some = np.r_[0:9, B - 9:B]
+    sub = type("Sub", (), {})()
+    sub.c, sub.k8 = {key: val[some] for key, val in ca.c.items()}, ca.k8
+    check_attend(sub, q[some], d ** -0.5, dtype, o[some], lse[some], seen[some], [counts[b] for b in some])
+    pad = torch.from_numpy(np.arange(n) >= np.array(counts)[:, None]).cuda()[:, None, :].expand(lse.shape)
+    assert (o[pad] == 0).all() and torch.isneginf(lse[pad]).all() and torch.isfinite(o).all()
+    assert status() == ea.ATTN_WARN_EMPTY_ROW                         # sequence 6 has nodes and no keys
+
+
 @pytest.mark.parametrize("B,G,n,lengths", [
     (100, 1, 4, [320]),             # more heads than CTAs, all alike: whole heads a CTA
     (100, 8, 5, [320]),
