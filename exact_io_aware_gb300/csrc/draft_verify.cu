@@ -25,6 +25,7 @@
 #include <cooperative_groups.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "draft.h"
 #include "kv8_common.cuh"
@@ -480,6 +481,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   const int64_t nodes = static_cast<int64_t>(b) * p.n;
   const float u0 = __ldg(p.uniforms + nodes);
   int cnt = 0;
+  // A CTA's shared memory may be touched by others only once it runs: each says so here, and all wait for
+  // it before the first command, behind the first CTA's gather.
+  auto running = cluster.barrier_arrive();
 
   if (rank == 0) {
     uint32_t odd_at = 0, bit = 1;  // of the thread's nodes, those with a token or parent out of range
@@ -520,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   };
   int child = leads ? child_from(next) : 0;
   Command cmd;
+  cluster.barrier_wait(std::move(running));
   for (;;) {
     if (leads) {
       bool refusing = false;
