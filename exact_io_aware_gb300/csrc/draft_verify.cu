@@ -148,18 +148,22 @@ struct Pair2 {
 // Which residual: the probabilities themselves (S = 0), after a first refusal (S = 1), or after more.
 enum Kind : int { kAll, kFirst, kMore };
 __device__ __forceinline__ Kind kind_of(Pair S) { return S.hi == 0.0f ? kAll : S.hi == 1.0f && S.lo == 0.0f ? kFirst : kMore; }
-// max(p - S q, 0) of two elements.  With h = S q rounded, m = max(p, h) and d = m - h rounded, what d leaves
-// is (m - d) - h, exactly, as m >= h.  (An element with p = h counts as 0, though S q may lie 2^-25 of it off.)
+// max(p - S q, 0) of two elements, as pairs.  After one refusal, with m = max(p, q) and d = m - q rounded, what
+// d leaves is (m - d) - q, exactly, as m >= q.  After more, h = S q is rounded too, and where p lies within a
+// few of its last places all that is left may be in what was rounded off: so x = (p - d) - h + (h - S q) joins
+// d = p - h before the sign is looked at.  (p - d) - h is exact where p >= h / 2, below that d is negative
+// by far more than x; the roundings of x come to 2^-45 of p.
 template <int kKind>
 __device__ __forceinline__ Pair2 residual(float2 p, float2 q, Pair S) {
   if (kKind == kAll) return {p, both(0.0f)};
-  const float2 h = kKind == kFirst ? q : mul2(both(S.hi), q), m = max2(p, h), d = sub2(m, h);
-  float2 lo = sub2(sub2(m, d), h);
-  if (kKind == kMore) {
-    const float2 e = fma2(both(-S.lo), q, fma2(both(-S.hi), q, h));  // h - S q
-    lo = add2(lo, make_float2(d.x > 0.0f ? e.x : 0.0f, d.y > 0.0f ? e.y : 0.0f));
+  if (kKind == kFirst) {
+    const float2 m = max2(p, q), d = sub2(m, q);
+    return {d, sub2(sub2(m, d), q)};
   }
-  return {d, lo};
+  const float2 h = mul2(both(S.hi), q), d = sub2(p, h);
+  const float2 x = add2(sub2(sub2(p, d), h), fma2(both(-S.lo), q, fma2(both(-S.hi), q, h)));
+  const float2 t = add2(d, x), lo = sub2(x, sub2(t, d));
+  return {max2(t, both(0.0f)), make_float2(t.x > 0.0f ? lo.x : 0.0f, t.y > 0.0f ? lo.y : 0.0f)};
 }
 __device__ __forceinline__ Pair2 residual(float2 p, float2 q, Pair S) {
   const Kind k = kind_of(S);
@@ -464,7 +468,7 @@ __device__ __forceinline__ bool accepts(float u, float p, float q, Pair S, Pair 
     right = r.hi.x + r.lo.x;
   }
   const float left = u * q * W.hi;
-  // Both sides are within 2^-22 of theirs, and t's cancellation within 2^-44 of p.
+  // Both sides are within 2^-22 of theirs, and t besides within 2^-45 of p (residual).
   if (fabsf(left - right) > 1e-6f * (fabsf(left) + right) + 1e-12f * p && fabsf(left) + right > 1e-30f)
     return left < right;
   const double t = fmax(__dsub_rn(p, __dmul_rn(S.value(), q)), 0.0);
