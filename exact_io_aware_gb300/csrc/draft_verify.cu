@@ -19,9 +19,11 @@
 //
 // The device has two 64-bit units a multiprocessor, and a dependent 64-bit step of a warp takes about a
 // hundred cycles: walk, sums and scans in 64 bits took 37 us where these take 23 (32 trees of 32 nodes over
-// 131072 values).  So sums are pairs of float32 values (error-free sums and products; what the second
-// value rounds off comes to about 2^-40 of a row's mass), two elements an instruction, and a child's test is
-// float32 unless its sides lie within 10^-6.
+// 131072 values).  So sums are pairs of float32 values, by Knuth's and Dekker's error-free sums and products,
+// two elements an instruction, and a child's test is float32 unless its sides lie within 10^-6.  Of a row of
+// mass 1 the pairs' second values round off at most 2^-42 + V 2^-48: an element's two additions 2^-49 while its
+// accumulator holds less than 2^-5, and 2^-44 of what it holds beyond that, so 2^-48 together (Sum); fifteen
+// additions of pairs above one another 1.5 2^-47 each.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -171,7 +173,9 @@ __device__ __forceinline__ Pair2 residual(float2 p, float2 q, Pair S) {
 }
 
 // A sum of nonnegative values.  It starts at kFrom, so that the sum is never below a value of at most kFrom
-// and what an addition rounds off comes out of two more (of any value: five).
+// and what an addition rounds off comes out of two more (of any value: five).  settle() keeps what was rounded
+// off below a last place of the sum: left alone it would grow with a row's length, and be rounded ever more
+// coarsely (2^26 equal values: 2^-20 of the mass).
 struct Sum {
   static constexpr float kFrom = 1.0f / 64.0f;
   Pair2 x{both(kFrom), both(0.0f)};
@@ -180,6 +184,11 @@ struct Sum {
     const float2 s = add2(x.hi, v.hi), b = sub2(s, x.hi);
     const float2 e = kSmall ? sub2(v.hi, b) : add2(sub2(x.hi, sub2(s, b)), sub2(v.hi, b));
     x.lo = add2(add2(x.lo, v.lo), e);
+    x.hi = s;
+  }
+  __device__ __forceinline__ void settle() {
+    const float2 s = add2(x.hi, x.lo);
+    x.lo = sub2(x.lo, sub2(s, x.hi));
     x.hi = s;
   }
   __device__ __forceinline__ Pair total() const {
@@ -340,6 +349,7 @@ __device__ __forceinline__ Pair share_mass_of(const Share<kType, kDrawn>& s) {
       s.template add_to<kKind>(sum, v, t[0], q[0]);
       v += S::kTile;
     }
+    sum.settle();
   }
   return scan(sum.total());
 }

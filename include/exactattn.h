@@ -394,9 +394,10 @@ int attn_fwd_kv8_tree(int dtype, int B, int H, int H_kv, int n_q, int d, int cap
  *   accepted    int32 [B]: how many (0 for a sequence of no nodes)
  *   next_token  int32 [B]: the token that follows; -1 for a sequence of no nodes, and where the
  *               residual is 0 everywhere, which raises ATTN_WARN_EMPTY_ROW
- * n: 1 .. 1024; V: 1 .. 2^30; B at most 2^24.  Sums over V elements of mass 1 are off by about 2^-40
- * (at most V 2^-46), decisions beside them by no more; the result repeats bit for bit.  Outputs must
- * not overlap inputs or one another.  Errors as for attn_tree_mask.
+ * n: 1 .. 1024; V: 1 .. 2^30; B at most 2^24.  A sum over V elements of mass 1 is off by at most
+ * 2^-42 + V 2^-48 (usually by far less), a residual after k refusals by k times that, and decisions by no
+ * more; the result repeats bit for bit.  Outputs must not overlap inputs or one another.  Errors as for
+ * attn_tree_mask.
  */
 int attn_draft_verify(int dtype, int B, int n, int V, const void* target, const void* draft,
                       const int32_t* tokens, const int32_t* parents, const int32_t* counts,

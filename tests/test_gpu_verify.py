@@ -131,3 +131,21 @@ def test_many_refusals(V, exact):
     seen = check_verify(target, given, tokens, np.tile(np.r_[-1, np.zeros(n - 1, int)], (B, 1)),
                         rng.random((B, n)).astype(F32), [int(x) + 7 for x in k], exact)
     assert len(seen) > 1 and status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_mass_of_a_long_row(dtype):
+    """2^26 equal probabilities: what the additions round off all has one sign.  A sum is off by at most
+    2^-42 + 2^26 2^-48 of mass 1; the border of a child of the residual, of mass 0.7, by less than 2^-21 of itself."""
+    V = 1 << 26
+    target, given = (torch.zeros(1, 3, V, dtype=dtype, device="cuda") for _ in range(2))
+    target[0, 0] = 0.7 / V
+    target[0, 0, 5], given[0, 0, 5], target[0, 0, 7] = 0.2, 0.1875, 0.0
+    (a, p), q = (Fraction(x) for x in target[0, 0, 4:6].tolist()), Fraction(given[0, 0, 5].item())
+    border = float((p - q) / (q * ((V - 2) * a + p - q)))
+    for f in (1 - 2.0 ** -18, 1 - 2.0 ** -20, 1 - 2.0 ** -21, 1 + 2.0 ** -21, 1 + 2.0 ** -20, 1 + 2.0 ** -18):
+        u = F32(border * f)
+        got = ea.attn_draft_verify(target, given, i32([[0, 7, 5]]), i32([[-1, 0, 0]]),
+                                   torch.tensor([[0.5, 0.5, float(u)]], device="cuda"))
+        assert got[1].tolist() == [2 if float(u) < border else 1], f
+    status()
