@@ -18,7 +18,7 @@
 // for the token.
 //
 // The device has two 64-bit units a multiprocessor, and a dependent 64-bit step of a warp takes about a
-// hundred cycles: walk, sums and scans in 64 bits took 37 us where these take 23 (32 trees of 32 nodes over
+// hundred cycles: walk, sums and scans in 64 bits took 37 us where these take 24 (32 trees of 32 nodes over
 // 131072 values).  So sums are pairs of float32 values, by Knuth's and Dekker's error-free sums and products,
 // two elements an instruction, and a child's test is float32 unless its sides lie within 10^-6.  Of a row of
 // mass 1 the pairs' second values round off at most 2^-42 + V 2^-48: an element's two additions 2^-49 while its
